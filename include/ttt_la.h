@@ -360,6 +360,148 @@ TTT_LA_API ttt_la_status ttt_la_backward_recurrent(const ttt_la_grad_args *args,
 TTT_LA_API size_t ttt_la_backward_chunked_workspace_size(const ttt_la_grad_args *args);
 TTT_LA_API ttt_la_status ttt_la_backward_chunked(const ttt_la_grad_args *args, void *stream);
 
+/* The layer with a decay for each head: the fast weight forgets by a constant
+ * factor per token before it takes the token's gradient step,
+ *   W_t = gamma_h W_{t-1} + a v_t k_t^T ,  o_t = W_t q_t ,
+ *   gamma_h = exp(log_decay[h]) ,  a = sigma * eta_const
+ * (weight decay in the inner loop of Variant 5 in Table 2 of the
+ * thelatestinai.com listing; as linear attention, every pair of tokens s <= t
+ * is weighted by gamma^(t-s)).  A per-token learning rate is folded into v by
+ * the caller; there is no momentum.
+ *
+ * Layout.  N sequences.  q, k: [N,H,T,d_k], v, o: [N,H,T,d_v] in any memory
+ * order whose features are contiguous: x_stride[3] are the elements between
+ * sequences, heads and tokens, multiples of 16 bytes (not read for a
+ * dimension of size 1); rows of different (sequence, head, token) of an output
+ * must not overlap.  With cu_seqlens (device int32 [N+1], not decreasing) the
+ * sequences are packed: q, k, v, o have T rows in all, sequence n's are rows
+ * [cu_seqlens[n], cu_seqlens[n+1]), x_stride[0] is not read, and rows in no
+ * sequence are neither read into a result nor written.  Sequences may be
+ * empty: their state passes through.  Values of cu_seqlens outside [0, T] are
+ * clamped to it.  log_decay: device fp32 [H], <= 0 (-inf: gamma = 0); it is a
+ * constant, without a gradient.  state_in / state_out: fp32 [N,H,d_v,d_k],
+ * state_out may be state_in.
+ *
+ * dtype bf16: d_k and d_v multiples of 8 up to 256; fp32: multiples of 4 up to
+ * 256; others TTT_LA_ERR_UNSUPPORTED.  Sums and states are fp32.  A value that
+ * is not finite may reach every output of its own tile of 64 tokens, earlier
+ * ones included, and all later ones of its (sequence, head), never another
+ * sequence or head.
+ *
+ * segment_tokens: tokens of a sequence handled by one block, a multiple of 64;
+ * 0 = automatic (fills the SMs).  The workspace holds one state per segment
+ * where sequences have several (size query; pointers are not read, but whether
+ * cu_seqlens is NULL is). */
+typedef struct ttt_la_decay_args {
+  int32_t N, H, T, d_k, d_v;
+  int32_t dtype;            /* of q, k, v, o */
+  const void *q, *k, *v;
+  void *o;
+  int64_t q_stride[3], k_stride[3], v_stride[3], o_stride[3];
+  const float *log_decay;
+  const int32_t *cu_seqlens;
+  float eta_const;
+  int32_t ascent;
+  const float *state_in;    /* or NULL -> zeros */
+  float *state_out;         /* or NULL -> not returned */
+  int32_t segment_tokens;
+  void *workspace;
+  size_t workspace_bytes;
+} ttt_la_decay_args;
+
+TTT_LA_API size_t ttt_la_decay_workspace_size(const ttt_la_decay_args *args);
+TTT_LA_API ttt_la_status ttt_la_forward_decay(const ttt_la_decay_args *args, void *stream);
+
+/* Gradient of ttt_la_forward_decay for dL/do and (optional) dL/dW_T: with
+ * G_t = dL/dW_t = gamma G_{t+1} + do_t q_t^T,
+ *   dq_t = W_t^T do_t ,  dv_t = a G_t k_t ,  dk_t = a G_t^T v_t ,  dW_0 = gamma G_1 .
+ * Arguments as there; grad_o like o, grad_q, grad_k, grad_v like q, k, v (all
+ * required), grad_state and grad_state_in [N,H,d_v,d_k] fp32 (optional).
+ * Outputs must not overlap inputs or one another. */
+typedef struct ttt_la_decay_grad_args {
+  int32_t N, H, T, d_k, d_v;
+  int32_t dtype;
+  const void *q, *k, *v, *grad_o;
+  void *grad_q, *grad_k, *grad_v;
+  int64_t q_stride[3], k_stride[3], v_stride[3], grad_o_stride[3];
+  int64_t grad_q_stride[3], grad_k_stride[3], grad_v_stride[3];
+  const float *log_decay;
+  const int32_t *cu_seqlens;
+  float eta_const;
+  int32_t ascent;
+  const float *state_in, *grad_state;
+  float *grad_state_in;
+  int32_t segment_tokens;
+  void *workspace;
+  size_t workspace_bytes;
+} ttt_la_decay_grad_args;
+
+TTT_LA_API size_t ttt_la_backward_decay_workspace_size(const ttt_la_decay_grad_args *args);
+TTT_LA_API ttt_la_status ttt_la_backward_decay(const ttt_la_decay_grad_args *args, void *stream);
+
+/* The same layer for one new token of each of N sequences, the state updated
+ * IN PLACE: q, k [N,H,d_k], v, o [N,H,d_v] with contiguous features and
+ * x_stride[2] elements between sequences and heads (multiples of 16 bytes);
+ * state [N,H,d_v,d_k] fp32.  d_k in {32, 64, 128}, any d_v with
+ * N H d_v < 2^31; memory-bound. */
+typedef struct ttt_la_decay_decode_args {
+  int32_t N, H, d_k, d_v;
+  int32_t dtype;            /* of q, k, v, o */
+  const void *q, *k, *v;
+  void *o;
+  int64_t q_stride[2], k_stride[2], v_stride[2], o_stride[2];
+  const float *log_decay;
+  float eta_const;
+  int32_t ascent;
+  float *state;
+} ttt_la_decay_decode_args;
+
+TTT_LA_API ttt_la_status ttt_la_decode_step_decay(const ttt_la_decay_decode_args *args, void *stream);
+
+/* Group norm over channels-last data with its activation, for the layer's
+ * output (every head's output normalised by itself: L = 1, G = heads) and for
+ * positions x channels in general.  x, y, gate: [N,L,C] contiguous; G groups
+ * of C / G adjacent channels; over the L * C/G values of a (sample, group)
+ *   t = (x - mean) * rstd * weight + bias ,  rstd = 1 / sqrt(var + eps)
+ *   y = act(t), or with a gate  y = t * act(gate)
+ * activation: 0 none, 1 silu (silu(z) = z / (1 + exp(-z))).  weight, bias [C]
+ * of param_dtype, or NULL (1, 0).  mean, rstd: fp32 [N,G], written (the
+ * gradient reads them).  C a multiple of 16 bytes of x's type, G <= 4096, else
+ * TTT_LA_ERR_UNSUPPORTED; any width of a group.  y must not overlap x, gate,
+ * weight or bias. */
+typedef struct ttt_la_group_norm_args {
+  int32_t N, L, C, G;
+  int32_t dtype;            /* of x, gate, y */
+  int32_t param_dtype;      /* of weight and bias */
+  int32_t activation;
+  float eps;
+  const void *x, *gate, *weight, *bias;
+  void *y;
+  float *mean, *rstd;
+  void *workspace;
+  size_t workspace_bytes;
+} ttt_la_group_norm_args;
+
+TTT_LA_API size_t ttt_la_group_norm_workspace_size(const ttt_la_group_norm_args *args);
+TTT_LA_API ttt_la_status ttt_la_group_norm(const ttt_la_group_norm_args *args, void *stream);
+
+/* Its gradient for dL/dy, with the forward's x, gate, weight, bias, mean and
+ * rstd: grad_x (required), grad_gate (required with a gate), grad_weight and
+ * grad_bias of param_dtype (each optional).  Sums in fp32 in a fixed order.
+ * Outputs must not overlap inputs or one another. */
+typedef struct ttt_la_group_norm_grad_args {
+  int32_t N, L, C, G;
+  int32_t dtype, param_dtype, activation;
+  const void *grad_y, *x, *gate, *weight, *bias;
+  const float *mean, *rstd;
+  void *grad_x, *grad_gate, *grad_weight, *grad_bias;
+  void *workspace;
+  size_t workspace_bytes;
+} ttt_la_group_norm_grad_args;
+
+TTT_LA_API size_t ttt_la_group_norm_backward_workspace_size(const ttt_la_group_norm_grad_args *args);
+TTT_LA_API ttt_la_status ttt_la_group_norm_backward(const ttt_la_group_norm_grad_args *args, void *stream);
+
 /* Synchronises `stream`, returns the device status word (TTT_LA_OK,
  * TTT_LA_ERR_TIMEOUT, or in debug builds TTT_LA_ERR_DEVICE_CHECK, which wins
  * over a timeout) of the current device and clears it. */

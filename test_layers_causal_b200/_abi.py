@@ -76,6 +76,68 @@ class TttPlan(ctypes.Structure):
     ]
 
 
+_c_i64 = ctypes.c_int64
+
+
+class TttDecayArgs(ctypes.Structure):
+    """Mirror of ``ttt_la_decay_args``."""
+    _fields_ = [
+        ("N", _c_i32), ("H", _c_i32), ("T", _c_i32), ("d_k", _c_i32), ("d_v", _c_i32), ("dtype", _c_i32),
+        ("q", _c_vp), ("k", _c_vp), ("v", _c_vp), ("o", _c_vp),
+        ("q_stride", _c_i64 * 3), ("k_stride", _c_i64 * 3), ("v_stride", _c_i64 * 3), ("o_stride", _c_i64 * 3),
+        ("log_decay", _c_vp), ("cu_seqlens", _c_vp), ("eta_const", _c_f32), ("ascent", _c_i32),
+        ("state_in", _c_vp), ("state_out", _c_vp), ("segment_tokens", _c_i32),
+        ("workspace", _c_vp), ("workspace_bytes", _c_sz),
+    ]
+
+
+class TttDecayGradArgs(ctypes.Structure):
+    """Mirror of ``ttt_la_decay_grad_args``."""
+    _fields_ = [
+        ("N", _c_i32), ("H", _c_i32), ("T", _c_i32), ("d_k", _c_i32), ("d_v", _c_i32), ("dtype", _c_i32),
+        ("q", _c_vp), ("k", _c_vp), ("v", _c_vp), ("grad_o", _c_vp),
+        ("grad_q", _c_vp), ("grad_k", _c_vp), ("grad_v", _c_vp),
+        ("q_stride", _c_i64 * 3), ("k_stride", _c_i64 * 3), ("v_stride", _c_i64 * 3), ("grad_o_stride", _c_i64 * 3),
+        ("grad_q_stride", _c_i64 * 3), ("grad_k_stride", _c_i64 * 3), ("grad_v_stride", _c_i64 * 3),
+        ("log_decay", _c_vp), ("cu_seqlens", _c_vp), ("eta_const", _c_f32), ("ascent", _c_i32),
+        ("state_in", _c_vp), ("grad_state", _c_vp), ("grad_state_in", _c_vp), ("segment_tokens", _c_i32),
+        ("workspace", _c_vp), ("workspace_bytes", _c_sz),
+    ]
+
+
+class TttDecayDecodeArgs(ctypes.Structure):
+    """Mirror of ``ttt_la_decay_decode_args``."""
+    _fields_ = [
+        ("N", _c_i32), ("H", _c_i32), ("d_k", _c_i32), ("d_v", _c_i32), ("dtype", _c_i32),
+        ("q", _c_vp), ("k", _c_vp), ("v", _c_vp), ("o", _c_vp),
+        ("q_stride", _c_i64 * 2), ("k_stride", _c_i64 * 2), ("v_stride", _c_i64 * 2), ("o_stride", _c_i64 * 2),
+        ("log_decay", _c_vp), ("eta_const", _c_f32), ("ascent", _c_i32), ("state", _c_vp),
+    ]
+
+
+class TttGroupNormArgs(ctypes.Structure):
+    """Mirror of ``ttt_la_group_norm_args``."""
+    _fields_ = [
+        ("N", _c_i32), ("L", _c_i32), ("C", _c_i32), ("G", _c_i32),
+        ("dtype", _c_i32), ("param_dtype", _c_i32), ("activation", _c_i32), ("eps", _c_f32),
+        ("x", _c_vp), ("gate", _c_vp), ("weight", _c_vp), ("bias", _c_vp),
+        ("y", _c_vp), ("mean", _c_vp), ("rstd", _c_vp),
+        ("workspace", _c_vp), ("workspace_bytes", _c_sz),
+    ]
+
+
+class TttGroupNormGradArgs(ctypes.Structure):
+    """Mirror of ``ttt_la_group_norm_grad_args``."""
+    _fields_ = [
+        ("N", _c_i32), ("L", _c_i32), ("C", _c_i32), ("G", _c_i32),
+        ("dtype", _c_i32), ("param_dtype", _c_i32), ("activation", _c_i32),
+        ("grad_y", _c_vp), ("x", _c_vp), ("gate", _c_vp), ("weight", _c_vp), ("bias", _c_vp),
+        ("mean", _c_vp), ("rstd", _c_vp),
+        ("grad_x", _c_vp), ("grad_gate", _c_vp), ("grad_weight", _c_vp), ("grad_bias", _c_vp),
+        ("workspace", _c_vp), ("workspace_bytes", _c_sz),
+    ]
+
+
 # (name, restype, argtypes) for every symbol of include/ttt_la.h
 SIGNATURES = [
     ("ttt_la_workspace_size", _c_sz, [ctypes.POINTER(TttArgs)]),
@@ -93,6 +155,15 @@ SIGNATURES = [
     ("ttt_la_backward_recurrent", ctypes.c_int, [ctypes.POINTER(TttGradArgs), _c_vp]),
     ("ttt_la_backward_chunked_workspace_size", _c_sz, [ctypes.POINTER(TttGradArgs)]),
     ("ttt_la_backward_chunked", ctypes.c_int, [ctypes.POINTER(TttGradArgs), _c_vp]),
+    ("ttt_la_decay_workspace_size", _c_sz, [ctypes.POINTER(TttDecayArgs)]),
+    ("ttt_la_forward_decay", ctypes.c_int, [ctypes.POINTER(TttDecayArgs), _c_vp]),
+    ("ttt_la_backward_decay_workspace_size", _c_sz, [ctypes.POINTER(TttDecayGradArgs)]),
+    ("ttt_la_backward_decay", ctypes.c_int, [ctypes.POINTER(TttDecayGradArgs), _c_vp]),
+    ("ttt_la_decode_step_decay", ctypes.c_int, [ctypes.POINTER(TttDecayDecodeArgs), _c_vp]),
+    ("ttt_la_group_norm_workspace_size", _c_sz, [ctypes.POINTER(TttGroupNormArgs)]),
+    ("ttt_la_group_norm", ctypes.c_int, [ctypes.POINTER(TttGroupNormArgs), _c_vp]),
+    ("ttt_la_group_norm_backward_workspace_size", _c_sz, [ctypes.POINTER(TttGroupNormGradArgs)]),
+    ("ttt_la_group_norm_backward", ctypes.c_int, [ctypes.POINTER(TttGroupNormGradArgs), _c_vp]),
     ("ttt_la_get_last_device_status", ctypes.c_int, [_c_vp]),
     ("ttt_la_debug_check_line", _c_i32, [_c_vp]),
     ("ttt_la_set_wait_limit_ns", ctypes.c_int, [ctypes.c_int64]),

@@ -1,0 +1,290 @@
+// decay_host.cuh -- C ABI of the decayed layer (ttt_la_forward_decay,
+// ttt_la_backward_decay, ttt_la_decode_step_decay): checks, plan, launches.
+// Included by ttt_la.cu, whose host helpers it uses.
+#pragma once
+
+namespace {
+
+// Tokens per segment.  `rows` tokens of `heads` independent (sequence, head)
+// runs are cut so that the launch fills the device's `slots` blocks: a wave
+// takes as long as its longest segment, and cutting at all costs a pass over
+// k and v for the segments' contributions (about half of the output pass, as
+// it moves half the bytes) and a scan (about the time of kDecayScanTiles
+// tiles).  Packed sequences are planned as one of their total length, since
+// the host does not see where they end.
+constexpr int kDecayTile = 64;
+constexpr double kDecayTotalCost = 0.5, kDecayScanTiles = 6.0;
+int decay_plan_tokens(long long heads, int rows, int slots) {
+  const int tiles = (rows + kDecayTile - 1) / kDecayTile;
+  int best = tiles;
+  double cost = 1e30;
+  for (int ns = 1; ns <= tiles && ns <= 1024; ++ns) {
+    const int per = (tiles + ns - 1) / ns;
+    const long long n = (tiles + per - 1) / per;
+    auto waves = [&](long long blocks) { return static_cast<double>((blocks + slots - 1) / slots); };
+    double c = waves(heads * n) * per;
+    if (n > 1) c += waves(heads * (n - 1)) * per * kDecayTotalCost + kDecayScanTiles;
+    if (c < cost) {
+      cost = c;
+      best = per;
+    }
+    if (heads * n > 4ll * slots) break;
+  }
+  return static_cast<int>(std::min<long long>(static_cast<long long>(best) * kDecayTile, 1 << 30));
+}
+
+struct DecayLayout {
+  ttt::DecayGeom g;
+  size_t run_floats;  // workspace of one run (0: one segment per sequence)
+};
+
+bool decay_fits(int d, int dtype) { return d >= 4 && d <= 256 && d % (dtype == TTT_LA_F32 ? 4 : 8) == 0; }
+
+DecayLayout decay_layout(const int32_t* cu, int N, int H, int T, int dk, int dv, int segment_tokens, long long blocks,
+                         int slots) {
+  DecayLayout l;
+  l.g.N = N;
+  l.g.H = H;
+  l.g.T = T;
+  l.g.cu = cu;
+  l.g.S = segment_tokens > 0 ? segment_tokens
+                             : decay_plan_tokens(blocks * H * (cu ? 1 : N), std::max(1, T), slots);
+  const bool multi = l.g.S < T;
+  const long long nseg = cu ? (multi ? T / l.g.S : 0) + static_cast<long long>(N)
+                            : static_cast<long long>(N) * (T > 0 ? (T - 1) / l.g.S + 1 : 1);
+  l.g.nseg = nseg < (1ll << 31) ? static_cast<int>(nseg) : -1;
+  l.run_floats = multi ? static_cast<size_t>(nseg) * H * dk * dv : 0;
+  return l;
+}
+
+ttt::DecayTensor decay_tensor(const void* p, const int64_t* stride) {
+  return ttt::DecayTensor{p, stride[0], stride[1], stride[2]};
+}
+
+template <typename T>
+ttt_la_status decay_simt_run(const ttt::DecayGeom& g, const ttt::DecayRun& r, const float* log_decay, bool totals,
+                             cudaStream_t st) {
+  const long long blocks = static_cast<long long>(g.nseg) * g.H * ((r.dv + ttt::kDecayVT - 1) / ttt::kDecayVT);
+  if (blocks >= (1ll << 31)) return TTT_LA_ERR_UNSUPPORTED;
+  const int smem = ttt::decay_simt_smem(r.dk);
+  auto kern = totals ? ttt::decay_simt_kernel<T, true> : ttt::decay_simt_kernel<T, false>;
+  if (!grant_smem(reinterpret_cast<const void*>(kern), smem)) return TTT_LA_ERR_CUDA;
+  return launch_kernel(kern, static_cast<int>(blocks), 256, smem, st, false, g, r, log_decay);
+}
+
+ttt_la_status decay_scan(const ttt::DecayGeom& g, const ttt::DecayRun& r, const float* log_decay, cudaStream_t st) {
+  const long long dd = static_cast<long long>(r.dk) * r.dv, slices = (dd / 4 + 255) / 256;
+  const long long blocks = slices * g.N * g.H;
+  if (blocks >= (1ll << 31)) return TTT_LA_ERR_UNSUPPORTED;
+  return launch_kernel(ttt::decay_scan_kernel, static_cast<int>(blocks), 256, 0, st, false, g, r, log_decay);
+}
+
+// `n` runs of the recurrence over the same tokens.
+ttt_la_status decay_runs(const ttt::DecayGeom& g, const ttt::DecayRun* r, int n, int dtype, const float* log_decay,
+                         cudaStream_t st) {
+  for (int i = 0; i < n; ++i) {
+    ttt_la_status s = TTT_LA_OK;
+    for (int pass = r[i].ws ? 0 : 2; pass < 3 && s == TTT_LA_OK; ++pass) {
+      if (pass == 1)
+        s = decay_scan(g, r[i], log_decay, st);
+      else
+        s = dtype == TTT_LA_F32 ? decay_simt_run<float>(g, r[i], log_decay, pass == 0, st)
+                                : decay_simt_run<__nv_bfloat16>(g, r[i], log_decay, pass == 0, st);
+    }
+    if (s != TTT_LA_OK) return s;
+  }
+  return TTT_LA_OK;
+}
+
+// Sizes and strides that the forward and the backward share.
+bool decay_strides_ok(const int64_t* s, int N, int H, int T, bool packed, int dtype) {
+  const int unit = dtype == TTT_LA_F32 ? 4 : 8;
+  const long long size[3] = {packed ? 1 : N, H, T};
+  for (int i = 0; i < 3; ++i)
+    if (size[i] > 1 && (s[i] < unit || s[i] % unit || s[i] > (1ll << 36))) return false;
+  return true;
+}
+
+ttt_la_status check_decay_shape(int N, int H, int T, int dk, int dv, int dtype, const int32_t* cu, const float* log_decay,
+                                int segment_tokens) {
+  if (N < 1 || H < 1 || T < 0 || dk < 1 || dv < 1 || (T == 0 && !cu)) return TTT_LA_ERR_INVALID_ARG;
+  if (dtype != TTT_LA_F32 && dtype != TTT_LA_BF16) return TTT_LA_ERR_INVALID_ARG;
+  if (!log_decay || (reinterpret_cast<uintptr_t>(log_decay) & 3) || (reinterpret_cast<uintptr_t>(cu) & 3))
+    return TTT_LA_ERR_INVALID_ARG;
+  if (segment_tokens < 0 || segment_tokens % kDecayTile) return TTT_LA_ERR_INVALID_ARG;
+  if (static_cast<long long>(N) * H > (1ll << 24) || T > (1 << 30)) return TTT_LA_ERR_INVALID_ARG;
+  if (!decay_fits(dk, dtype) || !decay_fits(dv, dtype)) return TTT_LA_ERR_UNSUPPORTED;
+  return TTT_LA_OK;
+}
+
+// The layer in its forward direction, as one run.
+ttt::DecayRun decay_forward_run(const ttt_la_decay_args* a) {
+  ttt::DecayRun r = {};
+  r.q = decay_tensor(a->q, a->q_stride);
+  r.k = decay_tensor(a->k, a->k_stride);
+  r.v = decay_tensor(a->v, a->v_stride);
+  r.o = decay_tensor(a->o, a->o_stride);
+  r.dk = a->d_k;
+  r.dv = a->d_v;
+  r.sP = r.sU = a->ascent ? -a->eta_const : a->eta_const;
+  r.sR = 1.f;
+  r.s_in = a->state_in;
+  r.s_out = a->state_out;
+  return r;
+}
+
+DecayLayout decay_forward_layout(const ttt_la_decay_args* a) {
+  return decay_layout(a->cu_seqlens, a->N, a->H, a->T, a->d_k, a->d_v, a->segment_tokens,
+                      (a->d_v + ttt::kDecayVT - 1) / ttt::kDecayVT, sm_count() * 2);
+}
+DecayLayout decay_backward_layout(const ttt_la_decay_grad_args* a) {
+  return decay_layout(a->cu_seqlens, a->N, a->H, a->T, a->d_k, a->d_v, a->segment_tokens,
+                      (std::max(a->d_k, a->d_v) + ttt::kDecayVT - 1) / ttt::kDecayVT, sm_count() * 2);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t ttt_la_decay_workspace_size(const ttt_la_decay_args* a) {
+  if (!a || check_decay_shape(a->N, a->H, a->T, a->d_k, a->d_v, a->dtype, a->cu_seqlens, a->log_decay,
+                              a->segment_tokens) != TTT_LA_OK)
+    return 0;
+  return decay_forward_layout(a).run_floats * sizeof(float);
+}
+
+ttt_la_status ttt_la_forward_decay(const ttt_la_decay_args* a, void* stream) {
+  NvtxRange range("ttt_la_forward_decay");
+  if (!a) return TTT_LA_ERR_INVALID_ARG;
+  const ttt_la_status s = check_decay_shape(a->N, a->H, a->T, a->d_k, a->d_v, a->dtype, a->cu_seqlens, a->log_decay,
+                                            a->segment_tokens);
+  if (s != TTT_LA_OK) return s;
+  const bool packed = a->cu_seqlens != nullptr;
+  const void* t[4] = {a->q, a->k, a->v, a->o};
+  const int64_t* stride[4] = {a->q_stride, a->k_stride, a->v_stride, a->o_stride};
+  for (int i = 0; i < 4; ++i)
+    if ((a->T > 0 && !t[i]) || !aligned16(t[i]) || !decay_strides_ok(stride[i], a->N, a->H, a->T, packed, a->dtype))
+      return TTT_LA_ERR_INVALID_ARG;
+  if (!aligned16(a->state_in) || !aligned16(a->state_out)) return TTT_LA_ERR_INVALID_ARG;
+  if (a->T > 0 && (a->o == a->q || a->o == a->k || a->o == a->v)) return TTT_LA_ERR_INVALID_ARG;
+  const DecayLayout l = decay_forward_layout(a);
+  if (l.g.nseg < 0) return TTT_LA_ERR_UNSUPPORTED;
+  const size_t need = l.run_floats * sizeof(float);
+  if (need && (!a->workspace || !aligned16(a->workspace) || a->workspace_bytes < need)) return TTT_LA_ERR_INVALID_ARG;
+  ttt::DecayRun r = decay_forward_run(a);
+  r.ws = need ? static_cast<float*>(a->workspace) : nullptr;
+  return decay_runs(l.g, &r, 1, a->dtype, a->log_decay, static_cast<cudaStream_t>(stream));
+}
+
+size_t ttt_la_backward_decay_workspace_size(const ttt_la_decay_grad_args* a) {
+  if (!a || check_decay_shape(a->N, a->H, a->T, a->d_k, a->d_v, a->dtype, a->cu_seqlens, a->log_decay,
+                              a->segment_tokens) != TTT_LA_OK)
+    return 0;
+  return 3 * decay_backward_layout(a).run_floats * sizeof(float);
+}
+
+ttt_la_status ttt_la_backward_decay(const ttt_la_decay_grad_args* a, void* stream) {
+  NvtxRange range("ttt_la_backward_decay");
+  if (!a) return TTT_LA_ERR_INVALID_ARG;
+  const ttt_la_status s = check_decay_shape(a->N, a->H, a->T, a->d_k, a->d_v, a->dtype, a->cu_seqlens, a->log_decay,
+                                            a->segment_tokens);
+  if (s != TTT_LA_OK) return s;
+  const bool packed = a->cu_seqlens != nullptr;
+  const void* t[7] = {a->q, a->k, a->v, a->grad_o, a->grad_q, a->grad_k, a->grad_v};
+  const int64_t* stride[7] = {a->q_stride,      a->k_stride,      a->v_stride,     a->grad_o_stride,
+                              a->grad_q_stride, a->grad_k_stride, a->grad_v_stride};
+  for (int i = 0; i < 7; ++i) {
+    if ((a->T > 0 && !t[i]) || !aligned16(t[i]) || !decay_strides_ok(stride[i], a->N, a->H, a->T, packed, a->dtype))
+      return TTT_LA_ERR_INVALID_ARG;
+    for (int j = std::max(4, i + 1); j < 7; ++j)  // an output is neither an input nor another output
+      if (a->T > 0 && t[i] == t[j]) return TTT_LA_ERR_INVALID_ARG;
+  }
+  if (!aligned16(a->state_in) || !aligned16(a->grad_state) || !aligned16(a->grad_state_in))
+    return TTT_LA_ERR_INVALID_ARG;
+  if (a->grad_state_in && (a->grad_state_in == a->grad_state || a->grad_state_in == a->state_in))
+    return TTT_LA_ERR_INVALID_ARG;
+  const DecayLayout l = decay_backward_layout(a);
+  if (l.g.nseg < 0) return TTT_LA_ERR_UNSUPPORTED;
+  const size_t need = 3 * l.run_floats * sizeof(float);
+  if (need && (!a->workspace || !aligned16(a->workspace) || a->workspace_bytes < need)) return TTT_LA_ERR_INVALID_ARG;
+  const ttt::DecayTensor q = decay_tensor(a->q, a->q_stride), k = decay_tensor(a->k, a->k_stride),
+                         v = decay_tensor(a->v, a->v_stride), dO = decay_tensor(a->grad_o, a->grad_o_stride);
+  const float c = a->ascent ? -a->eta_const : a->eta_const;
+  ttt::DecayRun r[3] = {};
+  // dq: W^T read with do
+  r[0].q = dO, r[0].k = v, r[0].v = k, r[0].o = decay_tensor(a->grad_q, a->grad_q_stride);
+  r[0].dk = a->d_v, r[0].dv = a->d_k;
+  r[0].sP = r[0].sU = c, r[0].sR = 1.f;
+  r[0].s_in = a->state_in, r[0].s_in_t = 1;
+  // dk: (dL/dW)^T read with v, last token to first
+  r[1].q = v, r[1].k = dO, r[1].v = q, r[1].o = decay_tensor(a->grad_k, a->grad_k_stride);
+  r[1].dk = a->d_v, r[1].dv = a->d_k;
+  r[1].rev = 1, r[1].sP = r[1].sR = c, r[1].sU = 1.f;
+  r[1].s_in = a->grad_state, r[1].s_in_t = 1;
+  // dv: dL/dW read with k; where it ends is dL/dW_0
+  r[2].q = k, r[2].k = q, r[2].v = dO, r[2].o = decay_tensor(a->grad_v, a->grad_v_stride);
+  r[2].dk = a->d_k, r[2].dv = a->d_v;
+  r[2].rev = 1, r[2].sP = r[2].sR = c, r[2].sU = 1.f;
+  r[2].s_in = a->grad_state, r[2].s_out = a->grad_state_in;
+  for (int i = 0; i < 3 && need; ++i) r[i].ws = static_cast<float*>(a->workspace) + i * l.run_floats;
+  return decay_runs(l.g, r, 3, a->dtype, a->log_decay, static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"
+
+namespace {
+template <int DK, typename T>
+ttt_la_status launch_decay_step(const ttt::DecayStep& p, cudaStream_t st) {
+  constexpr int RPW = 32 / (DK / 4);
+  const long long rows = static_cast<long long>(p.N) * p.H * p.dv;
+  const long long slots = static_cast<long long>(sm_count()) * 8;  // blocks of 256 threads
+  constexpr int U = 4;
+  if (rows <= slots * 8 * RPW * U) {
+    // less than one wave of the deep kernel: one row group a warp, small blocks over all SMs
+    const long long warps = (rows + RPW - 1) / RPW;
+    ttt::decay_step_kernel<DK, T, 1><<<static_cast<int>((warps + 3) / 4), 128, 0, st>>>(p);
+  } else {
+    ttt::decay_step_kernel<DK, T, U><<<static_cast<int>(slots), 256, 0, st>>>(p);
+  }
+  return launched();
+}
+template <typename T>
+ttt_la_status decay_step_dk(const ttt::DecayStep& p, cudaStream_t st) {
+  switch (p.dk) {
+    case 32: return launch_decay_step<32, T>(p, st);
+    case 64: return launch_decay_step<64, T>(p, st);
+    case 128: return launch_decay_step<128, T>(p, st);
+    default: return TTT_LA_ERR_UNSUPPORTED;
+  }
+}
+}  // namespace
+
+extern "C" ttt_la_status ttt_la_decode_step_decay(const ttt_la_decay_decode_args* a, void* stream) {
+  NvtxRange range("ttt_la_decode_step_decay");
+  if (!a || a->N < 1 || a->H < 1 || a->d_k < 1 || a->d_v < 1) return TTT_LA_ERR_INVALID_ARG;
+  if (a->dtype != TTT_LA_F32 && a->dtype != TTT_LA_BF16) return TTT_LA_ERR_INVALID_ARG;
+  if (!a->log_decay || (reinterpret_cast<uintptr_t>(a->log_decay) & 3) || !a->state || !aligned16(a->state))
+    return TTT_LA_ERR_INVALID_ARG;
+  if (static_cast<long long>(a->N) * a->H * a->d_v >= (1ll << 31)) return TTT_LA_ERR_INVALID_ARG;
+  const void* t[4] = {a->q, a->k, a->v, a->o};
+  const int64_t* stride[4] = {a->q_stride, a->k_stride, a->v_stride, a->o_stride};
+  const int unit = a->dtype == TTT_LA_F32 ? 4 : 8;
+  ttt::DecayTensor x[4];
+  for (int i = 0; i < 4; ++i) {
+    if (!t[i] || !aligned16(t[i])) return TTT_LA_ERR_INVALID_ARG;
+    const long long size[2] = {a->N, a->H};
+    for (int j = 0; j < 2; ++j)
+      if (size[j] > 1 && (stride[i][j] < unit || stride[i][j] % unit || stride[i][j] > (1ll << 36)))
+        return TTT_LA_ERR_INVALID_ARG;
+    x[i] = ttt::DecayTensor{t[i], stride[i][0], stride[i][1], 0};
+  }
+  if (a->o == a->q || a->o == a->k || a->o == a->v) return TTT_LA_ERR_INVALID_ARG;
+  ttt::DecayStep p = {};
+  p.N = a->N, p.H = a->H, p.dk = a->d_k, p.dv = a->d_v;
+  p.q = x[0], p.k = x[1], p.v = x[2], p.o = x[3];
+  p.log_decay = a->log_decay;
+  p.a = a->ascent ? -a->eta_const : a->eta_const;
+  p.S = a->state;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return a->dtype == TTT_LA_F32 ? decay_step_dk<float>(p, st) : decay_step_dk<__nv_bfloat16>(p, st);
+}

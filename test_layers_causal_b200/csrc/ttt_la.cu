@@ -12,6 +12,7 @@
 #include <cstdint>
 #include <cstring>
 #include <mutex>
+#include <type_traits>
 #include <utility>
 #include <vector>
 
@@ -25,8 +26,10 @@
 #include "chunked_tc.cuh"
 #include "chunked_tc_mom.cuh"
 #include "common.cuh"
+#include "decay.cuh"
 #include "decode.cuh"
 #include "feature_map.cuh"
+#include "group_norm.cuh"
 #include "recurrent.cuh"
 #include "seqshard.cuh"
 
@@ -1551,3 +1554,5 @@ ttt_la_status ttt_la_backward_chunked(const ttt_la_grad_args* a, void* stream) {
 
 }  // extern "C"
 
+#include "decay_host.cuh"
+#include "group_norm_host.cuh"

@@ -1,0 +1,364 @@
+"""GPU parity of the layer with a decay for each head (forward_decay,
+backward_decay, decode_step_decay, forward_decay_norm) against the float64
+oracle on the exact inputs given to the GPU.
+
+Bounds, elementwise.  Every output is a sum of products x = sum s_i; let A be
+the same sum of absolute values, which the oracle gives for absolute inputs.
+u = 2^-8 is half a bf16 step relative to the value, e = 2^-24 half an fp32 step.
+  fp32 inputs: sums of at most T + d terms in any order, each power of gamma
+    off by less than 2 (T / 32 + 4) steps (at most T / 32 + 1 products of
+    powers, each power within 2 steps and its exponent within one, x exp(-x) < 1):
+    |err| <= (T + d + T / 8 + 32) e A for outputs and states.
+  bf16 inputs: the same in fp32, and on the tensor cores the weighted scores,
+    the update's weighted operand and the state read for an output are each
+    rounded to bf16 once, at most two of them in one product chain, and the
+    result once: |err| <= u |x| + 2.1 u A.  States take no rounding below
+    2^-16 (a bf16 pair), and the tensor cores add in at least 22 bits:
+    |err| <= (2^-16 + 2^-22 (T / 16 + 16)) A.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from tests.gpu_util import f64
+
+pytestmark = pytest.mark.gpu
+
+if torch.cuda.is_available():
+    import test_layers_causal_b200 as ttt
+
+U, E = 2.0 ** -8, 2.0 ** -24
+
+
+@pytest.fixture(autouse=True)
+def _no_timed_out_wait():
+    yield
+    assert ttt.device_status() == 0
+
+
+def _log_decay(H):
+    """From one that keeps everything to one that forgets at once."""
+    half = np.linspace(0.0, 1.0, max(H, 2))[:H]
+    ld = -np.exp2(2.0 - 12.0 * half)
+    if H > 1:
+        ld[-1] = 0.0
+    if H > 2:
+        ld[0] = -np.inf
+    return torch.tensor(ld, dtype=torch.float32)
+
+
+def _make(lens, H, dk, dv, dtype, packed, order, states, seed, extra=(0, 0)):
+    """extra: rows before the first and behind the last packed sequence."""
+    g = torch.Generator().manual_seed(seed)
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    B, T = (1, sum(lens) + sum(extra)) if packed else (len(lens), lens[0])
+
+    def rows(d, unit):
+        x = torch.randn(B, T, H, d, generator=g)
+        if unit:
+            x = x / x.norm(dim=-1, keepdim=True)
+        if extra[0] and packed:
+            x[:, :extra[0]] = float("nan")
+        if extra[1] and packed:
+            x[:, T - extra[1]:] = float("nan")
+        x = x.to(dt).cuda().transpose(1, 2)
+        return x if order == "tokens" else x.contiguous()
+
+    c = dict(q=rows(dk, True), k=rows(dk, True), v=rows(dv, False), dO=rows(dv, False), ld=_log_decay(H).cuda(),
+             W0=None, dW=None, cu=None, lens=lens, packed=packed, first=extra[0])
+    if states:
+        c["W0"] = (0.3 * torch.randn(len(lens), H, dv, dk, generator=g)).cuda()
+        c["dW"] = torch.randn(len(lens), H, dv, dk, generator=g).cuda()
+    if packed:
+        c["cu"] = torch.tensor(np.concatenate([[0], np.cumsum(lens)]) + extra[0], dtype=torch.int32).cuda()
+    return c
+
+
+def _of_seq(x, c, n):
+    """[H, len, d] of sequence n."""
+    if not c["packed"]:
+        return x[n]
+    a = c["first"] + sum(c["lens"][:n])
+    return x[0, :, a:a + c["lens"][n]]
+
+
+def _check(x, ref, A, what, dtype, T, d, state=False):
+    x = f64(x)
+    assert np.isfinite(x).all(), what
+    if dtype == "f32":
+        tol = (T + d + T / 8 + 32) * E * A
+    elif state:
+        tol = (2.0 ** -16 + 2.0 ** -22 * (T / 16 + 16)) * A
+    else:
+        tol = U * np.abs(ref) + 2.1 * U * A
+    bad = np.abs(x - ref) - tol
+    assert (bad <= 1e-30).all(), f"{what}: {np.abs(x - ref).max():.3e} off, {bad.max():.3e} past the bound"
+
+
+def _abs(*xs):
+    return [None if x is None else np.abs(x) for x in xs]
+
+
+def _check_forward(c, o, W, dtype, a):
+    H, dk, dv = c["q"].shape[1], c["q"].shape[-1], c["v"].shape[-1]
+    ld = f64(c["ld"])
+    for n, T in enumerate(c["lens"]):
+        q, k, v = (f64(_of_seq(c[x], c, n)) for x in ("q", "k", "v"))
+        W0 = None if c["W0"] is None else f64(c["W0"][n])
+        ro, rW = oracle.decay_forward_f64(q, k, v, ld, a, W0)
+        Ao, AW = oracle.decay_forward_f64(*_abs(q, k, v), ld, abs(a), None if W0 is None else np.abs(W0))
+        _check(_of_seq(o, c, n), ro, Ao, f"o of sequence {n}", dtype, T, dk)
+        if W is not None:
+            _check(W[n], rW, AW, f"W_T of sequence {n}", dtype, T, dk, True)
+
+
+def _check_backward(c, g, dtype, a):
+    dk = c["q"].shape[-1]
+    ld = f64(c["ld"])
+    for n, T in enumerate(c["lens"]):
+        x = [f64(_of_seq(c[y], c, n)) for y in ("q", "k", "v", "dO")]
+        s = [None if c[y] is None else f64(c[y][n]) for y in ("W0", "dW")]
+        ref = oracle.decay_backward_f64(*x, ld, a, *s)
+        A = oracle.decay_backward_f64(*_abs(*x), ld, abs(a), *_abs(*s))
+        for name in ("dq", "dk", "dv"):
+            _check(_of_seq(g[name], c, n), ref[name], A[name], f"{name} of sequence {n}", dtype, T, dk)
+        _check(g["dW0"][n], ref["dW0"], A["dW0"], f"dW0 of sequence {n}", dtype, T, dk, True)
+
+
+CASES = [
+    # lens, H, dk, dv, dtype, packed, order, states, segment_tokens
+    ([1], 1, 64, 64, "bf16", False, "heads", False, 0),
+    ([1], 3, 128, 128, "bf16", False, "tokens", True, 0),
+    ([64, 64], 2, 64, 64, "bf16", False, "tokens", True, 0),
+    ([129], 4, 64, 64, "bf16", False, "heads", True, 0),
+    ([128], 2, 128, 64, "bf16", False, "tokens", False, 0),
+    ([300, 300], 3, 128, 128, "bf16", False, "tokens", True, 0),
+    ([513], 2, 128, 128, "bf16", False, "heads", True, 128),
+    ([700], 3, 64, 128, "bf16", False, "tokens", True, 256),
+    ([450], 2, 64, 64, "bf16", False, "heads", False, 64),
+    ([390], 2, 128, 64, "bf16", False, "heads", True, 192),
+    ([130, 0, 1, 65, 511, 127], 3, 128, 128, "bf16", True, "tokens", True, 0),
+    ([130, 0, 1, 65, 511, 127], 3, 64, 64, "bf16", True, "tokens", True, 128),
+    ([3, 400, 0, 77], 2, 64, 128, "bf16", True, "heads", False, 64),
+    ([0, 256, 256], 2, 128, 64, "bf16", True, "tokens", True, 128),
+    ([200], 2, 96, 80, "bf16", False, "tokens", True, 64),   # widths between the tiles'
+    ([150, 60], 2, 8, 24, "bf16", True, "tokens", True, 64),
+    ([140], 2, 256, 136, "bf16", False, "heads", True, 64),  # wider than the tiles
+    ([1], 2, 32, 32, "f32", False, "heads", True, 0),
+    ([95, 95], 2, 64, 64, "f32", False, "tokens", True, 64),
+    ([257], 2, 32, 128, "f32", False, "heads", False, 0),
+    ([33, 0, 200, 1], 3, 64, 32, "f32", True, "tokens", True, 64),
+    ([70], 1, 4, 12, "f32", True, "heads", True, 64),
+    ([100], 2, 256, 252, "f32", False, "heads", True, 0),
+]
+
+
+@pytest.mark.parametrize("case", CASES, ids=lambda c: "-".join(str(x).replace(" ", "") for x in c))
+@pytest.mark.parametrize("ascent", [False, True])
+def test_forward_matches_oracle(case, ascent):
+    lens, H, dk, dv, dtype, packed, order, states, seg = case
+    c = _make(lens, H, dk, dv, dtype, packed, order, states, seed=len(lens) + dk + 3 * dv)
+    o, W = ttt.forward_decay(c["q"], c["k"], c["v"], c["ld"], ascent=ascent, cu_seqlens=c["cu"], state_in=c["W0"],
+                             segment_tokens=seg)
+    assert o.stride() == c["v"].stride()
+    a = np.float64(np.float32(1.0 / math.sqrt(dk)))
+    _check_forward(c, o, W, dtype, -a if ascent else a)
+    # the output alone, and the state in place, give the same bits
+    o2, none = ttt.forward_decay(c["q"], c["k"], c["v"], c["ld"], ascent=ascent, cu_seqlens=c["cu"], state_in=c["W0"],
+                                 segment_tokens=seg, return_state=False)
+    assert none is None and torch.equal(o, o2)
+    if states:
+        S = c["W0"].clone()
+        o3, W3 = ttt.forward_decay(c["q"], c["k"], c["v"], c["ld"], ascent=ascent, cu_seqlens=c["cu"], state_in=S,
+                                   state_out=S, segment_tokens=seg)
+        assert W3 is S and torch.equal(W3, W) and torch.equal(o3, o)
+
+
+@pytest.mark.parametrize("case", CASES, ids=lambda c: "-".join(str(x).replace(" ", "") for x in c))
+def test_backward_matches_oracle(case):
+    lens, H, dk, dv, dtype, packed, order, states, seg = case
+    c = _make(lens, H, dk, dv, dtype, packed, order, states, seed=50 + len(lens) + dk + 3 * dv)
+    g = ttt.backward_decay(c["q"], c["k"], c["v"], c["dO"], c["ld"], eta_const=0.2, cu_seqlens=c["cu"],
+                           state_in=c["W0"], grad_state=c["dW"], segment_tokens=seg)
+    assert g["dq"].stride() == c["q"].stride() and g["dv"].stride() == c["v"].stride()
+    _check_backward(c, g, dtype, np.float64(np.float32(0.2)))
+
+
+def test_gradient_agrees_with_differences():
+    """<gradient, direction> against the fp32 layer's own central difference;
+    the loss is a sum over o and W_T, linear in each input alone, so the
+    difference's only error is the fp32 rounding of the two losses."""
+    c = _make([70], 2, 32, 32, "f32", False, "heads", True, seed=7)
+    g = ttt.backward_decay(c["q"], c["k"], c["v"], c["dO"], c["ld"], state_in=c["W0"], grad_state=c["dW"])
+
+    def loss(**kw):
+        x = {n: kw.get(n, c[n]) for n in ("q", "k", "v", "W0")}
+        o, W = ttt.forward_decay(x["q"], x["k"], x["v"], c["ld"], state_in=x["W0"])
+        return float((o.double() * c["dO"].double()).sum() + (W.double() * c["dW"].double()).sum())
+
+    for n, gn in (("q", "dq"), ("k", "dk"), ("v", "dv"), ("W0", "dW0")):
+        d = torch.randn(c[n].shape, generator=torch.Generator().manual_seed(3)).cuda()
+        num = (loss(**{n: c[n] + d}) - loss(**{n: c[n] - d})) / 2
+        ref = float((g[gn].double() * d.double()).sum())
+        # 4500 outputs of magnitude up to 10, each off by at most 150 steps of 2^-24
+        assert abs(num - ref) <= 4500 * 10 * 150 * E, n
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("seg", [0, 64])
+def test_rows_in_no_sequence(dtype, seg):
+    """Rows before the first and behind the last sequence hold NaN and are
+    neither read into a result nor written."""
+    c = _make([70, 0, 200], 2, 64, 64, dtype, True, "tokens", True, seed=9, extra=(5, 37))
+    out = torch.full_like(c["v"], 7.0)
+    o, W = ttt.forward_decay(c["q"], c["k"], c["v"], c["ld"], cu_seqlens=c["cu"], state_in=c["W0"], out=out,
+                             segment_tokens=seg)
+    a = np.float64(np.float32(1.0 / math.sqrt(64)))
+    _check_forward(c, o, W, dtype, a)
+    T = o.shape[2]
+    assert (o[:, :, :5] == 7).all() and (o[:, :, T - 37:] == 7).all()
+    g = ttt.backward_decay(c["q"], c["k"], c["v"], c["dO"], c["ld"], cu_seqlens=c["cu"], state_in=c["W0"],
+                           grad_state=c["dW"], segment_tokens=seg)
+    _check_backward(c, g, dtype, a)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_not_finite_stays_in_its_sequence_and_head(d):
+    """Infinities and NaN in one (sequence, head), at its last row, reach no
+    other, whose rows lie in the same tiles of memory."""
+    c = _make([100, 90, 300], 2, d, d, "bf16", True, "tokens", True, seed=12)
+    clean, Wc = ttt.forward_decay(c["q"], c["k"], c["v"], c["ld"], cu_seqlens=c["cu"], state_in=c["W0"])
+    v, k = c["v"].clone(memory_format=torch.preserve_format), c["k"].clone(memory_format=torch.preserve_format)
+    v[0, 1, 189] = float("inf")
+    v[0, 1, 100] = float("nan")
+    k[0, 1, 150] = float("nan")
+    o, W = ttt.forward_decay(c["q"], k, v, c["ld"], cu_seqlens=c["cu"], state_in=c["W0"])
+    keep = torch.ones(o.shape[1:3], dtype=torch.bool, device="cuda")
+    keep[1, 100:190] = False
+    assert torch.equal(o[0][keep], clean[0][keep])
+    ok = torch.ones(3, 2, dtype=torch.bool, device="cuda")
+    ok[1, 1] = False
+    assert torch.equal(W[ok], Wc[ok]) and not torch.isfinite(W[1, 1]).all()
+
+
+@pytest.mark.parametrize("dtype,dk,dv", [("bf16", 128, 128), ("bf16", 64, 96), ("f32", 32, 64)])
+def test_prompt_then_steps_is_one_sequence(dtype, dk, dv):
+    """A prompt and then single tokens give what the whole sequence gives."""
+    T, P, H = 140, 133, 3
+    c = _make([T, T], H, dk, dv, dtype, False, "tokens", True, seed=21)
+    S = torch.empty_like(c["W0"])
+    o, _ = ttt.forward_decay(c["q"][:, :, :P], c["k"][:, :, :P], c["v"][:, :, :P], c["ld"], state_in=c["W0"],
+                             state_out=S)
+    outs = [o]
+    for t in range(P, T):
+        outs.append(ttt.decode_step_decay(c["q"][:, :, t], c["k"][:, :, t], c["v"][:, :, t], c["ld"], S)[:, :, None])
+    _check_forward(c, torch.cat(outs, 2), S, dtype, np.float64(np.float32(1.0 / math.sqrt(dk))))
+
+
+@pytest.mark.parametrize("dtype,N,H,dk,dv", [("bf16", 1, 1, 128, 1), ("bf16", 5, 3, 64, 128), ("f32", 2, 2, 32, 40),
+                                             ("bf16", 300, 7, 128, 64), ("f32", 97, 3, 64, 64)])
+def test_step_matches_oracle(dtype, N, H, dk, dv):
+    g = torch.Generator().manual_seed(N + dk)
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    pad = 8  # rows longer than the features: strides are the caller's
+    q, k = (torch.randn(N, H, dk + pad, generator=g).to(dt).cuda()[..., :dk] for _ in range(2))
+    v = torch.randn(N, H, dv + pad + -dv % 8, generator=g).to(dt).cuda()[..., :dv]
+    S = torch.randn(N, H, dv, dk, generator=g).cuda()
+    ld = _log_decay(H).cuda()
+    W0 = f64(S)
+    ro, rW = oracle.decay_forward_f64(*(f64(x)[..., None, :] for x in (q, k, v)), f64(ld), -0.25, W0)
+    Ao, AW = oracle.decay_forward_f64(*(np.abs(f64(x))[..., None, :] for x in (q, k, v)), f64(ld), 0.25, np.abs(W0))
+    o = ttt.decode_step_decay(q, k, v, ld, S, eta_const=0.25, ascent=True)
+    _check(S, rW, AW, "state", "f32", 1, 1)
+    tol = (dk + 8) * E * Ao[..., 0, :] + (U * np.abs(ro[..., 0, :]) if dtype == "bf16" else 0)
+    assert (np.abs(f64(o) - ro[..., 0, :]) <= tol * 1.001).all()
+
+
+def test_streams_graphs_and_repeats_give_the_same_bits():
+    c = _make([700, 700], 3, 128, 128, "bf16", False, "tokens", True, seed=30)
+    kw = dict(state_in=c["W0"], segment_tokens=128)
+    fwd = lambda: ttt.forward_decay(c["q"], c["k"], c["v"], c["ld"], **kw)  # noqa: E731
+    bwd = lambda: ttt.backward_decay(c["q"], c["k"], c["v"], c["dO"], c["ld"], grad_state=c["dW"], **kw)  # noqa: E731
+    flat = lambda: [*fwd(), *bwd().values()]  # noqa: E731
+    a = flat()
+    torch.cuda.synchronize()
+    s, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        b = flat()
+    b2 = ttt.forward_decay(c["q"], c["k"], c["v"], c["ld"], stream=s2, **kw)  # another stream, beside the first
+    torch.cuda.synchronize()
+    g, g2 = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        d = flat()
+    with torch.cuda.graph(g2):
+        e = flat()
+    for _ in range(2):
+        g.replay()
+        g2.replay()
+    torch.cuda.synchronize()
+    for x, *others in zip(a, b, d, e):
+        assert all(torch.equal(x, y) for y in others)
+    assert torch.equal(a[0], b2[0]) and torch.equal(a[1], b2[1])
+
+
+def test_caller_workspace_and_out():
+    c = _make([300], 2, 64, 64, "bf16", False, "heads", True, seed=31)
+    o, W = ttt.forward_decay(c["q"], c["k"], c["v"], c["ld"], state_in=c["W0"], segment_tokens=64)
+    w = torch.full((1 << 21,), 255, dtype=torch.uint8, device="cuda")  # NaN where it is read unwritten
+    out, S = torch.empty_like(c["v"]), torch.empty_like(c["W0"])
+    o2, W2 = ttt.forward_decay(c["q"], c["k"], c["v"], c["ld"], state_in=c["W0"], segment_tokens=64, out=out,
+                               state_out=S, workspace=w)
+    assert o2 is out and W2 is S and torch.equal(o, o2) and torch.equal(W, W2)
+
+
+def test_many_short_sequences():
+    lens = [(7 * i) % 40 for i in range(700)]
+    c = _make(lens, 1, 64, 64, "bf16", True, "tokens", True, seed=33)
+    o, W = ttt.forward_decay(c["q"], c["k"], c["v"], c["ld"], cu_seqlens=c["cu"], state_in=c["W0"])
+    _check_forward(c, o, W, "bf16", np.float64(0.125))
+
+
+@pytest.mark.parametrize("cu", [[0, 500, 90, 200], [-7, 100, 100, 1 << 30], [200, 200, 0, 0]])
+def test_offsets_outside_the_rows_touch_nothing_else(cu):
+    """Offsets that leave the rows or decrease are clamped: the call returns,
+    with memory around the output as it was."""
+    c = _make([200], 2, 64, 64, "bf16", True, "tokens", False, seed=35)
+    room = torch.full((3, 200, 2, 64), 5.0, dtype=torch.bfloat16, device="cuda")
+    ttt.forward_decay(c["q"], c["k"], c["v"], c["ld"], cu_seqlens=torch.tensor(cu, dtype=torch.int32).cuda(),
+                      out=room[1:2].transpose(1, 2), segment_tokens=64)
+    assert (room[0] == 5).all() and (room[2] == 5).all()
+
+
+@pytest.mark.parametrize("packed", [False, True])
+def test_layer_then_norm(packed):
+    """The layer and its gated output norm in one call are the two calls."""
+    c = _make([130, 60] if packed else [95, 95], 3, 64, 64, "bf16", packed, "tokens", True, seed=40)
+    B, H, T, dv = c["v"].shape
+    g = torch.Generator().manual_seed(1)
+    gate = torch.randn(B, T, H * dv, generator=g).to(torch.bfloat16).cuda()
+    w, b = (torch.randn(H * dv, generator=g).cuda() for _ in range(2))
+    y, W = ttt.forward_decay_norm(c["q"], c["k"], c["v"], c["ld"], gate=gate, weight=w, bias=b, cu_seqlens=c["cu"],
+                                  state_in=c["W0"])
+    o, W2 = ttt.forward_decay(c["q"], c["k"], c["v"], c["ld"], cu_seqlens=c["cu"], state_in=c["W0"])
+    x = o.transpose(1, 2).reshape(B * T, 1, H * dv)
+    y2, _, _ = ttt.group_norm(x, H, w, b, gate=gate.reshape(x.shape))
+    assert torch.equal(y.view(x.shape), y2) and torch.equal(W, W2)
+
+
+def test_past_2_31_elements():
+    """q, k, v of 257 heads x 65536 tokens x 128 (2^31 elements and more):
+    the last head against the oracle."""
+    H, T, d = 257, 65536, 128
+    c = _make([T], 1, d, d, "bf16", False, "heads", False, seed=60)
+    x = {}
+    for n in ("q", "k", "v"):
+        x[n] = torch.zeros(1, H, T, d, dtype=torch.bfloat16, device="cuda")
+        x[n][:, H - 1] = c[n][:, 0]
+    ld = torch.full((H,), -0.01, device="cuda")
+    o, W = ttt.forward_decay(x["q"], x["k"], x["v"], ld)
+    c["ld"] = ld[-1:]
+    _check_forward(c, o[:, H - 1:], W[:, H - 1:], "bf16", np.float64(np.float32(1.0 / math.sqrt(d))))
+    assert not o[:, :H - 1].any() and not W[:, :H - 1].any()
