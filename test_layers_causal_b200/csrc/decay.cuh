@@ -166,16 +166,33 @@ __device__ __forceinline__ const float* decay_start(const DecayRun& p, const Dec
 // In place over ws: the contribution of each segment of a sequence becomes the
 // state the segment starts from.  One thread per 4 elements of a (sequence,
 // head)'s state, all segments in order (reverse runs: last to first); eight
-// loads are in flight at a time, since each is a round trip to L2.
-__global__ void __launch_bounds__(256) decay_scan_kernel(const DecayGeom g, const DecayRun p,
-                                                         const float* __restrict__ log_decay) {
+// loads are in flight at a time, since each is a round trip to L2.  FINAL: the
+// last segment walked has left its contribution too, and the state behind it
+// goes to s_out; `all` takes in sequences of one segment.
+struct DecayScan {
+  DecayGeom g;
+  int dk, dv, rev;
+  const float* s_in;  // [N][H][dv][dk], or [N][H][dk][dv] where s_in_t; nullptr: zeros
+  int s_in_t;
+  float* s_out;       // or nullptr
+  float* ws;
+  int all;
+};
+struct DecayScans {
+  DecayScan s[2];  // one per blockIdx.y
+};
+
+template <bool FINAL>
+__global__ void __launch_bounds__(256) decay_scan_kernel(const DecayScans ps, const float* __restrict__ log_decay) {
+  const DecayScan& p = ps.s[blockIdx.y];
+  const DecayGeom& g = p.g;
   const size_t dd = static_cast<size_t>(p.dv) * p.dk;
   const int slices = static_cast<int>((dd / 4 + blockDim.x - 1) / blockDim.x);
   const int h = (blockIdx.x / slices) % g.H, n = blockIdx.x / slices / g.H;
   int a, b;
   decay_rows(g, n, a, b);
   const int len = b - a, nseg = decay_segments(len, g.S);
-  if (nseg <= 1) return;
+  if (nseg <= 1 && !p.all) return;
   const int first = decay_first_segment(g, n);
   const size_t e = (static_cast<size_t>(blockIdx.x % slices) * blockDim.x + threadIdx.x) * 4;
   if (e >= dd) return;
@@ -194,21 +211,22 @@ __global__ void __launch_bounds__(256) decay_scan_kernel(const DecayGeom g, cons
   }
   const size_t pitch = static_cast<size_t>(g.H) * dd;
   float* w = p.ws + (static_cast<size_t>(first) * g.H + h) * dd + e;
+  const int sums = FINAL && p.s_out ? nseg : nseg - 1;  // contributions that are there
   constexpr int U = 8;
   for (int i0 = 0; i0 < nseg; i0 += U) {
     float4 t[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int i = i0 + u, j = p.rev ? nseg - 1 - i : i;
-      // (the last segment walked contributes to no start state; segments past the bound have no slot)
-      if (i < nseg - 1 && first + j < g.nseg) t[u] = __ldcg(reinterpret_cast<const float4*>(w + j * pitch));
+      // (segments past the bound, of offsets that overlap, have no slot)
+      if (i < sums && first + j < g.nseg) t[u] = __ldcg(reinterpret_cast<const float4*>(w + j * pitch));
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int i = i0 + u, j = p.rev ? nseg - 1 - i : i;
       if (i < nseg && first + j < g.nseg) {
         __stcg(reinterpret_cast<float4*>(w + j * pitch), run);
-        if (i < nseg - 1) {
+        if (i < sums) {
           const float f = (j == nseg - 1) ? gL : gS;
           run.x = fmaf(f, run.x, t[u].x);
           run.y = fmaf(f, run.y, t[u].y);
@@ -218,6 +236,7 @@ __global__ void __launch_bounds__(256) decay_scan_kernel(const DecayGeom g, cons
       }
     }
   }
+  if (FINAL && p.s_out) *reinterpret_cast<float4*>(p.s_out + (static_cast<size_t>(n) * g.H + h) * dd + e) = run;
 }
 
 // ---------------------------------------------------------- fp32 FMA ----

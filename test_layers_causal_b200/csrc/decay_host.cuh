@@ -40,20 +40,20 @@ struct DecayLayout {
 
 bool decay_fits(int d, int dtype) { return d >= 4 && d <= 256 && d % (dtype == TTT_LA_F32 ? 4 : 8) == 0; }
 
-DecayLayout decay_layout(const int32_t* cu, int N, int H, int T, int dk, int dv, int segment_tokens, long long blocks,
-                         int slots) {
+// `tokens`: of a segment; `every`: one state per segment even where no
+// sequence has two.
+DecayLayout decay_layout(const int32_t* cu, int N, int H, int T, int dk, int dv, int tokens, bool every) {
   DecayLayout l;
   l.g.N = N;
   l.g.H = H;
   l.g.T = T;
   l.g.cu = cu;
-  l.g.S = segment_tokens > 0 ? segment_tokens
-                             : decay_plan_tokens(blocks * H * (cu ? 1 : N), std::max(1, T), slots);
-  const bool multi = l.g.S < T;
-  const long long nseg = cu ? (multi ? T / l.g.S : 0) + static_cast<long long>(N)
-                            : static_cast<long long>(N) * (T > 0 ? (T - 1) / l.g.S + 1 : 1);
+  l.g.S = tokens;
+  const bool multi = tokens < T;
+  const long long nseg = cu ? (multi ? T / tokens : 0) + static_cast<long long>(N)
+                            : static_cast<long long>(N) * (T > 0 ? (T - 1) / tokens + 1 : 1);
   l.g.nseg = nseg < (1ll << 31) ? static_cast<int>(nseg) : -1;
-  l.run_floats = multi ? static_cast<size_t>(nseg) * H * dk * dv : 0;
+  l.run_floats = multi || every ? static_cast<size_t>(nseg) * H * dk * dv : 0;
   return l;
 }
 
@@ -72,21 +72,34 @@ ttt_la_status decay_simt_run(const ttt::DecayGeom& g, const ttt::DecayRun& r, co
   return launch_kernel(kern, static_cast<int>(blocks), 256, smem, st, false, g, r, log_decay);
 }
 
-ttt_la_status decay_scan(const ttt::DecayGeom& g, const ttt::DecayRun& r, const float* log_decay, cudaStream_t st) {
-  const long long dd = static_cast<long long>(r.dk) * r.dv, slices = (dd / 4 + 255) / 256;
-  const long long blocks = slices * g.N * g.H;
+// One scan per entry of `p` (at most two), all over the same sequences.
+ttt_la_status decay_scan(const ttt::DecayScans& p, int n, bool final, const float* log_decay, cudaStream_t st) {
+  long long blocks = 0;
+  for (int i = 0; i < n; ++i) {
+    const long long dd = static_cast<long long>(p.s[i].dk) * p.s[i].dv, slices = (dd / 4 + 255) / 256;
+    blocks = std::max(blocks, slices * p.s[i].g.N * p.s[i].g.H);
+  }
   if (blocks >= (1ll << 31)) return TTT_LA_ERR_UNSUPPORTED;
-  return launch_kernel(ttt::decay_scan_kernel, static_cast<int>(blocks), 256, 0, st, false, g, r, log_decay);
+  const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(n));
+  if (final)
+    ttt::decay_scan_kernel<true><<<grid, 256, 0, st>>>(p, log_decay);
+  else
+    ttt::decay_scan_kernel<false><<<grid, 256, 0, st>>>(p, log_decay);
+  return launched();
 }
 
-// `n` runs of the recurrence over the same tokens.
-ttt_la_status decay_runs(const ttt::DecayGeom& g, const ttt::DecayRun* r, int n, int dtype, const float* log_decay,
-                         cudaStream_t st) {
+ttt::DecayScan decay_scan_of(const ttt::DecayGeom& g, const ttt::DecayRun& r) {
+  return ttt::DecayScan{g, r.dk, r.dv, r.rev, r.s_in, r.s_in_t, nullptr, r.ws, 0};
+}
+
+// `n` runs of the recurrence over the same tokens, in fp32 FMA.
+ttt_la_status decay_simt_runs(const ttt::DecayGeom& g, const ttt::DecayRun* r, int n, int dtype, const float* log_decay,
+                              cudaStream_t st) {
   for (int i = 0; i < n; ++i) {
     ttt_la_status s = TTT_LA_OK;
     for (int pass = r[i].ws ? 0 : 2; pass < 3 && s == TTT_LA_OK; ++pass) {
       if (pass == 1)
-        s = decay_scan(g, r[i], log_decay, st);
+        s = decay_scan(ttt::DecayScans{{decay_scan_of(g, r[i])}}, 1, false, log_decay, st);
       else
         s = dtype == TTT_LA_F32 ? decay_simt_run<float>(g, r[i], log_decay, pass == 0, st)
                                 : decay_simt_run<__nv_bfloat16>(g, r[i], log_decay, pass == 0, st);
@@ -94,6 +107,92 @@ ttt_la_status decay_runs(const ttt::DecayGeom& g, const ttt::DecayRun* r, int n,
     if (s != TTT_LA_OK) return s;
   }
   return TTT_LA_OK;
+}
+
+// ------------------------------------------------- tensor-core kernels ----
+bool decay_on_tc(int dtype, int T, int dk, int dv) { return dtype == TTT_LA_BF16 && T > 0 && dk <= 128 && dv <= 128; }
+
+// Tokens per segment of the tensor-core kernels, whose blocks have an SM each.
+// `heads` sequences of `rows` tokens, `runs` outputs of each.  In units of one
+// tile's outputs: a block costs kDecayBlock more than its tiles (its start
+// state, filling and draining its pipeline), the totals' pass kDecayTotal of
+// that, and cutting the scan.  Whether the final state is asked for plays no
+// part, so that the outputs' bits do not depend on it.
+constexpr double kDecayBlock = 2.0, kDecayTotal = 0.5, kDecayScan = 2.0;
+int decay_tc_plan_tokens(long long heads, int rows, int runs, int slots) {
+  const int tiles = (rows + ttt::kDecayTcC - 1) / ttt::kDecayTcC;
+  int best = tiles;
+  double cost = 1e30;
+  auto waves = [&](long long blocks) { return static_cast<double>((blocks + slots - 1) / slots); };
+  for (int ns = 1; ns <= tiles && ns <= 4096; ++ns) {
+    const int per = (tiles + ns - 1) / ns;
+    const long long n = (tiles + per - 1) / per;
+    double c = waves(heads * n * runs) * (per + kDecayBlock);
+    c += waves(heads * n * (runs > 1 ? 2 : 1)) * (per + kDecayBlock) * kDecayTotal;
+    if (n > 1) c += kDecayScan;
+    if (c < cost) {
+      cost = c;
+      best = per;
+    }
+    if (heads * n * runs > 8ll * slots) break;
+  }
+  return static_cast<int>(std::min<long long>(static_cast<long long>(best) * ttt::kDecayTcC, 1 << 30));
+}
+
+// [N][H][T][d] bf16 in the order of `t`'s strides, boxes of 64 features x 128
+// tokens; features behind d read as zeros and are not written.
+bool decay_map(CUtensorMap* m, const ttt::DecayTensor& t, int N, int H, int T, int d) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(T), static_cast<cuuint64_t>(H),
+                        static_cast<cuuint64_t>(N)};
+  // (the stride of a dimension of size 1 is the caller's to leave out)
+  const long long s[3] = {T > 1 ? t.st : d, H > 1 ? t.sh : d, N > 1 ? t.sb : d};
+  cuuint64_t strides[3];
+  for (int i = 0; i < 3; ++i) strides[i] = static_cast<cuuint64_t>(s[i]) * 2;
+  cuuint32_t box[4] = {64, ttt::kDecayTcC, 1, 1}, es[4] = {1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(t.p), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int DK, int DV>
+ttt_la_status decay_tc_launch(const ttt::DecayTcArgs& a, bool totals, cudaStream_t st) {
+  using Cfg = ttt::DecayTcCfg<DK, DV>;
+  const long long blocks = static_cast<long long>(a.g.nseg) * a.g.H * a.nrun;
+  if (blocks >= (1ll << 31)) return TTT_LA_ERR_UNSUPPORTED;
+  auto kern = totals ? ttt::decay_tc_total_kernel<DK, DV> : ttt::decay_tc_out_kernel<DK, DV>;
+  const int smem = totals ? Cfg::A_SMEM : Cfg::SMEM;
+  if (!grant_smem(reinterpret_cast<const void*>(kern), smem)) return TTT_LA_ERR_CUDA;
+  return launch_kernel(kern, static_cast<int>(blocks), totals ? Cfg::A_THREADS : Cfg::THREADS, smem, st, false, a);
+}
+// Launches the runs r[0 .. n) of `a`, those of equal tile widths together.
+ttt_la_status decay_tc_group(ttt::DecayTcArgs& a, const ttt::DecayTcRun* r, int n, bool totals, cudaStream_t st) {
+  auto wide = [](int d) { return d > 64; };
+  for (int shape = 0; shape < 4; ++shape) {
+    a.nrun = 0;
+    for (int i = 0; i < n; ++i)
+      if ((wide(r[i].dk) ? 1 : 0) + (wide(r[i].dv) ? 2 : 0) == shape) a.run[a.nrun++] = r[i];
+    if (!a.nrun) continue;
+    const ttt_la_status s = shape == 0   ? decay_tc_launch<64, 64>(a, totals, st)
+                            : shape == 1 ? decay_tc_launch<128, 64>(a, totals, st)
+                            : shape == 2 ? decay_tc_launch<64, 128>(a, totals, st)
+                                         : decay_tc_launch<128, 128>(a, totals, st);
+    if (s != TTT_LA_OK) return s;
+  }
+  return TTT_LA_OK;
+}
+
+ttt::DecayTcRun decay_tc_run(int q, int k, int v, int o, const ttt::DecayRun& r) {
+  ttt::DecayTcRun t = {};
+  t.q = q, t.k = k, t.v = v, t.o = o;
+  t.dk = r.dk, t.dv = r.dv, t.rev = r.rev;
+  t.sP = r.sP, t.sR = r.sR, t.sU = r.sU;
+  t.s_in = r.s_in, t.s_in_t = r.s_in_t, t.s_out = r.s_out, t.ws = r.ws;
+  t.op = static_cast<__nv_bfloat16*>(const_cast<void*>(r.o.p));
+  t.ob = r.o.sb, t.oh = r.o.sh, t.ot = r.o.st;
+  t.total_last = r.s_out != nullptr;
+  return t;
 }
 
 // Sizes and strides that the forward and the backward share.
@@ -133,13 +232,34 @@ ttt::DecayRun decay_forward_run(const ttt_la_decay_args* a) {
   return r;
 }
 
-DecayLayout decay_forward_layout(const ttt_la_decay_args* a) {
-  return decay_layout(a->cu_seqlens, a->N, a->H, a->T, a->d_k, a->d_v, a->segment_tokens,
-                      (a->d_v + ttt::kDecayVT - 1) / ttt::kDecayVT, sm_count() * 2);
+// The final states overwrite the start states, which the outputs are read
+// from: those go through the workspace.
+bool decay_in_place(const ttt_la_decay_args* a) {
+  return a->state_in && a->state_in == a->state_out && decay_on_tc(a->dtype, a->T, a->d_k, a->d_v);
 }
-DecayLayout decay_backward_layout(const ttt_la_decay_grad_args* a) {
-  return decay_layout(a->cu_seqlens, a->N, a->H, a->T, a->d_k, a->d_v, a->segment_tokens,
-                      (std::max(a->d_k, a->d_v) + ttt::kDecayVT - 1) / ttt::kDecayVT, sm_count() * 2);
+
+int decay_segment_tokens(int asked, const int32_t* cu, int N, int H, int T, int dk, int dv, int dtype, int runs) {
+  if (asked > 0) return asked;
+  const int rows = std::max(1, T);
+  const long long seqs = cu ? 1 : N;
+  if (decay_on_tc(dtype, T, dk, dv)) return decay_tc_plan_tokens(seqs * H, rows, runs, sm_count());
+  const int widest = runs > 1 ? std::max(dk, dv) : dv;
+  return decay_plan_tokens(seqs * H * ((widest + ttt::kDecayVT - 1) / ttt::kDecayVT), rows, sm_count() * 2);
+}
+
+DecayLayout decay_forward_layout(const ttt_la_decay_args* a) {
+  const int tokens = decay_segment_tokens(a->segment_tokens, a->cu_seqlens, a->N, a->H, a->T, a->d_k, a->d_v, a->dtype,
+                                          1);
+  return decay_layout(a->cu_seqlens, a->N, a->H, a->T, a->d_k, a->d_v, tokens, decay_in_place(a));
+}
+// Workspaces of one run each: dq's and dk's and dv's states; on the tensor
+// cores dk's are dv's.
+DecayLayout decay_backward_layout(const ttt_la_decay_grad_args* a, size_t* floats) {
+  const int tokens = decay_segment_tokens(a->segment_tokens, a->cu_seqlens, a->N, a->H, a->T, a->d_k, a->d_v, a->dtype,
+                                          3);
+  const DecayLayout l = decay_layout(a->cu_seqlens, a->N, a->H, a->T, a->d_k, a->d_v, tokens, false);
+  *floats = 3 * l.run_floats;
+  return l;
 }
 
 }  // namespace
@@ -173,14 +293,37 @@ ttt_la_status ttt_la_forward_decay(const ttt_la_decay_args* a, void* stream) {
   if (need && (!a->workspace || !aligned16(a->workspace) || a->workspace_bytes < need)) return TTT_LA_ERR_INVALID_ARG;
   ttt::DecayRun r = decay_forward_run(a);
   r.ws = need ? static_cast<float*>(a->workspace) : nullptr;
-  return decay_runs(l.g, &r, 1, a->dtype, a->log_decay, static_cast<cudaStream_t>(stream));
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (!decay_on_tc(a->dtype, a->T, a->d_k, a->d_v))
+    return decay_simt_runs(l.g, &r, 1, a->dtype, a->log_decay, st);
+  ttt::DecayTcArgs m = {};
+  const int batch = packed ? 1 : a->N;
+  if (!decay_map(&m.map[0], r.q, batch, a->H, a->T, a->d_k) || !decay_map(&m.map[1], r.k, batch, a->H, a->T, a->d_k) ||
+      !decay_map(&m.map[2], r.v, batch, a->H, a->T, a->d_v) || !decay_map(&m.map[3], r.o, batch, a->H, a->T, a->d_v))
+    return TTT_LA_ERR_CUDA;
+  m.g = l.g, m.log_decay = a->log_decay, m.limit_ns = g_limit_ns;
+  ttt::DecayTcRun run = decay_tc_run(0, 1, 2, 3, r);
+  run.ws_all = decay_in_place(a);
+  if (r.ws || r.s_out) {
+    const ttt_la_status e = decay_tc_group(m, &run, 1, true, st);
+    if (e != TTT_LA_OK) return e;
+  }
+  if (r.ws) {
+    ttt::DecayScan sc = decay_scan_of(l.g, r);
+    sc.s_out = r.s_out, sc.all = run.ws_all;
+    const ttt_la_status e = decay_scan(ttt::DecayScans{{sc}}, 1, true, a->log_decay, st);
+    if (e != TTT_LA_OK) return e;
+  }
+  return decay_tc_group(m, &run, 1, false, st);
 }
 
 size_t ttt_la_backward_decay_workspace_size(const ttt_la_decay_grad_args* a) {
   if (!a || check_decay_shape(a->N, a->H, a->T, a->d_k, a->d_v, a->dtype, a->cu_seqlens, a->log_decay,
                               a->segment_tokens) != TTT_LA_OK)
     return 0;
-  return 3 * decay_backward_layout(a).run_floats * sizeof(float);
+  size_t floats = 0;
+  decay_backward_layout(a, &floats);
+  return floats * sizeof(float);
 }
 
 ttt_la_status ttt_la_backward_decay(const ttt_la_decay_grad_args* a, void* stream) {
@@ -203,9 +346,10 @@ ttt_la_status ttt_la_backward_decay(const ttt_la_decay_grad_args* a, void* strea
     return TTT_LA_ERR_INVALID_ARG;
   if (a->grad_state_in && (a->grad_state_in == a->grad_state || a->grad_state_in == a->state_in))
     return TTT_LA_ERR_INVALID_ARG;
-  const DecayLayout l = decay_backward_layout(a);
+  size_t need = 0;
+  const DecayLayout l = decay_backward_layout(a, &need);
   if (l.g.nseg < 0) return TTT_LA_ERR_UNSUPPORTED;
-  const size_t need = 3 * l.run_floats * sizeof(float);
+  need *= sizeof(float);
   if (need && (!a->workspace || !aligned16(a->workspace) || a->workspace_bytes < need)) return TTT_LA_ERR_INVALID_ARG;
   const ttt::DecayTensor q = decay_tensor(a->q, a->q_stride), k = decay_tensor(a->k, a->k_stride),
                          v = decay_tensor(a->v, a->v_stride), dO = decay_tensor(a->grad_o, a->grad_o_stride);
@@ -227,7 +371,30 @@ ttt_la_status ttt_la_backward_decay(const ttt_la_decay_grad_args* a, void* strea
   r[2].rev = 1, r[2].sP = r[2].sR = c, r[2].sU = 1.f;
   r[2].s_in = a->grad_state, r[2].s_out = a->grad_state_in;
   for (int i = 0; i < 3 && need; ++i) r[i].ws = static_cast<float*>(a->workspace) + i * l.run_floats;
-  return decay_runs(l.g, r, 3, a->dtype, a->log_decay, static_cast<cudaStream_t>(stream));
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (!decay_on_tc(a->dtype, a->T, a->d_k, a->d_v))
+    return decay_simt_runs(l.g, r, 3, a->dtype, a->log_decay, st);
+  ttt::DecayTcArgs m = {};
+  const ttt::DecayTensor x[7] = {q, k, v, dO, r[0].o, r[1].o, r[2].o};
+  const bool values[7] = {false, false, true, true, false, false, true};  // d_v wide
+  for (int i = 0; i < 7; ++i)
+    if (!decay_map(&m.map[i], x[i], packed ? 1 : a->N, a->H, a->T, values[i] ? a->d_v : a->d_k)) return TTT_LA_ERR_CUDA;
+  m.g = l.g, m.log_decay = a->log_decay, m.limit_ns = g_limit_ns;
+  // dk reads the transpose of dv's states
+  ttt::DecayTcRun run[3] = {decay_tc_run(3, 2, 1, 4, r[0]), decay_tc_run(1, 0, 3, 6, r[2]), decay_tc_run(2, 3, 0, 5, r[1])};
+  run[2].ws = run[1].ws, run[2].ws_t = 1;
+  if (need || a->grad_state_in) {
+    // (without segments only dL/dW_0 is wanted)
+    const ttt_la_status e = decay_tc_group(m, need ? run : run + 1, need ? 2 : 1, true, st);
+    if (e != TTT_LA_OK) return e;
+  }
+  if (need) {
+    ttt::DecayScans sc = {{decay_scan_of(l.g, r[0]), decay_scan_of(l.g, r[2])}};
+    sc.s[1].s_out = a->grad_state_in;
+    const ttt_la_status e = decay_scan(sc, 2, true, a->log_decay, st);
+    if (e != TTT_LA_OK) return e;
+  }
+  return decay_tc_group(m, run, 3, false, st);
 }
 
 }  // extern "C"

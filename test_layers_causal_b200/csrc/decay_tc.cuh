@@ -1,0 +1,735 @@
+// decay_tc.cuh -- the recurrence of decay.cuh on the sm_100a tensor cores
+// (tcgen05 + TMEM, operands staged by TMA), bf16 in, fp32 accumulate, for
+// widths up to 128 (narrower ones are zero-filled to 64 or 128 by the loads).
+//
+// Per tile of C = 128 tokens, rows r and columns c in memory order, with P and
+// the powers of decay.cuh:
+//   Sc = Q K^T                       M = C,  N = C,  K = DK
+//   O2 = Q Wbf^T                     M = C,  N = DV, K = DK   Wbf = bf16(X)
+//   D  = V^T K~ , K~_c = w_c k_c     M = DV, N = DK, K = C
+//   O1 = P V , P = bf16(weights * Sc) M = C,  N = DV, K = C
+//   o_r = O1 + (read power of r) O2 ,  X <- gamma^n X + D
+// The state X stays in registers in fp32: D is a fresh product every tile, so
+// the decay between tiles is one FMA and the tensor memory is only read.  The
+// read power multiplies O2 in fp32 in the epilogue, so Q is used as loaded.
+//
+// Three launches where a sequence has several segments or its final state is
+// wanted:
+//   decay_tc_total_kernel   every segment's own contribution to the state,
+//       summed over the segment in one TMEM accumulator (each token weighted
+//       by its distance to the segment's end, so nothing is rescaled), K~ as a
+//       bf16 pair hi + lo whose sum carries it to 2^-16: the states that the
+//       caller sees take no rounding to 8 bits.
+//   decay_scan_kernel       contributions -> start states and final states.
+//   decay_tc_out_kernel     the outputs.  Its X takes bf16(K~) alone, since X
+//       is read for the outputs only, as bf16.
+//
+// Weights gamma^(r-c) <= 1 come as products of a row's and a column's power,
+// each with a distance >= 0 to the edge of a 32-column block, so no power
+// overflows however strong the decay: an underflow is a weight below 2^-126.
+//
+// Waits are bounded as in chunked_tc.cuh: a thread whose wait runs out stops
+// waiting but keeps arriving, so that the block drains and exits.
+#pragma once
+#include "chunked_tc.cuh"
+#include "common.cuh"
+#include "decay.cuh"
+
+namespace ttt {
+
+__device__ __forceinline__ void tma_load_4d(const CUtensorMap* m, uint64_t* bar, void* dst, int x, int y, int z, int w,
+                                            uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint "
+      "[%0], [%1, {%3, %4, %5, %6}], [%2], %7;" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w), "l"(policy)
+      : "memory");
+}
+__device__ __forceinline__ void tma_store_4d(const CUtensorMap* m, const void* src, int x, int y, int z, int w) {
+  asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4, %5}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(m)),
+               "r"(smem_u32(src)), "r"(x), "r"(y), "r"(z), "r"(w)
+               : "memory");
+}
+// tmem_ld_half32 with 16 columns a thread.
+__device__ __forceinline__ void tmem_ld_half16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x32bx2.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16], 16;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+
+constexpr int kDecayTcC = 128;      // tokens per tile
+constexpr int kDecayTcRuns = 3;     // the most runs in one launch
+constexpr int kDecayTcMaps = 7;
+
+// One run: indices of its tensors' maps, and the recurrence's parameters.
+struct DecayTcRun {
+  int q, k, v, o;           // indices into DecayTcArgs::map
+  int dk, dv;
+  int rev;
+  float sP, sR, sU;
+  const float* s_in;        // start states of sequences that are one segment (ws_all: of none)
+  int s_in_t;               // they are [dk][dv]
+  float* s_out;             // total kernel: final states of sequences that are one segment, or nullptr
+  float* ws;                // per segment: contributions, then start states; nullptr: one segment each
+  int ws_t;                 // start states there are [dk][dv] (they are another run's)
+  int ws_all;               // sequences of one segment go through ws too
+  int total_last;           // total kernel: contributions of the last segment in walking order as well
+  // outputs of tiles that end inside the tensor's rows
+  __nv_bfloat16* op;
+  long long ob, oh, ot;
+};
+struct alignas(64) DecayTcArgs {
+  CUtensorMap map[kDecayTcMaps];
+  DecayGeom g;
+  DecayTcRun run[kDecayTcRuns];
+  int nrun;
+  const float* log_decay;
+  uint64_t limit_ns;
+};
+
+// decay_span by all threads of the block; sh: 40 ints of shared memory.
+__device__ __forceinline__ DecaySpan decay_span_block(const DecayGeom& g, int s, int* sh) {
+  if (!g.cu) return decay_span(g, s);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
+  if (tid == 0) sh[32] = -1;
+  int before = 0;
+  for (int n0 = 0; n0 < g.N; n0 += static_cast<int>(blockDim.x)) {
+    const int n = n0 + tid;
+    int a = 0, b = 0, c = 0;
+    if (n < g.N) {
+      decay_rows(g, n, a, b);
+      c = decay_segments(b - a, g.S);
+    }
+    int incl = c;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, off);
+      if (lane >= off) incl += y;
+    }
+    if (lane == 31) sh[warp] = incl;
+    __syncthreads();
+    int below = before, all = before;
+    for (int w = 0; w < nw; ++w) {
+      if (w < warp) below += sh[w];
+      all += sh[w];
+    }
+    incl += below;
+    if (incl > s && incl - c <= s && c > 0) {  // exactly one thread, if any
+      sh[32] = n;
+      sh[33] = a;
+      sh[34] = b;
+      sh[35] = s - (incl - c);
+      sh[36] = c;
+    }
+    before = all;
+    __syncthreads();
+    if (sh[32] >= 0) break;
+  }
+  DecaySpan r;
+  r.seq = sh[32];
+  r.batch = 0;
+  r.row0 = r.len = r.j = r.nseg = 0;
+  if (r.seq >= 0) {
+    r.j = sh[35];
+    r.nseg = sh[36];
+    r.row0 = sh[33] + r.j * g.S;
+    r.len = min(g.S, sh[34] - r.row0);
+  }
+  return r;
+}
+
+template <int DK, int DV>
+struct DecayTcCfg {
+  static constexpr int C = kDecayTcC;
+  static constexpr int TK = C * DK * 2, TV = C * DV * 2;   // bytes of a tile
+  static constexpr int STAGE = 2 * TK + TV;                // Q, K, V
+  static constexpr bool PSEP = DK == 64;                   // P beside the stages; else over Q once Sc and O2 have read it
+  static constexpr int PB = PSEP ? C * C * 2 : 0;
+  static constexpr int WBF = DK * DV * 2;
+  static constexpr int NST = (DK == 64 && DV == 64) ? 3 : 2;
+  static constexpr int BIG = NST * STAGE + WBF + PB;
+  static constexpr int SMEM = BIG + 1024 + 1024;           // + barriers and tables, + alignment
+  static constexpr int THREADS = 576;                      // TMA, MMA, 4 warps P, 4 warps O, 8 warps state
+  static constexpr int NW = DK * DV / 256;                 // elements of X per state thread
+  // tensor memory: Sc (then O1) twice, O2, D
+  static constexpr int T_O2 = 2 * C, T_D = 2 * C + DV;
+  static_assert(T_D + DK <= 512, "tensor memory");
+  static_assert(SMEM <= 232448, "shared memory");
+  static_assert(!PSEP ? C * C * 2 <= TK : true, "P over Q");
+  // total kernel: K (then hi), V, lo per stage
+  static constexpr int A_STAGE = 2 * TK + TV;
+  static constexpr int A_NST = (DK == 64 && DV == 64) ? 4 : 2;
+  static constexpr int A_SMEM = A_NST * A_STAGE + 1024 + 1024;
+  static constexpr int A_THREADS = 320;                    // TMA, MMA, 8 warps
+  static_assert(A_SMEM <= 232448, "shared memory");
+};
+
+// The elements of the DV x DK state that thread (w = 0..7, lane) of the state
+// warps owns: row `row`, columns col .. col + NW.  DV = 128: a TMEM lane a row.
+// DV = 64: an M = 64 accumulator fills lanes 0-15 of each quadrant, read in two
+// column halves by the two halves of the warp.  Warp w must be on quadrant w & 3.
+template <int DK, int DV>
+__device__ __forceinline__ void decay_state_at(int quad, int half, int lane, int& row, int& col) {
+  if constexpr (DV == 128) {
+    row = quad * 32 + lane;
+    col = half * (DK / 2);
+  } else {
+    row = quad * 16 + (lane & 15);
+    col = half * (DK / 2) + (lane >> 4) * (DK / 4);
+  }
+}
+// Elements [I * 32, I * 32 + 32) of them (all 16 where there are 16).
+template <int DK, int DV, int I, int N>
+__device__ __forceinline__ void decay_state_ld(uint32_t t_d, int quad, int half, uint32_t (&r)[N]) {
+  const uint32_t at = t_d + (static_cast<uint32_t>(quad * 32) << 16) + half * (DK / 2) + I * 32;
+  if constexpr (DV == 128)
+    tmem_ld32(at, r);
+  else if constexpr (DK == 128)
+    tmem_ld_half32(at, r);
+  else
+    tmem_ld_half16(at, r);
+}
+
+// Scales rows of a K tile (NB 64-column blocks of C rows of 128 bytes) in
+// place by weight(row), 0 for rows >= n, and zeroes V's rows >= n, so that
+// nothing behind the segment's end enters a sum, whatever it holds.  `t` of
+// 256 threads.  LO: the rest K~ - bf16(K~) goes to the tile `lo`.
+template <int DK, int DV, bool LO, typename F>
+__device__ __forceinline__ void decay_scale_tile(uint8_t* kt, uint8_t* vt, uint8_t* lo, int n, int t, bool scale,
+                                                 F&& weight) {
+  constexpr int C = kDecayTcC, UNITS = C * DK / 8;
+  if (scale) {
+#pragma unroll 4
+    for (int i = 0; i < UNITS / 256; ++i) {
+      const int u = i * 256 + t, row = (u >> 3) & (C - 1);  // (a unit's place in its row does not matter here)
+      const float w = row < n ? weight(row) : 0.f;
+      uint4 x = *reinterpret_cast<const uint4*>(kt + u * 16);
+      uint32_t* xs = reinterpret_cast<uint32_t*>(&x);
+      uint4 l;
+      uint32_t* ls = reinterpret_cast<uint32_t*>(&l);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float a = row < n ? __uint_as_float(xs[e] << 16) * w : 0.f;
+        const float b = row < n ? __uint_as_float(xs[e] & 0xffff0000u) * w : 0.f;
+        const uint32_t h = pack_bf16x2(a, b);
+        xs[e] = h;
+        if constexpr (LO) ls[e] = pack_bf16x2(a - __uint_as_float(h << 16), b - __uint_as_float(h & 0xffff0000u));
+      }
+      *reinterpret_cast<uint4*>(kt + u * 16) = x;
+      if constexpr (LO) *reinterpret_cast<uint4*>(lo + u * 16) = l;
+    }
+  }
+  if (n < C) {
+    const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+    for (int u = t; u < C * DV / 8; u += 256)
+      if (((u >> 3) & (C - 1)) >= n) *reinterpret_cast<uint4*>(vt + u * 16) = z;
+  }
+}
+
+__device__ __forceinline__ bool decay_wait(bool& dead, uint64_t* bar, uint32_t parity, uint64_t lim) {
+  if (!dead) dead = !mbar_wait(bar, parity, lim);
+  return !dead;
+}
+// This warp's writes (and tensor memory reads) before one arrival for it.
+__device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
+  tc_fence_before();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
+}
+
+// ------------------------------------------------------------- totals ----
+// One block per (segment, head, run).  Tiles are walked from the far end of
+// the walking order to its start, so that the tiles the output kernel reads
+// first are the ones last left in L2.
+template <int DK, int DV>
+__global__ void __launch_bounds__(320, 1) decay_tc_total_kernel(const __grid_constant__ DecayTcArgs A) {
+  using Cfg = DecayTcCfg<DK, DV>;
+  constexpr int C = Cfg::C, NST = Cfg::A_NST, STAGE = Cfg::A_STAGE, TK = Cfg::TK, TV = Cfg::TV, NW = Cfg::NW;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + NST * STAGE);
+  uint64_t *full = bars, *ready = bars + NST, *empty = bars + 2 * NST, *done = bars + 3 * NST;
+  uint32_t* holder = reinterpret_cast<uint32_t*>(bars + 3 * NST + 1);
+  int* sh = reinterpret_cast<int*>(holder + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const DecayGeom& g = A.g;
+  const int b = blockIdx.x, ri = b % A.nrun, h = (b / A.nrun) % g.H, s = b / A.nrun / g.H;
+  const DecayTcRun& p = A.run[ri];
+  const DecaySpan sp = decay_span_block(g, s, sh);
+  if (sp.seq < 0) return;
+  if (!p.total_last && sp.j == (p.rev ? 0 : sp.nseg - 1)) return;
+  const uint64_t lim = A.limit_ns;
+  const int nt = (sp.len + C - 1) / C;
+  auto tile_at = [&](int i) { return p.rev ? i : nt - 1 - i; };
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NST; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&ready[i], 8);
+      mbar_init(&empty[i], 1);
+    }
+    mbar_init(done, 1);
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(holder, DK);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *holder;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      bool dead = false;
+      const uint64_t pol = l2_policy_evict_last();
+      for (int i = 0; i < nt; ++i) {
+        const int st = i % NST, y = sp.row0 + tile_at(i) * C;
+        if (i >= NST) decay_wait(dead, &empty[st], (i / NST - 1) & 1, lim);
+        mbar_arrive_expect_tx(&full[st], TK + TV);
+        uint8_t* d = smem + st * STAGE;
+#pragma unroll
+        for (int x = 0; x < DK / 64; ++x) tma_load_4d(&A.map[p.k], &full[st], d + x * C * 128, x * 64, y, h, sp.batch, pol);
+#pragma unroll
+        for (int x = 0; x < DV / 64; ++x)
+          tma_load_4d(&A.map[p.v], &full[st], d + TK + x * C * 128, x * 64, y, h, sp.batch, pol);
+      }
+      for (int i = max(0, nt - NST); i < nt; ++i) mbar_wait(&full[i % NST], (i / NST) & 1, lim);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      bool dead = false;
+      constexpr uint32_t ID = idesc_bf16_f32(DV, DK, true, true);
+      for (int i = 0; i < nt; ++i) {
+        const int st = i % NST;
+        const uint32_t base = smem_u32(smem) + st * STAGE;
+        const uint64_t dk = sdesc_sw128(base, C * 128, 1024), dv = sdesc_sw128(base + TK, C * 128, 1024);
+        const uint64_t dl = sdesc_sw128(base + TK + TV, C * 128, 1024);
+        decay_wait(dead, &ready[st], (i / NST) & 1, lim);
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < C / 16; ++kk) mma_bf16_ss(tmem, dv + mn_step(kk), dk + mn_step(kk), ID, i > 0 || kk > 0);
+#pragma unroll
+        for (int kk = 0; kk < C / 16; ++kk) mma_bf16_ss(tmem, dv + mn_step(kk), dl + mn_step(kk), ID, 1);
+        tc_commit(&empty[st]);
+      }
+      tc_commit(done);
+      mbar_wait(done, 0, lim);
+    }
+  } else {
+    bool dead = false;
+    const int t = static_cast<int>(threadIdx.x) - 64, w = warp - 2, quad = warp & 3, half = w >> 2;
+    const float l = decay_log(A.log_decay, h);
+    for (int i = 0; i < nt; ++i) {
+      const int st = i % NST, at = tile_at(i) * C, n = min(C, sp.len - at);
+      // distance to where the contribution is taken: behind the last token, or (reverse) before the first
+      const int far = p.rev ? at + 1 : sp.len - 1 - at, step = p.rev ? 1 : -1;
+      decay_wait(dead, &full[st], (i / NST) & 1, lim);
+      uint8_t* d = smem + st * STAGE;
+      decay_scale_tile<DK, DV, true>(d, d + TK, d + TK + TV, n, t, true,
+                                     [&](int r) { return p.sU * expf(l * static_cast<float>(far + step * r)); });
+      fence_async_smem();
+      warp_arrive(&ready[st], lane);
+    }
+    decay_wait(dead, done, 0, lim);
+    __syncwarp();
+    tc_fence_after();
+    int row, col;
+    decay_state_at<DK, DV>(quad, half, lane, row, col);
+    const size_t dd = static_cast<size_t>(p.dk) * p.dv, off = static_cast<size_t>(row) * p.dk;
+    // a sequence of one segment: its final state is made here
+    const bool direct = sp.nseg == 1 && !p.ws_all;
+    float* dst = (direct ? p.s_out + (static_cast<size_t>(sp.seq) * g.H + h) * dd
+                         : p.ws + (static_cast<size_t>(s) * g.H + h) * dd) + off;
+    const float* src = direct && p.s_in ? p.s_in + (static_cast<size_t>(sp.seq) * g.H + h) * dd + off : nullptr;
+    const float gl = expf(l * static_cast<float>(sp.len));
+    constexpr int PIECE = NW < 32 ? NW : 32;
+#pragma unroll
+    for (int i = 0; i < NW / PIECE; ++i) {
+      uint32_t r[PIECE];
+      if (nt > 0) {
+        if (i == 0)
+          decay_state_ld<DK, DV, 0>(tmem, quad, half, r);
+        else
+          decay_state_ld<DK, DV, 1>(tmem, quad, half, r);
+        tmem_ld_wait();
+      } else {
+#pragma unroll
+        for (int e = 0; e < PIECE; ++e) r[e] = 0u;
+      }
+#pragma unroll
+      for (int e = 0; e < PIECE; e += 4) {
+        const int c = col + i * 32 + e;
+        if (row >= p.dv || c >= p.dk) continue;
+        float4 x = make_float4(__uint_as_float(r[e]), __uint_as_float(r[e + 1]), __uint_as_float(r[e + 2]),
+                               __uint_as_float(r[e + 3]));
+        if (src) {
+          const float4 y = *reinterpret_cast<const float4*>(src + c);
+          x.x = fmaf(gl, y.x, x.x);
+          x.y = fmaf(gl, y.y, x.y);
+          x.z = fmaf(gl, y.z, x.z);
+          x.w = fmaf(gl, y.w, x.w);
+        }
+        *reinterpret_cast<float4*>(dst + c) = x;
+      }
+    }
+    tc_fence_before();
+  }
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, DK);
+  }
+}
+
+// ------------------------------------------------------------ outputs ----
+// One block per (segment, head, run), one per SM.  18 warps: 0 TMA loads, 1
+// MMA issue, 2-5 P, 6-9 outputs, 10-17 the state (and K~).  Order of the MMAs
+// for tile c: O2, D, Sc of tile c+1 (as soon as it has landed), O1; Sc/O1 is
+// double-buffered in tensor memory, so that scores are ready when their P can
+// be written.
+template <int DK, int DV>
+__global__ void __launch_bounds__(576, 1) decay_tc_out_kernel(const __grid_constant__ DecayTcArgs A) {
+  using Cfg = DecayTcCfg<DK, DV>;
+  constexpr int C = Cfg::C, NST = Cfg::NST, STAGE = Cfg::STAGE, TK = Cfg::TK, TV = Cfg::TV, NW = Cfg::NW;
+  constexpr bool PSEP = Cfg::PSEP;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const uint32_t sbase = smem_u32(smem);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Cfg::BIG);
+  uint64_t* full = bars;                // [NST] tile landed
+  uint64_t* empty = bars + NST;         // [NST] stage free: its output has left
+  uint64_t* sfull = bars + 2 * NST;     // [2] scores complete
+  uint64_t* kready = sfull + 2;         // K~ written, rows past the end zeroed; D of the tile before read out
+  uint64_t* qdone = sfull + 3;          // O2 complete: Q and Wbf have been read
+  uint64_t* pready = sfull + 4;         // P written, scores read out
+  uint64_t* dfull = sfull + 5;          // D complete
+  uint64_t* wready = sfull + 6;         // Wbf written
+  uint64_t* ofull = sfull + 7;          // O1 complete (and everything before it)
+  uint64_t* ofree = sfull + 8;          // O1 and O2 read out
+  uint64_t* drain = sfull + 9;
+  float* colp = reinterpret_cast<float*>(bars + 2 * NST + 12);  // [32] gamma^(31-t), reverse gamma^t
+  float* gp = colp + 32;                                        // [32] gamma^t
+  uint32_t* holder = reinterpret_cast<uint32_t*>(gp + 32);
+  int* sh = reinterpret_cast<int*>(holder + 1);                 // [40]
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const DecayGeom& g = A.g;
+  const int b = blockIdx.x, ri = b % A.nrun, h = (b / A.nrun) % g.H, s = b / A.nrun / g.H;
+  const DecayTcRun& p = A.run[ri];
+  const DecaySpan sp = decay_span_block(g, s, sh);
+  if (sp.seq < 0 || sp.len <= 0) return;
+  const uint64_t lim = A.limit_ns;
+  const bool rev = p.rev != 0;
+  const int nt = (sp.len + C - 1) / C;
+  auto tile_at = [&](int i) { return (rev ? nt - 1 - i : i) * C; };  // first token of the i-th tile walked
+  const float l = decay_log(A.log_decay, h);
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NST; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    mbar_init(&sfull[0], 1);
+    mbar_init(&sfull[1], 1);
+    mbar_init(kready, 8);
+    mbar_init(qdone, 1);
+    mbar_init(pready, 4);
+    mbar_init(dfull, 1);
+    mbar_init(wready, 8);
+    mbar_init(ofull, 1);
+    mbar_init(ofree, 4);
+    mbar_init(drain, 1);
+    fence_mbar_init();
+  }
+  if (threadIdx.x < 32) {
+    gp[lane] = expf(l * static_cast<float>(lane));
+    colp[lane] = expf(l * static_cast<float>(rev ? lane : 31 - lane));
+  }
+  if (warp == 1) {
+    tmem_alloc(holder, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *holder;
+  const uint32_t t_o2 = tmem + Cfg::T_O2, t_d = tmem + Cfg::T_D;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ loads --
+    if (lane == 0) {
+      bool dead = false;
+      const uint64_t pol = l2_policy_evict_first();
+      for (int i = 0; i < nt; ++i) {
+        const int st = i % NST, y = sp.row0 + tile_at(i);
+        if (i >= NST) decay_wait(dead, &empty[st], (i / NST - 1) & 1, lim);
+        mbar_arrive_expect_tx(&full[st], 2 * TK + TV);
+        uint8_t* d = smem + st * STAGE;
+#pragma unroll
+        for (int x = 0; x < DK / 64; ++x) {
+          tma_load_4d(&A.map[p.q], &full[st], d + x * C * 128, x * 64, y, h, sp.batch, pol);
+          tma_load_4d(&A.map[p.k], &full[st], d + TK + x * C * 128, x * 64, y, h, sp.batch, pol);
+        }
+#pragma unroll
+        for (int x = 0; x < DV / 64; ++x)
+          tma_load_4d(&A.map[p.v], &full[st], d + 2 * TK + x * C * 128, x * 64, y, h, sp.batch, pol);
+      }
+      for (int i = max(0, nt - NST); i < nt; ++i) mbar_wait(&full[i % NST], (i / NST) & 1, lim);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------- MMAs --
+    if (lane == 0) {
+      bool dead = false;
+      constexpr uint32_t ID_S = idesc_bf16_f32(C, C, false, false), ID_Q = idesc_bf16_f32(C, DV, false, false);
+      constexpr uint32_t ID_D = idesc_bf16_f32(DV, DK, true, true), ID_P = idesc_bf16_f32(C, DV, false, true);
+      const uint64_t d_w = sdesc_sw128(sbase + NST * STAGE, 16, 1024);
+      const uint64_t d_psep = sdesc_sw128(sbase + NST * STAGE + Cfg::WBF, 16, 1024);
+      auto scores = [&](int i) {  // its tile has landed
+        const uint32_t base = sbase + (i % NST) * STAGE;
+        const uint64_t dq = sdesc_sw128(base, 16, 1024), dk = sdesc_sw128(base + TK, 16, 1024);
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < DK / 16; ++kk)
+          mma_bf16_ss(tmem + (i & 1) * C, dq + k_step(C, kk), dk + k_step(C, kk), ID_S, kk > 0);
+        tc_commit(&sfull[i & 1]);
+      };
+      decay_wait(dead, &full[0], 0, lim);
+      scores(0);
+      for (int i = 0; i < nt; ++i) {
+        const uint32_t base = sbase + (i % NST) * STAGE, par = i & 1;
+        const uint64_t dq = sdesc_sw128(base, 16, 1024), dkm = sdesc_sw128(base + TK, C * 128, 1024);
+        const uint64_t dvm = sdesc_sw128(base + 2 * TK, C * 128, 1024);
+        decay_wait(dead, wready, par, lim);
+        if (i > 0) decay_wait(dead, ofree, (i - 1) & 1, lim);
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < DK / 16; ++kk)
+          mma_bf16_ss(t_o2, dq + k_step(C, kk), d_w + k_step(DV, kk), ID_Q, kk > 0);
+        tc_commit(qdone);
+        decay_wait(dead, kready, par, lim);
+        tc_fence_after();
+        if (i + 1 < nt) {
+#pragma unroll
+          for (int kk = 0; kk < C / 16; ++kk) mma_bf16_ss(t_d, dvm + mn_step(kk), dkm + mn_step(kk), ID_D, kk > 0);
+          tc_commit(dfull);
+        }
+        // (the other score buffer was read out when ofree of tile i - 1 came)
+        const int j = i + 1;
+        bool ahead = j < nt && !dead && mbar_try_wait(smem_u32(&full[j % NST]), (j / NST) & 1);
+        if (ahead) scores(j);
+        decay_wait(dead, pready, par, lim);
+        tc_fence_after();
+        const uint64_t dp = PSEP ? d_psep : dq;
+#pragma unroll
+        for (int kk = 0; kk < C / 16; ++kk)
+          mma_bf16_ss(tmem + par * C, dp + k_step(C, kk), dvm + mn_step(kk), ID_P, kk > 0);
+        tc_commit(ofull);
+        if (j < nt && !ahead) {
+          decay_wait(dead, &full[j % NST], (j / NST) & 1, lim);
+          scores(j);
+        }
+      }
+      tc_commit(drain);
+      mbar_wait(drain, 0, lim);
+    }
+  } else if (warp < 6) {
+    // ---------------------------------------------------------------- P --
+    bool dead = false;
+    const int quad = warp & 3, r = quad * 32 + lane;
+    for (int i = 0; i < nt; ++i) {
+      const int n = min(C, sp.len - tile_at(i));
+      decay_wait(dead, &sfull[i & 1], (i >> 1) & 1, lim);
+      if (PSEP) {
+        if (i > 0) decay_wait(dead, ofull, (i - 1) & 1, lim);  // P of the tile before has been read
+      } else {
+        decay_wait(dead, qdone, i & 1, lim);
+      }
+      __syncwarp();
+      tc_fence_after();
+      const uint32_t tile = PSEP ? sbase + NST * STAGE + Cfg::WBF : sbase + (i % NST) * STAGE;
+      const uint32_t ts = tmem + (static_cast<uint32_t>(quad * 32) << 16) + (i & 1) * C;
+#pragma unroll 1
+      for (int jb = 0; jb < C / 32; ++jb) {
+        uint32_t x[32];
+        const int j0 = jb * 32;
+        if (rev ? jb < quad : jb > quad) {
+          if (PSEP && i > 0) continue;  // the zeros of the first tile are still there
+#pragma unroll
+          for (int e = 0; e < 32; ++e) x[e] = 0u;
+          store_row32_bf16(tile, C * 128, r, j0, x);
+          continue;
+        }
+        tmem_ld32(ts + j0, x);
+        if (jb == quad) {
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const int d = rev ? e - lane : lane - e;
+            const float wgt = p.sP * gp[d & 31];
+            x[e] = d >= 0 ? __float_as_uint(wgt * __uint_as_float(x[e])) : 0u;
+          }
+        } else {
+          const float rp = p.sP * expf(l * static_cast<float>(rev ? j0 - r : r - j0 - 31));
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            const float4 cp = *reinterpret_cast<const float4*>(colp + e);
+            x[e] = __float_as_uint(rp * cp.x * __uint_as_float(x[e]));
+            x[e + 1] = __float_as_uint(rp * cp.y * __uint_as_float(x[e + 1]));
+            x[e + 2] = __float_as_uint(rp * cp.z * __uint_as_float(x[e + 2]));
+            x[e + 3] = __float_as_uint(rp * cp.w * __uint_as_float(x[e + 3]));
+          }
+        }
+        if (rev && j0 + 32 > n) {  // columns behind the segment's end (forward: c <= r < n)
+#pragma unroll
+          for (int e = 0; e < 32; ++e) x[e] = j0 + e < n ? x[e] : 0u;
+        }
+        store_row32_bf16(tile, C * 128, r, j0, x);
+      }
+      fence_async_smem();
+      warp_arrive(pready, lane);
+    }
+  } else if (warp < 10) {
+    // ---------------------------------------------------------- outputs --
+    bool dead = false;
+    const int quad = warp & 3, r = quad * 32 + lane;
+    for (int i = 0; i < nt; ++i) {
+      const int at = tile_at(i), n = min(C, sp.len - at), y = sp.row0 + at;
+      const float rp = r < n ? p.sR * expf(l * static_cast<float>(rev ? n - 1 - r : r + 1)) : 0.f;
+      decay_wait(dead, ofull, i & 1, lim);
+      __syncwarp();
+      tc_fence_after();
+      const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
+      const uint32_t stage = sbase + (i % NST) * STAGE + 2 * TK;
+      // a tile that ends inside the tensor's rows is stored row by row: a box would reach the rows behind
+      const bool whole = n == C || y + n == g.T;
+      __nv_bfloat16* out = p.op + static_cast<size_t>(sp.batch) * p.ob + static_cast<size_t>(h) * p.oh +
+                           static_cast<size_t>(y + r) * p.ot;
+#pragma unroll
+      for (int c0 = 0; c0 < DV; c0 += 32) {
+        uint32_t a[32], q[32];
+        tmem_ld32(tmem + lanes + (i & 1) * C + c0, a);
+        tmem_ld32(t_o2 + lanes + c0, q);
+        tmem_ld_wait();
+        if (c0 + 32 == DV) warp_arrive(ofree, lane);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) a[e] = __float_as_uint(fmaf(rp, __uint_as_float(q[e]), __uint_as_float(a[e])));
+        if (whole) {
+          store_row32_bf16(stage, C * 128, r, c0, a);
+        } else if (r < n) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 8)
+            if (c0 + e < p.dv)
+              *reinterpret_cast<uint4*>(out + c0 + e) = make_uint4(
+                  pack_bf16x2(__uint_as_float(a[e]), __uint_as_float(a[e + 1])),
+                  pack_bf16x2(__uint_as_float(a[e + 2]), __uint_as_float(a[e + 3])),
+                  pack_bf16x2(__uint_as_float(a[e + 4]), __uint_as_float(a[e + 5])),
+                  pack_bf16x2(__uint_as_float(a[e + 6]), __uint_as_float(a[e + 7])));
+        }
+      }
+      if (whole) {
+        fence_async_smem();
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        if (threadIdx.x == 6 * 32) {
+#pragma unroll
+          for (int x = 0; x < DV / 64; ++x)
+            tma_store_4d(&A.map[p.o], smem + (i % NST) * STAGE + 2 * TK + x * C * 128, x * 64, y, h, sp.batch);
+          bulk_commit();
+          bulk_wait_read0();
+          mbar_arrive(&empty[i % NST]);
+        }
+      } else if (threadIdx.x == 6 * 32) {
+        mbar_arrive(&empty[i % NST]);
+      }
+    }
+    if (threadIdx.x == 6 * 32) bulk_wait0();
+  } else {
+    // ------------------------------------------------------------ state --
+    bool dead = false;
+    const int t = static_cast<int>(threadIdx.x) - 320, quad = warp & 3, half = (warp - 10) >> 2;
+    int row, col;
+    decay_state_at<DK, DV>(quad, half, lane, row, col);
+    float w[NW];
+    {
+      const size_t dd = static_cast<size_t>(p.dk) * p.dv;
+      const bool via = p.ws && (sp.nseg > 1 || p.ws_all);
+      const float* src = via ? p.ws + (static_cast<size_t>(s) * g.H + h) * dd
+                             : p.s_in ? p.s_in + (static_cast<size_t>(sp.seq) * g.H + h) * dd : nullptr;
+      const bool tr = via ? p.ws_t != 0 : p.s_in_t != 0;
+#pragma unroll
+      for (int e = 0; e < NW; ++e) w[e] = 0.f;
+      if (src && row < p.dv) {
+        if (tr) {
+#pragma unroll
+          for (int e = 0; e < NW; ++e)
+            if (col + e < p.dk) w[e] = __ldcg(src + static_cast<size_t>(col + e) * p.dv + row);
+        } else {
+#pragma unroll
+          for (int e = 0; e < NW; e += 4)
+            if (col + e < p.dk) {
+              const float4 x = __ldcg(reinterpret_cast<const float4*>(src + static_cast<size_t>(row) * p.dk + col + e));
+              w[e] = x.x, w[e + 1] = x.y, w[e + 2] = x.z, w[e + 3] = x.w;
+            }
+        }
+      }
+    }
+    const uint32_t wtile = sbase + NST * STAGE;
+    auto put_w = [&]() {
+#pragma unroll
+      for (int e = 0; e < NW; e += 8)
+        st_shared_v4(wtile + ((col + e) >> 6) * (DV * 128) + sw128_off(row, ((col + e) & 63) >> 3),
+                     pack_bf16x2(w[e], w[e + 1]), pack_bf16x2(w[e + 2], w[e + 3]), pack_bf16x2(w[e + 4], w[e + 5]),
+                     pack_bf16x2(w[e + 6], w[e + 7]));
+      fence_async_smem();
+      warp_arrive(wready, lane);
+    };
+    put_w();
+    for (int i = 0; i < nt; ++i) {
+      const int st = i % NST, n = min(C, sp.len - tile_at(i));
+      const bool more = i + 1 < nt;
+      decay_wait(dead, &full[st], (i / NST) & 1, lim);
+      decay_wait(dead, &sfull[i & 1], (i >> 1) & 1, lim);  // K has been read for the scores
+      __syncwarp();
+      uint8_t* d = smem + st * STAGE;
+      decay_scale_tile<DK, DV, false>(d + TK, d + 2 * TK, nullptr, n, t, more, [&](int x) {
+        return p.sU * expf(l * static_cast<float>(rev ? x + 1 : n - 1 - x));
+      });
+      fence_async_smem();
+      warp_arrive(kready, lane);
+      if (!more) break;
+      const float gn = expf(l * static_cast<float>(n));
+      decay_wait(dead, dfull, i & 1, lim);
+      __syncwarp();
+      tc_fence_after();
+      constexpr int PIECE = NW < 32 ? NW : 32;
+#pragma unroll
+      for (int x = 0; x < NW / PIECE; ++x) {
+        uint32_t y[PIECE];
+        if (x == 0)
+          decay_state_ld<DK, DV, 0>(t_d, quad, half, y);
+        else
+          decay_state_ld<DK, DV, 1>(t_d, quad, half, y);
+        tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < PIECE; ++e) w[x * PIECE + e] = fmaf(gn, w[x * PIECE + e], __uint_as_float(y[e]));
+      }
+      decay_wait(dead, qdone, i & 1, lim);  // Wbf has been read
+      __syncwarp();
+      put_w();
+    }
+    tc_fence_before();
+  }
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+}  // namespace ttt

@@ -27,6 +27,7 @@
 #include "chunked_tc_mom.cuh"
 #include "common.cuh"
 #include "decay.cuh"
+#include "decay_tc.cuh"
 #include "decode.cuh"
 #include "feature_map.cuh"
 #include "group_norm.cuh"
