@@ -51,6 +51,14 @@ __device__ __forceinline__ void tma_store_4d(const CUtensorMap* m, const void* s
                "r"(smem_u32(src)), "r"(x), "r"(y), "r"(z), "r"(w)
                : "memory");
 }
+// tmem_ld32 with 16 columns.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
 // tmem_ld_half32 with 16 columns a thread.
 __device__ __forceinline__ void tmem_ld_half16(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
@@ -152,7 +160,7 @@ struct DecayTcCfg {
   static constexpr int NST = (DK == 64 && DV == 64) ? 3 : 2;
   static constexpr int BIG = NST * STAGE + WBF + PB;
   static constexpr int SMEM = BIG + 1024 + 1024;           // + barriers and tables, + alignment
-  static constexpr int THREADS = 576;                      // TMA, MMA, 4 warps P, 4 warps O, 8 warps state
+  static constexpr int THREADS = 576;                      // TMA, MMA, 8 warps P and outputs, 8 warps state
   static constexpr int NW = DK * DV / 256;                 // elements of X per state thread
   // tensor memory: Sc (then O1) twice, O2, D
   static constexpr int T_O2 = 2 * C, T_D = 2 * C + DV;
@@ -181,56 +189,78 @@ __device__ __forceinline__ void decay_state_at(int quad, int half, int lane, int
     col = half * (DK / 2) + (lane >> 4) * (DK / 4);
   }
 }
-// Elements [I * 32, I * 32 + 32) of them (all 16 where there are 16).
-template <int DK, int DV, int I, int N>
-__device__ __forceinline__ void decay_state_ld(uint32_t t_d, int quad, int half, uint32_t (&r)[N]) {
-  const uint32_t at = t_d + (static_cast<uint32_t>(quad * 32) << 16) + half * (DK / 2) + I * 32;
+// Elements [i, i + N) of them (DV = 64: i = 0, N = NW).
+template <int DK, int DV, int N>
+__device__ __forceinline__ void decay_state_ld(uint32_t t_d, int quad, int half, int i, uint32_t (&r)[N]) {
+  const uint32_t at = t_d + (static_cast<uint32_t>(quad * 32) << 16) + half * (DK / 2) + i;
+  static_assert(DV == 128 ? N == 16 : N == DK / 4, "");
   if constexpr (DV == 128)
-    tmem_ld32(at, r);
+    tmem_ld16(at, r);
   else if constexpr (DK == 128)
     tmem_ld_half32(at, r);
   else
     tmem_ld_half16(at, r);
 }
 
-// Scales rows of a K tile (NB 64-column blocks of C rows of 128 bytes) in
-// place by weight(row), 0 for rows >= n, and zeroes V's rows >= n, so that
-// nothing behind the segment's end enters a sum, whatever it holds.  `t` of
-// 256 threads.  LO: the rest K~ - bf16(K~) goes to the tile `lo`.
-template <int DK, int DV, bool LO, typename F>
-__device__ __forceinline__ void decay_scale_tile(uint8_t* kt, uint8_t* vt, uint8_t* lo, int n, int t, bool scale,
-                                                 F&& weight) {
-  constexpr int C = kDecayTcC, UNITS = C * DK / 8;
-  if (scale) {
-#pragma unroll 4
-    for (int i = 0; i < UNITS / 256; ++i) {
-      const int u = i * 256 + t, row = (u >> 3) & (C - 1);  // (a unit's place in its row does not matter here)
-      const float w = row < n ? weight(row) : 0.f;
-      uint4 x = *reinterpret_cast<const uint4*>(kt + u * 16);
-      uint32_t* xs = reinterpret_cast<uint32_t*>(&x);
-      uint4 l;
-      uint32_t* ls = reinterpret_cast<uint32_t*>(&l);
+// Scales the rows of a K tile (64-column blocks of C rows of 128 bytes) in
+// place by w[i], the weight of row (t >> 3) + 32 i, for thread t of 256.  LO:
+// the rest K~ - bf16(K~) goes to the tile `lo`.  (A unit's place in its row
+// does not matter here, so the swizzle is left alone.)
+template <int DK, bool LO>
+__device__ __forceinline__ void decay_scale_tile(uint8_t* kt, uint8_t* lo, int t, const float (&w)[4]) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float a = row < n ? __uint_as_float(xs[e] << 16) * w : 0.f;
-        const float b = row < n ? __uint_as_float(xs[e] & 0xffff0000u) * w : 0.f;
-        const uint32_t h = pack_bf16x2(a, b);
-        xs[e] = h;
-        if constexpr (LO) ls[e] = pack_bf16x2(a - __uint_as_float(h << 16), b - __uint_as_float(h & 0xffff0000u));
-      }
-      *reinterpret_cast<uint4*>(kt + u * 16) = x;
-      if constexpr (LO) *reinterpret_cast<uint4*>(lo + u * 16) = l;
+  for (int i = 0; i < DK / 16; ++i) {
+    const int u = i * 256 + t;
+    uint4 x = *reinterpret_cast<const uint4*>(kt + u * 16);
+    uint32_t* xs = reinterpret_cast<uint32_t*>(&x);
+    uint4 l;
+    uint32_t* ls = reinterpret_cast<uint32_t*>(&l);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float a = __uint_as_float(xs[e] << 16) * w[i & 3], b = __uint_as_float(xs[e] & 0xffff0000u) * w[i & 3];
+      xs[e] = pack_bf16x2(a, b);
+      if constexpr (LO)
+        ls[e] = pack_bf16x2(a - __uint_as_float(xs[e] << 16), b - __uint_as_float(xs[e] & 0xffff0000u));
     }
-  }
-  if (n < C) {
-    const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-    for (int u = t; u < C * DV / 8; u += 256)
-      if (((u >> 3) & (C - 1)) >= n) *reinterpret_cast<uint4*>(vt + u * 16) = z;
+    *reinterpret_cast<uint4*>(kt + u * 16) = x;
+    if constexpr (LO) *reinterpret_cast<uint4*>(lo + u * 16) = l;
   }
 }
+// Zeroes the rows >= n of a tile of D features: what is in memory behind a
+// segment's end, whatever it holds, then enters no sum.
+template <int D>
+__device__ __forceinline__ void decay_zero_rows(uint8_t* tile, int n, int t) {
+  const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll 1
+  for (int u = t; u < kDecayTcC * D / 8; u += 256)
+    if (((u >> 3) & (kDecayTcC - 1)) >= n) *reinterpret_cast<uint4*>(tile + u * 16) = z;
+}
 
+// try_wait that may suspend the thread for up to `hint_ns` instead of polling.
+__device__ __forceinline__ bool mbar_try_wait_hint(uint32_t addr, uint32_t parity, uint32_t hint_ns) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(addr), "r"(parity), "r"(hint_ns)
+      : "memory");
+  return ok != 0;
+}
+__device__ __noinline__ bool decay_wait_slow(uint32_t a, uint32_t parity, uint64_t lim) {
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_try_wait_hint(a, parity, 20000)) {
+    if (globaltimer_ns() - t0 > lim) {
+      record_timeout();
+      return false;
+    }
+  }
+  return true;
+}
 __device__ __forceinline__ bool decay_wait(bool& dead, uint64_t* bar, uint32_t parity, uint64_t lim) {
-  if (!dead) dead = !mbar_wait(bar, parity, lim);
+  if (!dead) {
+    const uint32_t a = smem_u32(bar);
+    if (!mbar_try_wait_hint(a, parity, 20000)) dead = !decay_wait_slow(a, parity, lim);
+  }
   return !dead;
 }
 // This warp's writes (and tensor memory reads) before one arrival for it.
@@ -251,8 +281,8 @@ __global__ void __launch_bounds__(320, 1) decay_tc_total_kernel(const __grid_con
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + NST * STAGE);
-  uint64_t *full = bars, *ready = bars + NST, *empty = bars + 2 * NST, *done = bars + 3 * NST;
-  uint32_t* holder = reinterpret_cast<uint32_t*>(bars + 3 * NST + 1);
+  uint64_t *full = bars, *ready = bars + NST, *empty = bars + 2 * NST, *dfull = bars + 3 * NST;  // (dfull: [2])
+  uint32_t* holder = reinterpret_cast<uint32_t*>(bars + 3 * NST + 2);
   int* sh = reinterpret_cast<int*>(holder + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -272,11 +302,12 @@ __global__ void __launch_bounds__(320, 1) decay_tc_total_kernel(const __grid_con
       mbar_init(&ready[i], 8);
       mbar_init(&empty[i], 1);
     }
-    mbar_init(done, 1);
+    mbar_init(&dfull[0], 1);
+    mbar_init(&dfull[1], 1);
     fence_mbar_init();
   }
   if (warp == 1) {
-    tmem_alloc(holder, DK);
+    tmem_alloc(holder, 2 * DK);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -310,35 +341,70 @@ __global__ void __launch_bounds__(320, 1) decay_tc_total_kernel(const __grid_con
         const uint32_t base = smem_u32(smem) + st * STAGE;
         const uint64_t dk = sdesc_sw128(base, C * 128, 1024), dv = sdesc_sw128(base + TK, C * 128, 1024);
         const uint64_t dl = sdesc_sw128(base + TK + TV, C * 128, 1024);
+        // (ready of tile i comes after tile i - 2's product was read out)
         decay_wait(dead, &ready[st], (i / NST) & 1, lim);
         tc_fence_after();
 #pragma unroll
-        for (int kk = 0; kk < C / 16; ++kk) mma_bf16_ss(tmem, dv + mn_step(kk), dk + mn_step(kk), ID, i > 0 || kk > 0);
+        for (int kk = 0; kk < C / 16; ++kk)
+          mma_bf16_ss(tmem + (i & 1) * DK, dv + mn_step(kk), dl + mn_step(kk), ID, kk > 0);
 #pragma unroll
-        for (int kk = 0; kk < C / 16; ++kk) mma_bf16_ss(tmem, dv + mn_step(kk), dl + mn_step(kk), ID, 1);
+        for (int kk = 0; kk < C / 16; ++kk) mma_bf16_ss(tmem + (i & 1) * DK, dv + mn_step(kk), dk + mn_step(kk), ID, 1);
         tc_commit(&empty[st]);
+        tc_commit(&dfull[i & 1]);
       }
-      tc_commit(done);
-      mbar_wait(done, 0, lim);
+      for (int i = max(0, nt - 2); i < nt; ++i) mbar_wait(&dfull[i & 1], (i >> 1) & 1, lim);
     }
   } else {
     bool dead = false;
-    const int t = static_cast<int>(threadIdx.x) - 64, w = warp - 2, quad = warp & 3, half = w >> 2;
+    const int t = static_cast<int>(threadIdx.x) - 64, quad = warp & 3, half = (warp - 2) >> 2;
     const float l = decay_log(A.log_decay, h);
+    // row weights inside a tile: distance to its end (reverse: to before its start)
+    float wgt[4], acc[NW];
+    auto weights = [&](int n) {
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int r = (t >> 3) + 32 * x;
+        wgt[x] = p.sU * expf(l * static_cast<float>(p.rev ? r + 1 : max(n - 1 - r, 0)));
+      }
+    };
+    weights(C);
+#pragma unroll
+    for (int e = 0; e < NW; ++e) acc[e] = 0.f;
+    // adds the i-th tile's product, weighted by the tile's distance
+    auto add = [&](int i) {
+      const int at = tile_at(i) * C, n = min(C, sp.len - at);
+      const float f = expf(l * static_cast<float>(p.rev ? at : sp.len - at - n));
+      decay_wait(dead, &dfull[i & 1], (i >> 1) & 1, lim);
+      __syncwarp();
+      tc_fence_after();
+      constexpr int PIECE = DV == 128 ? 16 : NW;
+#pragma unroll
+      for (int x = 0; x < NW; x += PIECE) {
+        uint32_t r[PIECE];
+        decay_state_ld<DK, DV>(tmem + (i & 1) * DK, quad, half, x, r);
+        tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < PIECE; ++e) acc[x + e] = fmaf(f, __uint_as_float(r[e]), acc[x + e]);
+      }
+    };
     for (int i = 0; i < nt; ++i) {
-      const int st = i % NST, at = tile_at(i) * C, n = min(C, sp.len - at);
-      // distance to where the contribution is taken: behind the last token, or (reverse) before the first
-      const int far = p.rev ? at + 1 : sp.len - 1 - at, step = p.rev ? 1 : -1;
+      const int st = i % NST, n = min(C, sp.len - tile_at(i) * C);
       decay_wait(dead, &full[st], (i / NST) & 1, lim);
       uint8_t* d = smem + st * STAGE;
-      decay_scale_tile<DK, DV, true>(d, d + TK, d + TK + TV, n, t, true,
-                                     [&](int r) { return p.sU * expf(l * static_cast<float>(far + step * r)); });
+      if (n < C) weights(n);
+      decay_scale_tile<DK, true>(d, d + TK + TV, t, wgt);
+      if (n < C) {
+        // (a thread zeroes the units that it scaled itself)
+        decay_zero_rows<DK>(d, n, t);
+        decay_zero_rows<DK>(d + TK + TV, n, t);
+        decay_zero_rows<DV>(d + TK, n, t);
+        weights(C);
+      }
       fence_async_smem();
       warp_arrive(&ready[st], lane);
+      if (i > 0) add(i - 1);
     }
-    decay_wait(dead, done, 0, lim);
-    __syncwarp();
-    tc_fence_after();
+    if (nt > 0) add(nt - 1);
     int row, col;
     decay_state_at<DK, DV>(quad, half, lane, row, col);
     const size_t dd = static_cast<size_t>(p.dk) * p.dv, off = static_cast<size_t>(row) * p.dk;
@@ -348,48 +414,32 @@ __global__ void __launch_bounds__(320, 1) decay_tc_total_kernel(const __grid_con
                          : p.ws + (static_cast<size_t>(s) * g.H + h) * dd) + off;
     const float* src = direct && p.s_in ? p.s_in + (static_cast<size_t>(sp.seq) * g.H + h) * dd + off : nullptr;
     const float gl = expf(l * static_cast<float>(sp.len));
-    constexpr int PIECE = NW < 32 ? NW : 32;
 #pragma unroll
-    for (int i = 0; i < NW / PIECE; ++i) {
-      uint32_t r[PIECE];
-      if (nt > 0) {
-        if (i == 0)
-          decay_state_ld<DK, DV, 0>(tmem, quad, half, r);
-        else
-          decay_state_ld<DK, DV, 1>(tmem, quad, half, r);
-        tmem_ld_wait();
-      } else {
-#pragma unroll
-        for (int e = 0; e < PIECE; ++e) r[e] = 0u;
+    for (int e = 0; e < NW; e += 4) {
+      const int c = col + e;
+      if (row >= p.dv || c >= p.dk) continue;
+      float4 x = make_float4(acc[e], acc[e + 1], acc[e + 2], acc[e + 3]);
+      if (src) {
+        const float4 y = *reinterpret_cast<const float4*>(src + c);
+        x.x = fmaf(gl, y.x, x.x);
+        x.y = fmaf(gl, y.y, x.y);
+        x.z = fmaf(gl, y.z, x.z);
+        x.w = fmaf(gl, y.w, x.w);
       }
-#pragma unroll
-      for (int e = 0; e < PIECE; e += 4) {
-        const int c = col + i * 32 + e;
-        if (row >= p.dv || c >= p.dk) continue;
-        float4 x = make_float4(__uint_as_float(r[e]), __uint_as_float(r[e + 1]), __uint_as_float(r[e + 2]),
-                               __uint_as_float(r[e + 3]));
-        if (src) {
-          const float4 y = *reinterpret_cast<const float4*>(src + c);
-          x.x = fmaf(gl, y.x, x.x);
-          x.y = fmaf(gl, y.y, x.y);
-          x.z = fmaf(gl, y.z, x.z);
-          x.w = fmaf(gl, y.w, x.w);
-        }
-        *reinterpret_cast<float4*>(dst + c) = x;
-      }
+      *reinterpret_cast<float4*>(dst + c) = x;
     }
     tc_fence_before();
   }
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, DK);
+    tmem_dealloc(tmem, 2 * DK);
   }
 }
 
 // ------------------------------------------------------------ outputs ----
 // One block per (segment, head, run), one per SM.  18 warps: 0 TMA loads, 1
-// MMA issue, 2-5 P, 6-9 outputs, 10-17 the state (and K~).  Order of the MMAs
+// MMA issue, 2-9 P and the outputs, 10-17 the state and K~.  Order of the MMAs
 // for tile c: O2, D, Sc of tile c+1 (as soon as it has landed), O1; Sc/O1 is
 // double-buffered in tensor memory, so that scores are ready when their P can
 // be written.
@@ -414,8 +464,8 @@ __global__ void __launch_bounds__(576, 1) decay_tc_out_kernel(const __grid_const
   uint64_t* ofree = sfull + 8;          // O1 and O2 read out
   uint64_t* drain = sfull + 9;
   float* colp = reinterpret_cast<float*>(bars + 2 * NST + 12);  // [32] gamma^(31-t), reverse gamma^t
-  float* gp = colp + 32;                                        // [32] gamma^t
-  uint32_t* holder = reinterpret_cast<uint32_t*>(gp + 32);
+  float* diag = colp + 32;                                      // [64] sP gamma^(x-31) at x >= 31
+  uint32_t* holder = reinterpret_cast<uint32_t*>(diag + 64);
   int* sh = reinterpret_cast<int*>(holder + 1);                 // [40]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -439,17 +489,18 @@ __global__ void __launch_bounds__(576, 1) decay_tc_out_kernel(const __grid_const
     mbar_init(&sfull[1], 1);
     mbar_init(kready, 8);
     mbar_init(qdone, 1);
-    mbar_init(pready, 4);
+    mbar_init(pready, 8);
     mbar_init(dfull, 1);
     mbar_init(wready, 8);
     mbar_init(ofull, 1);
-    mbar_init(ofree, 4);
+    mbar_init(ofree, 8);
     mbar_init(drain, 1);
     fence_mbar_init();
   }
   if (threadIdx.x < 32) {
-    gp[lane] = expf(l * static_cast<float>(lane));
     colp[lane] = expf(l * static_cast<float>(rev ? lane : 31 - lane));
+    diag[lane] = lane == 31 ? p.sP : 0.f;
+    diag[32 + lane] = p.sP * expf(l * static_cast<float>(lane + 1));
   }
   if (warp == 1) {
     tmem_alloc(holder, 512);
@@ -538,44 +589,55 @@ __global__ void __launch_bounds__(576, 1) decay_tc_out_kernel(const __grid_const
       tc_commit(drain);
       mbar_wait(drain, 0, lim);
     }
-  } else if (warp < 6) {
-    // ---------------------------------------------------------------- P --
+  } else if (warp < 10) {
+    // --------------------------------------------------- P and outputs --
+    // Warp (quad, half): rows 32 quad + lane; of P the columns 64 half + [0, 64),
+    // of the output DV / 2 columns from half DV / 2.
     bool dead = false;
-    const int quad = warp & 3, r = quad * 32 + lane;
+    const int quad = warp & 3, half = (warp - 2) >> 2, r = quad * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
+    // 32-column blocks between P's two halves of zeros and of weights: distance of rows and columns in blocks,
+    // and the row's power to the block's near edge
+    int dist[2];
+    float edge[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      dist[x] = rev ? 2 * half + x - quad : quad - 2 * half - x;
+      edge[x] = p.sP * expf(l * static_cast<float>(max(rev ? 32 * dist[x] - lane : lane + 32 * dist[x] - 31, 0)));
+    }
+    const float read_full = p.sR * expf(l * static_cast<float>(rev ? C - 1 - r : r + 1));
     for (int i = 0; i < nt; ++i) {
-      const int n = min(C, sp.len - tile_at(i));
+      const int at = tile_at(i), n = min(C, sp.len - at), y = sp.row0 + at;
       decay_wait(dead, &sfull[i & 1], (i >> 1) & 1, lim);
-      if (PSEP) {
-        if (i > 0) decay_wait(dead, ofull, (i - 1) & 1, lim);  // P of the tile before has been read
-      } else {
-        decay_wait(dead, qdone, i & 1, lim);
-      }
+      // (P beside the stages: the tile before has read it, as its ofull came)
+      if (!PSEP) decay_wait(dead, qdone, i & 1, lim);
       __syncwarp();
       tc_fence_after();
       const uint32_t tile = PSEP ? sbase + NST * STAGE + Cfg::WBF : sbase + (i % NST) * STAGE;
-      const uint32_t ts = tmem + (static_cast<uint32_t>(quad * 32) << 16) + (i & 1) * C;
-#pragma unroll 1
-      for (int jb = 0; jb < C / 32; ++jb) {
+      const uint32_t ts = tmem + lanes + (i & 1) * C + 64 * half;
+#pragma unroll
+      for (int b2 = 0; b2 < 2; ++b2) {
         uint32_t x[32];
-        const int j0 = jb * 32;
-        if (rev ? jb < quad : jb > quad) {
+        const int j0 = 64 * half + 32 * b2;
+        if (dist[b2] < 0) {
           if (PSEP && i > 0) continue;  // the zeros of the first tile are still there
 #pragma unroll
           for (int e = 0; e < 32; ++e) x[e] = 0u;
-          store_row32_bf16(tile, C * 128, r, j0, x);
-          continue;
-        }
-        tmem_ld32(ts + j0, x);
-        if (jb == quad) {
+        } else if (dist[b2] == 0) {
+          tmem_ld32(ts + 32 * b2, x);
           tmem_ld_wait();
+          if (rev) {
+            const float* w = diag + 31 - lane;
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const int d = rev ? e - lane : lane - e;
-            const float wgt = p.sP * gp[d & 31];
-            x[e] = d >= 0 ? __float_as_uint(wgt * __uint_as_float(x[e])) : 0u;
+            for (int e = 0; e < 32; ++e) x[e] = e >= lane ? __float_as_uint(w[e] * __uint_as_float(x[e])) : 0u;
+          } else {
+            const float* w = diag + 31 + lane;
+#pragma unroll
+            for (int e = 0; e < 32; ++e) x[e] = lane >= e ? __float_as_uint(w[-e] * __uint_as_float(x[e])) : 0u;
           }
         } else {
-          const float rp = p.sP * expf(l * static_cast<float>(rev ? j0 - r : r - j0 - 31));
+          tmem_ld32(ts + 32 * b2, x);
+          const float rp = edge[b2];
           tmem_ld_wait();
 #pragma unroll
           for (int e = 0; e < 32; e += 4) {
@@ -594,35 +656,30 @@ __global__ void __launch_bounds__(576, 1) decay_tc_out_kernel(const __grid_const
       }
       fence_async_smem();
       warp_arrive(pready, lane);
-    }
-  } else if (warp < 10) {
-    // ---------------------------------------------------------- outputs --
-    bool dead = false;
-    const int quad = warp & 3, r = quad * 32 + lane;
-    for (int i = 0; i < nt; ++i) {
-      const int at = tile_at(i), n = min(C, sp.len - at), y = sp.row0 + at;
-      const float rp = r < n ? p.sR * expf(l * static_cast<float>(rev ? n - 1 - r : r + 1)) : 0.f;
-      decay_wait(dead, ofull, i & 1, lim);
-      __syncwarp();
-      tc_fence_after();
-      const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
+
+      float rp = read_full;
+      if (rev && n < C) rp = r < n ? p.sR * expf(l * static_cast<float>(n - 1 - r)) : 0.f;
       const uint32_t stage = sbase + (i % NST) * STAGE + 2 * TK;
       // a tile that ends inside the tensor's rows is stored row by row: a box would reach the rows behind
       const bool whole = n == C || y + n == g.T;
-      __nv_bfloat16* out = p.op + static_cast<size_t>(sp.batch) * p.ob + static_cast<size_t>(h) * p.oh +
-                           static_cast<size_t>(y + r) * p.ot;
+      decay_wait(dead, ofull, i & 1, lim);
+      __syncwarp();
+      tc_fence_after();
 #pragma unroll
-      for (int c0 = 0; c0 < DV; c0 += 32) {
+      for (int x = 0; x < DV / 2; x += 32) {
+        const int c0 = half * (DV / 2) + x;
         uint32_t a[32], q[32];
         tmem_ld32(tmem + lanes + (i & 1) * C + c0, a);
         tmem_ld32(t_o2 + lanes + c0, q);
         tmem_ld_wait();
-        if (c0 + 32 == DV) warp_arrive(ofree, lane);
+        if (x + 32 == DV / 2) warp_arrive(ofree, lane);
 #pragma unroll
         for (int e = 0; e < 32; ++e) a[e] = __float_as_uint(fmaf(rp, __uint_as_float(q[e]), __uint_as_float(a[e])));
         if (whole) {
           store_row32_bf16(stage, C * 128, r, c0, a);
         } else if (r < n) {
+          __nv_bfloat16* out = p.op + static_cast<size_t>(sp.batch) * p.ob + static_cast<size_t>(h) * p.oh +
+                               static_cast<size_t>(y + r) * p.ot;
 #pragma unroll
           for (int e = 0; e < 32; e += 8)
             if (c0 + e < p.dv)
@@ -635,8 +692,8 @@ __global__ void __launch_bounds__(576, 1) decay_tc_out_kernel(const __grid_const
       }
       if (whole) {
         fence_async_smem();
-        asm volatile("bar.sync 1, 128;" ::: "memory");
-        if (threadIdx.x == 6 * 32) {
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        if (threadIdx.x == 2 * 32) {
 #pragma unroll
           for (int x = 0; x < DV / 64; ++x)
             tma_store_4d(&A.map[p.o], smem + (i % NST) * STAGE + 2 * TK + x * C * 128, x * 64, y, h, sp.batch);
@@ -644,11 +701,11 @@ __global__ void __launch_bounds__(576, 1) decay_tc_out_kernel(const __grid_const
           bulk_wait_read0();
           mbar_arrive(&empty[i % NST]);
         }
-      } else if (threadIdx.x == 6 * 32) {
+      } else if (threadIdx.x == 2 * 32) {
         mbar_arrive(&empty[i % NST]);
       }
     }
-    if (threadIdx.x == 6 * 32) bulk_wait0();
+    if (threadIdx.x == 2 * 32) bulk_wait0();
   } else {
     // ------------------------------------------------------------ state --
     bool dead = false;
@@ -690,6 +747,16 @@ __global__ void __launch_bounds__(576, 1) decay_tc_out_kernel(const __grid_const
       warp_arrive(wready, lane);
     };
     put_w();
+    float wgt[4];
+    auto weights = [&](int n) {
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int r = (t >> 3) + 32 * x;
+        wgt[x] = p.sU * expf(l * static_cast<float>(rev ? r + 1 : max(n - 1 - r, 0)));
+      }
+    };
+    weights(C);
+    const float g_full = expf(l * static_cast<float>(C));
     for (int i = 0; i < nt; ++i) {
       const int st = i % NST, n = min(C, sp.len - tile_at(i));
       const bool more = i + 1 < nt;
@@ -697,27 +764,32 @@ __global__ void __launch_bounds__(576, 1) decay_tc_out_kernel(const __grid_const
       decay_wait(dead, &sfull[i & 1], (i >> 1) & 1, lim);  // K has been read for the scores
       __syncwarp();
       uint8_t* d = smem + st * STAGE;
-      decay_scale_tile<DK, DV, false>(d + TK, d + 2 * TK, nullptr, n, t, more, [&](int x) {
-        return p.sU * expf(l * static_cast<float>(rev ? x + 1 : n - 1 - x));
-      });
+      float gn = g_full;
+      if (n < C) {
+        weights(n);
+        gn = expf(l * static_cast<float>(n));
+      }
+      if (more) decay_scale_tile<DK, false>(d + TK, nullptr, t, wgt);
+      if (n < C) {
+        // (a thread zeroes the units that it scaled itself)
+        decay_zero_rows<DK>(d + TK, n, t);
+        decay_zero_rows<DV>(d + 2 * TK, n, t);
+        weights(C);
+      }
       fence_async_smem();
       warp_arrive(kready, lane);
       if (!more) break;
-      const float gn = expf(l * static_cast<float>(n));
       decay_wait(dead, dfull, i & 1, lim);
       __syncwarp();
       tc_fence_after();
-      constexpr int PIECE = NW < 32 ? NW : 32;
+      constexpr int PIECE = DV == 128 ? 16 : NW;
 #pragma unroll
-      for (int x = 0; x < NW / PIECE; ++x) {
+      for (int x = 0; x < NW; x += PIECE) {
         uint32_t y[PIECE];
-        if (x == 0)
-          decay_state_ld<DK, DV, 0>(t_d, quad, half, y);
-        else
-          decay_state_ld<DK, DV, 1>(t_d, quad, half, y);
+        decay_state_ld<DK, DV>(t_d, quad, half, x, y);
         tmem_ld_wait();
 #pragma unroll
-        for (int e = 0; e < PIECE; ++e) w[x * PIECE + e] = fmaf(gn, w[x * PIECE + e], __uint_as_float(y[e]));
+        for (int e = 0; e < PIECE; ++e) w[x + e] = fmaf(gn, w[x + e], __uint_as_float(y[e]));
       }
       decay_wait(dead, qdone, i & 1, lim);  // Wbf has been read
       __syncwarp();
