@@ -32,6 +32,7 @@
 // waiting but keeps arriving, so that the block drains and exits.
 #pragma once
 #include "chunked_tc.cuh"
+#include "chunked_tc_mom.cuh"
 #include "common.cuh"
 #include "decay.cuh"
 
@@ -154,19 +155,16 @@ struct DecayTcCfg {
   static constexpr int C = kDecayTcC;
   static constexpr int TK = C * DK * 2, TV = C * DV * 2;   // bytes of a tile
   static constexpr int STAGE = 2 * TK + TV;                // Q, K, V
-  static constexpr bool PSEP = DK == 64;                   // P beside the stages; else over Q once Sc and O2 have read it
-  static constexpr int PB = PSEP ? C * C * 2 : 0;
   static constexpr int WBF = DK * DV * 2;
-  static constexpr int NST = (DK == 64 && DV == 64) ? 3 : 2;
-  static constexpr int BIG = NST * STAGE + WBF + PB;
+  static constexpr int NST = (232448 - 2048 - WBF) / STAGE > 4 ? 4 : (232448 - 2048 - WBF) / STAGE;
+  static constexpr int BIG = NST * STAGE + WBF;
   static constexpr int SMEM = BIG + 1024 + 1024;           // + barriers and tables, + alignment
   static constexpr int THREADS = 576;                      // TMA, MMA, 8 warps P and outputs, 8 warps state
   static constexpr int NW = DK * DV / 256;                 // elements of X per state thread
-  // tensor memory: Sc (then O1) twice, O2, D
-  static constexpr int T_O2 = 2 * C, T_D = 2 * C + DV;
-  static_assert(T_D + DK <= 512, "tensor memory");
-  static_assert(SMEM <= 232448, "shared memory");
-  static_assert(!PSEP ? C * C * 2 <= TK : true, "P over Q");
+  // tensor memory: Sc (P over it; twice where it fits), O1, O2, D
+  static constexpr int NSB = 4 * C + DK <= 512 && DV == 64 ? 2 : 1;
+  static constexpr int T_O1 = NSB * C, T_O2 = T_O1 + DV, T_D = T_O2 + DV;
+  static_assert(NST >= 2 && T_D + DK <= 512, "shared and tensor memory");
   // total kernel: K (then hi), V, lo per stage
   static constexpr int A_STAGE = 2 * TK + TV;
   static constexpr int A_NST = (DK == 64 && DV == 64) ? 4 : 2;
@@ -440,30 +438,37 @@ __global__ void __launch_bounds__(320, 1) decay_tc_total_kernel(const __grid_con
 // ------------------------------------------------------------ outputs ----
 // One block per (segment, head, run), one per SM.  18 warps: 0 TMA loads, 1
 // MMA issue, 2-9 P and the outputs, 10-17 the state and K~.  Order of the MMAs
-// for tile c: O2, D, Sc of tile c+1 (as soon as it has landed), O1; Sc/O1 is
-// double-buffered in tensor memory, so that scores are ready when their P can
-// be written.
+// for tile i: O2, D, O1, and Sc of tile i + 1: after O1 where P's columns are
+// the only score columns (P lies over the scores, as the MMA's operand in
+// tensor memory), before it where there are two.  Q and K are free once D is
+// done, V once the output, staged over it, has been stored.
+//
+// Shared memory is the next bound after HBM: an MMA reads both operands of 128
+// bytes a clock, so a tile of 128 x 128 x 128 moves about 500 KB through it;
+// P in tensor memory saves 64 KB of that.
 template <int DK, int DV>
 __global__ void __launch_bounds__(576, 1) decay_tc_out_kernel(const __grid_constant__ DecayTcArgs A) {
   using Cfg = DecayTcCfg<DK, DV>;
   constexpr int C = Cfg::C, NST = Cfg::NST, STAGE = Cfg::STAGE, TK = Cfg::TK, TV = Cfg::TV, NW = Cfg::NW;
-  constexpr bool PSEP = Cfg::PSEP;
+  constexpr int NSB = Cfg::NSB;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t sbase = smem_u32(smem);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Cfg::BIG);
-  uint64_t* full = bars;                // [NST] tile landed
-  uint64_t* empty = bars + NST;         // [NST] stage free: its output has left
-  uint64_t* sfull = bars + 2 * NST;     // [2] scores complete
+  uint64_t* full = bars;                // [NST] Q and K landed
+  uint64_t* fullv = bars + NST;         // [NST] V landed
+  uint64_t* free_qk = bars + 2 * NST;   // [NST] Q and K read for the last time
+  uint64_t* empty = bars + 3 * NST;     // [NST] V's slot free: the output has left
+  uint64_t* sfull = bars + 4 * NST;     // [2] scores complete
   uint64_t* kready = sfull + 2;         // K~ written, rows past the end zeroed; D of the tile before read out
   uint64_t* qdone = sfull + 3;          // O2 complete: Q and Wbf have been read
-  uint64_t* pready = sfull + 4;         // P written, scores read out
+  uint64_t* pready = sfull + 4;         // P written over the scores
   uint64_t* dfull = sfull + 5;          // D complete
   uint64_t* wready = sfull + 6;         // Wbf written
   uint64_t* ofull = sfull + 7;          // O1 complete (and everything before it)
   uint64_t* ofree = sfull + 8;          // O1 and O2 read out
   uint64_t* drain = sfull + 9;
-  float* colp = reinterpret_cast<float*>(bars + 2 * NST + 12);  // [32] gamma^(31-t), reverse gamma^t
+  float* colp = reinterpret_cast<float*>(bars + 4 * NST + 12);  // [32] gamma^(31-t), reverse gamma^t
   float* diag = colp + 32;                                      // [64] sP gamma^(x-31) at x >= 31
   uint32_t* holder = reinterpret_cast<uint32_t*>(diag + 64);
   int* sh = reinterpret_cast<int*>(holder + 1);                 // [40]
@@ -483,6 +488,8 @@ __global__ void __launch_bounds__(576, 1) decay_tc_out_kernel(const __grid_const
   if (threadIdx.x == 0) {
     for (int i = 0; i < NST; ++i) {
       mbar_init(&full[i], 1);
+      mbar_init(&fullv[i], 1);
+      mbar_init(&free_qk[i], 1);
       mbar_init(&empty[i], 1);
     }
     mbar_init(&sfull[0], 1);
@@ -510,7 +517,7 @@ __global__ void __launch_bounds__(576, 1) decay_tc_out_kernel(const __grid_const
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *holder;
-  const uint32_t t_o2 = tmem + Cfg::T_O2, t_d = tmem + Cfg::T_D;
+  const uint32_t t_o1 = tmem + Cfg::T_O1, t_o2 = tmem + Cfg::T_O2, t_d = tmem + Cfg::T_D;
 
   if (warp == 0) {
     // ------------------------------------------------------------ loads --
@@ -519,19 +526,24 @@ __global__ void __launch_bounds__(576, 1) decay_tc_out_kernel(const __grid_const
       const uint64_t pol = l2_policy_evict_first();
       for (int i = 0; i < nt; ++i) {
         const int st = i % NST, y = sp.row0 + tile_at(i);
-        if (i >= NST) decay_wait(dead, &empty[st], (i / NST - 1) & 1, lim);
-        mbar_arrive_expect_tx(&full[st], 2 * TK + TV);
         uint8_t* d = smem + st * STAGE;
+        if (i >= NST) decay_wait(dead, &free_qk[st], (i / NST - 1) & 1, lim);
+        mbar_arrive_expect_tx(&full[st], 2 * TK);
 #pragma unroll
         for (int x = 0; x < DK / 64; ++x) {
           tma_load_4d(&A.map[p.q], &full[st], d + x * C * 128, x * 64, y, h, sp.batch, pol);
           tma_load_4d(&A.map[p.k], &full[st], d + TK + x * C * 128, x * 64, y, h, sp.batch, pol);
         }
+        if (i >= NST) decay_wait(dead, &empty[st], (i / NST - 1) & 1, lim);
+        mbar_arrive_expect_tx(&fullv[st], TV);
 #pragma unroll
         for (int x = 0; x < DV / 64; ++x)
-          tma_load_4d(&A.map[p.v], &full[st], d + 2 * TK + x * C * 128, x * 64, y, h, sp.batch, pol);
+          tma_load_4d(&A.map[p.v], &fullv[st], d + 2 * TK + x * C * 128, x * 64, y, h, sp.batch, pol);
       }
-      for (int i = max(0, nt - NST); i < nt; ++i) mbar_wait(&full[i % NST], (i / NST) & 1, lim);
+      for (int i = max(0, nt - NST); i < nt; ++i) {
+        mbar_wait(&full[i % NST], (i / NST) & 1, lim);
+        mbar_wait(&fullv[i % NST], (i / NST) & 1, lim);
+      }
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------- MMAs --
@@ -540,14 +552,13 @@ __global__ void __launch_bounds__(576, 1) decay_tc_out_kernel(const __grid_const
       constexpr uint32_t ID_S = idesc_bf16_f32(C, C, false, false), ID_Q = idesc_bf16_f32(C, DV, false, false);
       constexpr uint32_t ID_D = idesc_bf16_f32(DV, DK, true, true), ID_P = idesc_bf16_f32(C, DV, false, true);
       const uint64_t d_w = sdesc_sw128(sbase + NST * STAGE, 16, 1024);
-      const uint64_t d_psep = sdesc_sw128(sbase + NST * STAGE + Cfg::WBF, 16, 1024);
       auto scores = [&](int i) {  // its tile has landed
         const uint32_t base = sbase + (i % NST) * STAGE;
         const uint64_t dq = sdesc_sw128(base, 16, 1024), dk = sdesc_sw128(base + TK, 16, 1024);
         tc_fence_after();
 #pragma unroll
         for (int kk = 0; kk < DK / 16; ++kk)
-          mma_bf16_ss(tmem + (i & 1) * C, dq + k_step(C, kk), dk + k_step(C, kk), ID_S, kk > 0);
+          mma_bf16_ss(tmem + (i % NSB) * C, dq + k_step(C, kk), dk + k_step(C, kk), ID_S, kk > 0);
         tc_commit(&sfull[i & 1]);
       };
       decay_wait(dead, &full[0], 0, lim);
@@ -564,22 +575,26 @@ __global__ void __launch_bounds__(576, 1) decay_tc_out_kernel(const __grid_const
           mma_bf16_ss(t_o2, dq + k_step(C, kk), d_w + k_step(DV, kk), ID_Q, kk > 0);
         tc_commit(qdone);
         decay_wait(dead, kready, par, lim);
+        decay_wait(dead, &fullv[i % NST], (i / NST) & 1, lim);
         tc_fence_after();
         if (i + 1 < nt) {
 #pragma unroll
           for (int kk = 0; kk < C / 16; ++kk) mma_bf16_ss(t_d, dvm + mn_step(kk), dkm + mn_step(kk), ID_D, kk > 0);
           tc_commit(dfull);
+          tc_commit(&free_qk[i % NST]);
         }
-        // (the other score buffer was read out when ofree of tile i - 1 came)
         const int j = i + 1;
-        bool ahead = j < nt && !dead && mbar_try_wait(smem_u32(&full[j % NST]), (j / NST) & 1);
-        if (ahead) scores(j);
+        bool ahead = false;
+        if (NSB == 2) {  // (the other score columns were last P of tile i - 1, whose O1 is done)
+          ahead = j < nt && !dead && mbar_try_wait(smem_u32(&full[j % NST]), (j / NST) & 1);
+          if (ahead) scores(j);
+        }
         decay_wait(dead, pready, par, lim);
         tc_fence_after();
-        const uint64_t dp = PSEP ? d_psep : dq;
+        const uint32_t t_p = tmem + (i % NSB) * C;
 #pragma unroll
         for (int kk = 0; kk < C / 16; ++kk)
-          mma_bf16_ss(tmem + par * C, dp + k_step(C, kk), dvm + mn_step(kk), ID_P, kk > 0);
+          mma_bf16_ts(t_o1, t_p + (kk >> 2) * 64 + (kk & 3) * 8, dvm + mn_step(kk), ID_P, kk > 0);
         tc_commit(ofull);
         if (j < nt && !ahead) {
           decay_wait(dead, &full[j % NST], (j / NST) & 1, lim);
@@ -609,18 +624,14 @@ __global__ void __launch_bounds__(576, 1) decay_tc_out_kernel(const __grid_const
     for (int i = 0; i < nt; ++i) {
       const int at = tile_at(i), n = min(C, sp.len - at), y = sp.row0 + at;
       decay_wait(dead, &sfull[i & 1], (i >> 1) & 1, lim);
-      // (P beside the stages: the tile before has read it, as its ofull came)
-      if (!PSEP) decay_wait(dead, qdone, i & 1, lim);
       __syncwarp();
       tc_fence_after();
-      const uint32_t tile = PSEP ? sbase + NST * STAGE + Cfg::WBF : sbase + (i % NST) * STAGE;
-      const uint32_t ts = tmem + lanes + (i & 1) * C + 64 * half;
+      const uint32_t ts = tmem + lanes + (i % NSB) * C + 64 * half;
 #pragma unroll
       for (int b2 = 0; b2 < 2; ++b2) {
         uint32_t x[32];
         const int j0 = 64 * half + 32 * b2;
         if (dist[b2] < 0) {
-          if (PSEP && i > 0) continue;  // the zeros of the first tile are still there
 #pragma unroll
           for (int e = 0; e < 32; ++e) x[e] = 0u;
         } else if (dist[b2] == 0) {
@@ -652,9 +663,13 @@ __global__ void __launch_bounds__(576, 1) decay_tc_out_kernel(const __grid_const
 #pragma unroll
           for (int e = 0; e < 32; ++e) x[e] = j0 + e < n ? x[e] : 0u;
         }
-        store_row32_bf16(tile, C * 128, r, j0, x);
+        // over this warp's own score columns: those of the block before have been read
+        uint32_t pk[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) pk[e] = pack_bf16x2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
+        tmem_st16(ts + 16 * b2, pk);
       }
-      fence_async_smem();
+      tmem_st_wait();
       warp_arrive(pready, lane);
 
       float rp = read_full;
@@ -669,7 +684,7 @@ __global__ void __launch_bounds__(576, 1) decay_tc_out_kernel(const __grid_const
       for (int x = 0; x < DV / 2; x += 32) {
         const int c0 = half * (DV / 2) + x;
         uint32_t a[32], q[32];
-        tmem_ld32(tmem + lanes + (i & 1) * C + c0, a);
+        tmem_ld32(t_o1 + lanes + c0, a);
         tmem_ld32(t_o2 + lanes + c0, q);
         tmem_ld_wait();
         if (x + 32 == DV / 2) warp_arrive(ofree, lane);
@@ -761,6 +776,7 @@ __global__ void __launch_bounds__(576, 1) decay_tc_out_kernel(const __grid_const
       const int st = i % NST, n = min(C, sp.len - tile_at(i));
       const bool more = i + 1 < nt;
       decay_wait(dead, &full[st], (i / NST) & 1, lim);
+      if (n < C) decay_wait(dead, &fullv[st], (i / NST) & 1, lim);
       decay_wait(dead, &sfull[i & 1], (i >> 1) & 1, lim);  // K has been read for the scores
       __syncwarp();
       uint8_t* d = smem + st * STAGE;
