@@ -164,6 +164,7 @@ struct DecayTcCfg {
   // tensor memory: Sc (P over it; twice where it fits), O1, O2, D
   static constexpr int NSB = 4 * C + DK <= 512 && DV == 64 ? 2 : 1;
   static constexpr int T_O1 = NSB * C, T_O2 = T_O1 + DV, T_D = T_O2 + DV;
+  static_assert(DV * (DK + 4) * 4 <= STAGE, "the start state's buffer");
   static_assert(NST >= 2 && T_D + DK <= 512, "shared and tensor memory");
   // total kernel: K (then hi), V, lo per stage
   static constexpr int A_STAGE = 2 * TK + TV;
@@ -254,6 +255,38 @@ __device__ __noinline__ bool decay_wait_slow(uint32_t a, uint32_t parity, uint64
   }
   return true;
 }
+// The start state into registers through shared memory: 256 threads read whole
+// rows (a thread's own row would be a line of its own in each load: measured
+// 7 us for 128 x 128 where this takes 1), `buf` holds [DV][DK + 4] floats.
+template <int DK, int DV, int NW>
+__device__ __forceinline__ void decay_state_in(float* buf, const float* src, bool transposed, int dk, int dv, int t,
+                                               int row, int col, float (&w)[NW]) {
+  constexpr int LD = DK + 4;
+  const int wp = t >> 5, lane = t & 31;
+  if (transposed) {  // [dk][dv]
+#pragma unroll 4
+    for (int c = wp; c < DK; c += 8)
+#pragma unroll
+      for (int v = 0; v < DV; v += 32)
+        buf[(v + lane) * LD + c] = c < dk && v + lane < dv ? __ldcg(src + static_cast<size_t>(c) * dv + v + lane) : 0.f;
+  } else {
+    constexpr int PER = 128 / DK;  // rows a warp reads at once
+    const int c = (lane % (DK / 4)) * 4;
+#pragma unroll 8
+    for (int r = wp * PER + lane / (DK / 4); r < DV; r += 8 * PER) {
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (r < dv && c < dk) x = __ldcg(reinterpret_cast<const float4*>(src + static_cast<size_t>(r) * dk + c));
+      *reinterpret_cast<float4*>(buf + r * LD + c) = x;
+    }
+  }
+  asm volatile("bar.sync 2, 256;" ::: "memory");
+#pragma unroll
+  for (int e = 0; e < NW; e += 4) {
+    const float4 x = *reinterpret_cast<const float4*>(buf + row * LD + col + e);
+    w[e] = x.x, w[e + 1] = x.y, w[e + 2] = x.z, w[e + 3] = x.w;
+  }
+}
+
 __device__ __forceinline__ bool decay_wait(bool& dead, uint64_t* bar, uint32_t parity, uint64_t lim) {
   if (!dead) {
     const uint32_t a = smem_u32(bar);
@@ -468,6 +501,7 @@ __global__ void __launch_bounds__(576, 1) decay_tc_out_kernel(const __grid_const
   uint64_t* ofull = sfull + 7;          // O1 complete (and everything before it)
   uint64_t* ofree = sfull + 8;          // O1 and O2 read out
   uint64_t* drain = sfull + 9;
+  uint64_t* sread = sfull + 10;         // start state read: the last stage, its buffer, is free
   float* colp = reinterpret_cast<float*>(bars + 4 * NST + 12);  // [32] gamma^(31-t), reverse gamma^t
   float* diag = colp + 32;                                      // [64] sP gamma^(x-31) at x >= 31
   uint32_t* holder = reinterpret_cast<uint32_t*>(diag + 64);
@@ -502,6 +536,7 @@ __global__ void __launch_bounds__(576, 1) decay_tc_out_kernel(const __grid_const
     mbar_init(ofull, 1);
     mbar_init(ofree, 8);
     mbar_init(drain, 1);
+    mbar_init(sread, 8);
     fence_mbar_init();
   }
   if (threadIdx.x < 32) {
@@ -528,6 +563,7 @@ __global__ void __launch_bounds__(576, 1) decay_tc_out_kernel(const __grid_const
         const int st = i % NST, y = sp.row0 + tile_at(i);
         uint8_t* d = smem + st * STAGE;
         if (i >= NST) decay_wait(dead, &free_qk[st], (i / NST - 1) & 1, lim);
+        if (i == NST - 1) decay_wait(dead, sread, 0, lim);
         mbar_arrive_expect_tx(&full[st], 2 * TK);
 #pragma unroll
         for (int x = 0; x < DK / 64; ++x) {
@@ -734,22 +770,14 @@ __global__ void __launch_bounds__(576, 1) decay_tc_out_kernel(const __grid_const
       const float* src = via ? p.ws + (static_cast<size_t>(s) * g.H + h) * dd
                              : p.s_in ? p.s_in + (static_cast<size_t>(sp.seq) * g.H + h) * dd : nullptr;
       const bool tr = via ? p.ws_t != 0 : p.s_in_t != 0;
+      if (src) {
+        decay_state_in<DK, DV>(reinterpret_cast<float*>(smem + (NST - 1) * STAGE), src, tr, p.dk, p.dv, t, row, col, w);
+      } else {
 #pragma unroll
-      for (int e = 0; e < NW; ++e) w[e] = 0.f;
-      if (src && row < p.dv) {
-        if (tr) {
-#pragma unroll
-          for (int e = 0; e < NW; ++e)
-            if (col + e < p.dk) w[e] = __ldcg(src + static_cast<size_t>(col + e) * p.dv + row);
-        } else {
-#pragma unroll
-          for (int e = 0; e < NW; e += 4)
-            if (col + e < p.dk) {
-              const float4 x = __ldcg(reinterpret_cast<const float4*>(src + static_cast<size_t>(row) * p.dk + col + e));
-              w[e] = x.x, w[e + 1] = x.y, w[e + 2] = x.z, w[e + 3] = x.w;
-            }
-        }
+        for (int e = 0; e < NW; ++e) w[e] = 0.f;
       }
+      fence_async_smem();
+      warp_arrive(sread, lane);
     }
     const uint32_t wtile = sbase + NST * STAGE;
     auto put_w = [&]() {
