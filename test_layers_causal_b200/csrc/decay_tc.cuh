@@ -29,7 +29,8 @@
 // overflows however strong the decay: an underflow is a weight below 2^-126.
 //
 // Waits are bounded as in chunked_tc.cuh: a thread whose wait runs out stops
-// waiting but keeps arriving, so that the block drains and exits.
+// waiting, and issues no more copies or MMAs, but keeps arriving, so that the
+// block drains and exits with nothing of its own in flight.
 #pragma once
 #include "chunked_tc.cuh"
 #include "chunked_tc_mom.cuh"
@@ -68,6 +69,34 @@ __device__ __forceinline__ void tmem_ld_half16(uint32_t taddr, uint32_t (&r)[16]
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
 }
+
+// Two fp32 operations in one instruction.
+struct f2 {
+  unsigned long long v;
+};
+__device__ __forceinline__ f2 pair(float lo, float hi) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ f2 pair(uint32_t lo, uint32_t hi) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "r"(lo), "r"(hi));
+  return r;
+}
+__device__ __forceinline__ float lo_of(f2 x) { return __uint_as_float(static_cast<uint32_t>(x.v)); }
+__device__ __forceinline__ float hi_of(f2 x) { return __uint_as_float(static_cast<uint32_t>(x.v >> 32)); }
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_bf16x2(f2 x) { return pack_bf16x2(lo_of(x), hi_of(x)); }
 
 constexpr int kDecayTcC = 128;      // tokens per tile
 constexpr int kDecayTcRuns = 3;     // the most runs in one launch
@@ -159,17 +188,17 @@ struct DecayTcCfg {
   static constexpr int NST = (232448 - 2048 - WBF) / STAGE > 4 ? 4 : (232448 - 2048 - WBF) / STAGE;
   static constexpr int BIG = NST * STAGE + WBF;
   static constexpr int SMEM = BIG + 1024 + 1024;           // + barriers and tables, + alignment
-  static constexpr int THREADS = 576;                      // TMA, MMA, 8 warps P and outputs, 8 warps state
+  static constexpr int THREADS = 608;                      // TMA, MMA, 8 warps P and outputs, 8 warps state, MMA
   static constexpr int NW = DK * DV / 256;                 // elements of X per state thread
   // tensor memory: Sc (P over it; twice where it fits), O1, O2, D
-  static constexpr int NSB = 4 * C + DK <= 512 && DV == 64 ? 2 : 1;
+  static constexpr int NSB = DV == 64 ? 2 : 1;
   static constexpr int T_O1 = NSB * C, T_O2 = T_O1 + DV, T_D = T_O2 + DV;
   static_assert(DV * (DK + 4) * 4 <= STAGE, "the start state's buffer");
   static_assert(NST >= 2 && T_D + DK <= 512, "shared and tensor memory");
-  // total kernel: K (then hi), V, lo per stage
-  static constexpr int A_STAGE = 2 * TK + TV;
-  static constexpr int A_NST = (DK == 64 && DV == 64) ? 4 : 2;
-  static constexpr int A_SMEM = A_NST * A_STAGE + 1024 + 1024;
+  // total kernel: K (then hi) and V per stage, one lo
+  static constexpr int A_STAGE = TK + TV;
+  static constexpr int A_NST = (232448 - 2048 - TK) / A_STAGE > 6 ? 6 : (232448 - 2048 - TK) / A_STAGE;
+  static constexpr int A_SMEM = A_NST * A_STAGE + TK + 1024 + 1024;
   static constexpr int A_THREADS = 320;                    // TMA, MMA, 8 warps
   static_assert(A_SMEM <= 232448, "shared memory");
 };
@@ -214,12 +243,13 @@ __device__ __forceinline__ void decay_scale_tile(uint8_t* kt, uint8_t* lo, int t
     uint32_t* xs = reinterpret_cast<uint32_t*>(&x);
     uint4 l;
     uint32_t* ls = reinterpret_cast<uint32_t*>(&l);
+    const f2 wt = pair(w[i & 3], w[i & 3]);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const float a = __uint_as_float(xs[e] << 16) * w[i & 3], b = __uint_as_float(xs[e] & 0xffff0000u) * w[i & 3];
-      xs[e] = pack_bf16x2(a, b);
+      const f2 y = mul2(pair(xs[e] << 16, xs[e] & 0xffff0000u), wt);
+      xs[e] = pack_bf16x2(y);
       if constexpr (LO)
-        ls[e] = pack_bf16x2(a - __uint_as_float(xs[e] << 16), b - __uint_as_float(xs[e] & 0xffff0000u));
+        ls[e] = pack_bf16x2(lo_of(y) - __uint_as_float(xs[e] << 16), hi_of(y) - __uint_as_float(xs[e] & 0xffff0000u));
     }
     *reinterpret_cast<uint4*>(kt + u * 16) = x;
     if constexpr (LO) *reinterpret_cast<uint4*>(lo + u * 16) = l;
@@ -244,16 +274,6 @@ __device__ __forceinline__ bool mbar_try_wait_hint(uint32_t addr, uint32_t parit
       : "r"(addr), "r"(parity), "r"(hint_ns)
       : "memory");
   return ok != 0;
-}
-__device__ __noinline__ bool decay_wait_slow(uint32_t a, uint32_t parity, uint64_t lim) {
-  const uint64_t t0 = globaltimer_ns();
-  while (!mbar_try_wait_hint(a, parity, 20000)) {
-    if (globaltimer_ns() - t0 > lim) {
-      record_timeout();
-      return false;
-    }
-  }
-  return true;
 }
 // The start state into registers through shared memory: 256 threads read whole
 // rows (a thread's own row would be a line of its own in each load: measured
@@ -287,12 +307,20 @@ __device__ __forceinline__ void decay_state_in(float* buf, const float* src, boo
   }
 }
 
-__device__ __forceinline__ bool decay_wait(bool& dead, uint64_t* bar, uint32_t parity, uint64_t lim) {
-  if (!dead) {
-    const uint32_t a = smem_u32(bar);
-    if (!mbar_try_wait_hint(a, parity, 20000)) dead = !decay_wait_slow(a, parity, lim);
+// mbar_wait with suspending tries; nothing once `dead`.
+__device__ __forceinline__ void decay_wait(bool& dead, uint64_t* bar, uint32_t parity, uint64_t lim) {
+  if (dead) return;
+  const uint32_t a = smem_u32(bar);
+  if (mbar_try_wait_hint(a, parity, 20000)) return;
+  const uint64_t t0 = globaltimer_ns();
+#pragma unroll 1
+  while (!mbar_try_wait_hint(a, parity, 20000)) {
+    if (globaltimer_ns() - t0 > lim) {
+      atomicMax(&g_status, kStatusTimeout);
+      dead = true;
+      return;
+    }
   }
-  return !dead;
 }
 // This warp's writes (and tensor memory reads) before one arrival for it.
 __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
@@ -311,9 +339,15 @@ __global__ void __launch_bounds__(320, 1) decay_tc_total_kernel(const __grid_con
   constexpr int C = Cfg::C, NST = Cfg::A_NST, STAGE = Cfg::A_STAGE, TK = Cfg::TK, TV = Cfg::TV, NW = Cfg::NW;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + NST * STAGE);
-  uint64_t *full = bars, *ready = bars + NST, *empty = bars + 2 * NST, *dfull = bars + 3 * NST;  // (dfull: [2])
-  uint32_t* holder = reinterpret_cast<uint32_t*>(bars + 3 * NST + 2);
+  uint8_t* lo = smem + NST * STAGE;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(lo + TK);
+  uint64_t* full = bars;               // [NST] tile landed
+  uint64_t* ready = bars + NST;        // [NST] K~ written; the product two tiles before read out
+  uint64_t* empty = bars + 2 * NST;    // [NST] stage read
+  uint64_t* dfull = bars + 3 * NST;    // [2] product complete
+  uint64_t* lofree = dfull + 2;        // lo read
+  uint64_t* drain = dfull + 3;
+  uint32_t* holder = reinterpret_cast<uint32_t*>(drain + 1);
   int* sh = reinterpret_cast<int*>(holder + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -335,6 +369,8 @@ __global__ void __launch_bounds__(320, 1) decay_tc_total_kernel(const __grid_con
     }
     mbar_init(&dfull[0], 1);
     mbar_init(&dfull[1], 1);
+    mbar_init(lofree, 1);
+    mbar_init(drain, 1);
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -349,10 +385,12 @@ __global__ void __launch_bounds__(320, 1) decay_tc_total_kernel(const __grid_con
   if (warp == 0) {
     if (lane == 0) {
       bool dead = false;
+      int sent = 0;
       const uint64_t pol = l2_policy_evict_last();
       for (int i = 0; i < nt; ++i) {
         const int st = i % NST, y = sp.row0 + tile_at(i) * C;
         if (i >= NST) decay_wait(dead, &empty[st], (i / NST - 1) & 1, lim);
+        if (dead) break;
         mbar_arrive_expect_tx(&full[st], TK + TV);
         uint8_t* d = smem + st * STAGE;
 #pragma unroll
@@ -360,30 +398,36 @@ __global__ void __launch_bounds__(320, 1) decay_tc_total_kernel(const __grid_con
 #pragma unroll
         for (int x = 0; x < DV / 64; ++x)
           tma_load_4d(&A.map[p.v], &full[st], d + TK + x * C * 128, x * 64, y, h, sp.batch, pol);
+        sent = i + 1;
       }
-      for (int i = max(0, nt - NST); i < nt; ++i) mbar_wait(&full[i % NST], (i / NST) & 1, lim);
+      for (int i = max(0, sent - NST); i < sent; ++i) mbar_wait(&full[i % NST], (i / NST) & 1, lim);
     }
   } else if (warp == 1) {
     if (lane == 0) {
       bool dead = false;
       constexpr uint32_t ID = idesc_bf16_f32(DV, DK, true, true);
+      const uint64_t dl = sdesc_sw128(smem_u32(lo), C * 128, 1024);
       for (int i = 0; i < nt; ++i) {
         const int st = i % NST;
         const uint32_t base = smem_u32(smem) + st * STAGE;
         const uint64_t dk = sdesc_sw128(base, C * 128, 1024), dv = sdesc_sw128(base + TK, C * 128, 1024);
-        const uint64_t dl = sdesc_sw128(base + TK + TV, C * 128, 1024);
-        // (ready of tile i comes after tile i - 2's product was read out)
         decay_wait(dead, &ready[st], (i / NST) & 1, lim);
         tc_fence_after();
+        if (!dead) {
 #pragma unroll
-        for (int kk = 0; kk < C / 16; ++kk)
-          mma_bf16_ss(tmem + (i & 1) * DK, dv + mn_step(kk), dl + mn_step(kk), ID, kk > 0);
+          for (int kk = 0; kk < C / 16; ++kk)
+            mma_bf16_ss(tmem + (i & 1) * DK, dv + mn_step(kk), dl + mn_step(kk), ID, kk > 0);
+        }
+        tc_commit(lofree);
+        if (!dead) {
 #pragma unroll
-        for (int kk = 0; kk < C / 16; ++kk) mma_bf16_ss(tmem + (i & 1) * DK, dv + mn_step(kk), dk + mn_step(kk), ID, 1);
+          for (int kk = 0; kk < C / 16; ++kk) mma_bf16_ss(tmem + (i & 1) * DK, dv + mn_step(kk), dk + mn_step(kk), ID, 1);
+        }
         tc_commit(&empty[st]);
         tc_commit(&dfull[i & 1]);
       }
-      for (int i = max(0, nt - 2); i < nt; ++i) mbar_wait(&dfull[i & 1], (i >> 1) & 1, lim);
+      tc_commit(drain);
+      mbar_wait(drain, 0, lim);
     }
   } else {
     bool dead = false;
@@ -423,11 +467,12 @@ __global__ void __launch_bounds__(320, 1) decay_tc_total_kernel(const __grid_con
       decay_wait(dead, &full[st], (i / NST) & 1, lim);
       uint8_t* d = smem + st * STAGE;
       if (n < C) weights(n);
-      decay_scale_tile<DK, true>(d, d + TK + TV, t, wgt);
+      if (i > 0) decay_wait(dead, lofree, (i - 1) & 1, lim);
+      decay_scale_tile<DK, true>(d, lo, t, wgt);
       if (n < C) {
         // (a thread zeroes the units that it scaled itself)
         decay_zero_rows<DK>(d, n, t);
-        decay_zero_rows<DK>(d + TK + TV, n, t);
+        decay_zero_rows<DK>(lo, n, t);
         decay_zero_rows<DV>(d + TK, n, t);
         weights(C);
       }
@@ -469,18 +514,25 @@ __global__ void __launch_bounds__(320, 1) decay_tc_total_kernel(const __grid_con
 }
 
 // ------------------------------------------------------------ outputs ----
-// One block per (segment, head, run), one per SM.  18 warps: 0 TMA loads, 1
-// MMA issue, 2-9 P and the outputs, 10-17 the state and K~.  Order of the MMAs
-// for tile i: O2, D, O1, and Sc of tile i + 1: after O1 where P's columns are
-// the only score columns (P lies over the scores, as the MMA's operand in
-// tensor memory), before it where there are two.  Q and K are free once D is
-// done, V once the output, staged over it, has been stored.
+// One block per (segment, head, run), one per SM.  19 warps: 0 TMA loads, 1
+// issues Sc, O2 and O1, 2-9 P and the outputs, 10-17 the state and K~, 18
+// issues D.  P lies over the scores, as the MMA's operand in tensor memory.
+// Where tensor memory has room for one set of score columns, Sc of tile i + 1
+// follows O1 of tile i; where it has two, it comes before O1 and the warps
+// write P of tile i + 1 before they read the output of tile i.  Q and K are
+// free once O2 and D are done, V once the output, staged over it, is stored.
+//
+// A barrier's next phase must not complete before each waiter has seen this
+// one (two phases look like none).  Each single barrier below has that from the
+// order of the steps: its next arrival needs, directly or through another
+// barrier, something that every waiter does after its wait.  Scores and P,
+// which run a tile ahead, have two.
 //
 // Shared memory is the next bound after HBM: an MMA reads both operands of 128
 // bytes a clock, so a tile of 128 x 128 x 128 moves about 500 KB through it;
 // P in tensor memory saves 64 KB of that.
 template <int DK, int DV>
-__global__ void __launch_bounds__(576, 1) decay_tc_out_kernel(const __grid_constant__ DecayTcArgs A) {
+__global__ void __launch_bounds__(608, 1) decay_tc_out_kernel(const __grid_constant__ DecayTcArgs A) {
   using Cfg = DecayTcCfg<DK, DV>;
   constexpr int C = Cfg::C, NST = Cfg::NST, STAGE = Cfg::STAGE, TK = Cfg::TK, TV = Cfg::TV, NW = Cfg::NW;
   constexpr int NSB = Cfg::NSB;
@@ -490,19 +542,21 @@ __global__ void __launch_bounds__(576, 1) decay_tc_out_kernel(const __grid_const
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Cfg::BIG);
   uint64_t* full = bars;                // [NST] Q and K landed
   uint64_t* fullv = bars + NST;         // [NST] V landed
-  uint64_t* free_qk = bars + 2 * NST;   // [NST] Q and K read for the last time
+  uint64_t* free_qk = bars + 2 * NST;   // [NST] O2 and D complete: Q and K read for the last time, V by D
   uint64_t* empty = bars + 3 * NST;     // [NST] V's slot free: the output has left
   uint64_t* sfull = bars + 4 * NST;     // [2] scores complete
-  uint64_t* kready = sfull + 2;         // K~ written, rows past the end zeroed; D of the tile before read out
+  uint64_t* kready = sfull + 2;         // K~ written; D of the tile before read out
   uint64_t* qdone = sfull + 3;          // O2 complete: Q and Wbf have been read
-  uint64_t* pready = sfull + 4;         // P written over the scores
+  uint64_t* pready = sfull + 13;        // [2] P written over the scores
   uint64_t* dfull = sfull + 5;          // D complete
   uint64_t* wready = sfull + 6;         // Wbf written
-  uint64_t* ofull = sfull + 7;          // O1 complete (and everything before it)
+  uint64_t* ofull = sfull + 7;          // O1 complete
   uint64_t* ofree = sfull + 8;          // O1 and O2 read out
   uint64_t* drain = sfull + 9;
+  uint64_t* drain2 = sfull + 11;
+  uint64_t* cut = sfull + 12;           // rows past the segment's end zeroed in K and V (its last tile, if it has such)
   uint64_t* sread = sfull + 10;         // start state read: the last stage, its buffer, is free
-  float* colp = reinterpret_cast<float*>(bars + 4 * NST + 12);  // [32] gamma^(31-t), reverse gamma^t
+  float* colp = reinterpret_cast<float*>(bars + 4 * NST + 18);  // [32] gamma^(31-t), reverse gamma^t
   float* diag = colp + 32;                                      // [64] sP gamma^(x-31) at x >= 31
   uint32_t* holder = reinterpret_cast<uint32_t*>(diag + 64);
   int* sh = reinterpret_cast<int*>(holder + 1);                 // [40]
@@ -523,19 +577,22 @@ __global__ void __launch_bounds__(576, 1) decay_tc_out_kernel(const __grid_const
     for (int i = 0; i < NST; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&fullv[i], 1);
-      mbar_init(&free_qk[i], 1);
+      mbar_init(&free_qk[i], 2);
       mbar_init(&empty[i], 1);
     }
     mbar_init(&sfull[0], 1);
     mbar_init(&sfull[1], 1);
     mbar_init(kready, 8);
     mbar_init(qdone, 1);
-    mbar_init(pready, 8);
+    mbar_init(&pready[0], 8);
+    mbar_init(&pready[1], 8);
     mbar_init(dfull, 1);
     mbar_init(wready, 8);
     mbar_init(ofull, 1);
     mbar_init(ofree, 8);
     mbar_init(drain, 1);
+    mbar_init(drain2, 1);
+    mbar_init(cut, 8);
     mbar_init(sread, 8);
     fence_mbar_init();
   }
@@ -558,79 +615,83 @@ __global__ void __launch_bounds__(576, 1) decay_tc_out_kernel(const __grid_const
     // ------------------------------------------------------------ loads --
     if (lane == 0) {
       bool dead = false;
+      int sent = 0, sentv = 0;
       const uint64_t pol = l2_policy_evict_first();
       for (int i = 0; i < nt; ++i) {
         const int st = i % NST, y = sp.row0 + tile_at(i);
         uint8_t* d = smem + st * STAGE;
         if (i >= NST) decay_wait(dead, &free_qk[st], (i / NST - 1) & 1, lim);
         if (i == NST - 1) decay_wait(dead, sread, 0, lim);
+        if (dead) break;
         mbar_arrive_expect_tx(&full[st], 2 * TK);
 #pragma unroll
         for (int x = 0; x < DK / 64; ++x) {
           tma_load_4d(&A.map[p.q], &full[st], d + x * C * 128, x * 64, y, h, sp.batch, pol);
           tma_load_4d(&A.map[p.k], &full[st], d + TK + x * C * 128, x * 64, y, h, sp.batch, pol);
         }
+        sent = i + 1;
         if (i >= NST) decay_wait(dead, &empty[st], (i / NST - 1) & 1, lim);
+        if (dead) break;
         mbar_arrive_expect_tx(&fullv[st], TV);
 #pragma unroll
         for (int x = 0; x < DV / 64; ++x)
           tma_load_4d(&A.map[p.v], &fullv[st], d + 2 * TK + x * C * 128, x * 64, y, h, sp.batch, pol);
+        sentv = i + 1;
       }
-      for (int i = max(0, nt - NST); i < nt; ++i) {
-        mbar_wait(&full[i % NST], (i / NST) & 1, lim);
-        mbar_wait(&fullv[i % NST], (i / NST) & 1, lim);
-      }
+      for (int i = max(0, sent - NST); i < sent; ++i) mbar_wait(&full[i % NST], (i / NST) & 1, lim);
+      for (int i = max(0, sentv - NST); i < sentv; ++i) mbar_wait(&fullv[i % NST], (i / NST) & 1, lim);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------- MMAs --
     if (lane == 0) {
       bool dead = false;
       constexpr uint32_t ID_S = idesc_bf16_f32(C, C, false, false), ID_Q = idesc_bf16_f32(C, DV, false, false);
-      constexpr uint32_t ID_D = idesc_bf16_f32(DV, DK, true, true), ID_P = idesc_bf16_f32(C, DV, false, true);
+      constexpr uint32_t ID_P = idesc_bf16_f32(C, DV, false, true);
       const uint64_t d_w = sdesc_sw128(sbase + NST * STAGE, 16, 1024);
+      auto ragged = [&](int i) { return sp.len - tile_at(i) < C; };
       auto scores = [&](int i) {  // its tile has landed
+        if (ragged(i)) decay_wait(dead, cut, 0, lim);
         const uint32_t base = sbase + (i % NST) * STAGE;
         const uint64_t dq = sdesc_sw128(base, 16, 1024), dk = sdesc_sw128(base + TK, 16, 1024);
         tc_fence_after();
+        if (!dead) {
 #pragma unroll
-        for (int kk = 0; kk < DK / 16; ++kk)
-          mma_bf16_ss(tmem + (i % NSB) * C, dq + k_step(C, kk), dk + k_step(C, kk), ID_S, kk > 0);
+          for (int kk = 0; kk < DK / 16; ++kk)
+            mma_bf16_ss(tmem + (i % NSB) * C, dq + k_step(C, kk), dk + k_step(C, kk), ID_S, kk > 0);
+        }
         tc_commit(&sfull[i & 1]);
       };
       decay_wait(dead, &full[0], 0, lim);
       scores(0);
       for (int i = 0; i < nt; ++i) {
         const uint32_t base = sbase + (i % NST) * STAGE, par = i & 1;
-        const uint64_t dq = sdesc_sw128(base, 16, 1024), dkm = sdesc_sw128(base + TK, C * 128, 1024);
-        const uint64_t dvm = sdesc_sw128(base + 2 * TK, C * 128, 1024);
-        decay_wait(dead, wready, par, lim);
-        if (i > 0) decay_wait(dead, ofree, (i - 1) & 1, lim);
-        tc_fence_after();
-#pragma unroll
-        for (int kk = 0; kk < DK / 16; ++kk)
-          mma_bf16_ss(t_o2, dq + k_step(C, kk), d_w + k_step(DV, kk), ID_Q, kk > 0);
-        tc_commit(qdone);
-        decay_wait(dead, kready, par, lim);
-        decay_wait(dead, &fullv[i % NST], (i / NST) & 1, lim);
-        tc_fence_after();
-        if (i + 1 < nt) {
-#pragma unroll
-          for (int kk = 0; kk < C / 16; ++kk) mma_bf16_ss(t_d, dvm + mn_step(kk), dkm + mn_step(kk), ID_D, kk > 0);
-          tc_commit(dfull);
-          tc_commit(&free_qk[i % NST]);
-        }
+        const uint64_t dq = sdesc_sw128(base, 16, 1024), dvm = sdesc_sw128(base + 2 * TK, C * 128, 1024);
         const int j = i + 1;
+        // Wbf of tile i: the state warps are done with tile i - 1, its scores' barrier among that
+        decay_wait(dead, wready, par, lim);
         bool ahead = false;
-        if (NSB == 2) {  // (the other score columns were last P of tile i - 1, whose O1 is done)
-          ahead = j < nt && !dead && mbar_try_wait(smem_u32(&full[j % NST]), (j / NST) & 1);
+        if (NSB == 2) {  // (the other score columns were last P of tile i - 1, read by the O1 before)
+          ahead = j < nt && !dead && !ragged(j) && mbar_try_wait(smem_u32(&full[j % NST]), (j / NST) & 1);
           if (ahead) scores(j);
         }
-        decay_wait(dead, pready, par, lim);
+        if (i > 0) decay_wait(dead, ofree, (i - 1) & 1, lim);
+        tc_fence_after();
+        if (!dead) {
+#pragma unroll
+          for (int kk = 0; kk < DK / 16; ++kk)
+            mma_bf16_ss(t_o2, dq + k_step(C, kk), d_w + k_step(DV, kk), ID_Q, kk > 0);
+        }
+        tc_commit(qdone);
+        tc_commit(&free_qk[i % NST]);
+        decay_wait(dead, &fullv[i % NST], (i / NST) & 1, lim);
+        decay_wait(dead, &pready[par], (i >> 1) & 1, lim);
         tc_fence_after();
         const uint32_t t_p = tmem + (i % NSB) * C;
+        if (!dead) {
 #pragma unroll
-        for (int kk = 0; kk < C / 16; ++kk)
-          mma_bf16_ts(t_o1, t_p + (kk >> 2) * 64 + (kk & 3) * 8, dvm + mn_step(kk), ID_P, kk > 0);
+          for (int kk = 0; kk < C / 16; ++kk)
+            mma_bf16_ts(t_o1, t_p + (kk >> 2) * 64 + (kk & 3) * 8, dvm + mn_step(kk), ID_P, kk > 0);
+        }
         tc_commit(ofull);
         if (j < nt && !ahead) {
           decay_wait(dead, &full[j % NST], (j / NST) & 1, lim);
@@ -639,6 +700,28 @@ __global__ void __launch_bounds__(576, 1) decay_tc_out_kernel(const __grid_const
       }
       tc_commit(drain);
       mbar_wait(drain, 0, lim);
+    }
+  } else if (warp == 18) {
+    if (lane == 0) {
+      bool dead = false;
+      constexpr uint32_t ID_D = idesc_bf16_f32(DV, DK, true, true);
+      for (int i = 0; i < nt; ++i) {
+        if (i + 1 < nt) {
+          const uint32_t base = sbase + (i % NST) * STAGE;
+          const uint64_t dkm = sdesc_sw128(base + TK, C * 128, 1024), dvm = sdesc_sw128(base + 2 * TK, C * 128, 1024);
+          decay_wait(dead, &fullv[i % NST], (i / NST) & 1, lim);
+          decay_wait(dead, kready, i & 1, lim);
+          tc_fence_after();
+          if (!dead) {
+#pragma unroll
+            for (int kk = 0; kk < C / 16; ++kk) mma_bf16_ss(t_d, dvm + mn_step(kk), dkm + mn_step(kk), ID_D, kk > 0);
+          }
+          tc_commit(dfull);
+        }
+        tc_commit(&free_qk[i % NST]);
+      }
+      tc_commit(drain2);
+      mbar_wait(drain2, 0, lim);
     }
   } else if (warp < 10) {
     // --------------------------------------------------- P and outputs --
@@ -657,8 +740,7 @@ __global__ void __launch_bounds__(576, 1) decay_tc_out_kernel(const __grid_const
       edge[x] = p.sP * expf(l * static_cast<float>(max(rev ? 32 * dist[x] - lane : lane + 32 * dist[x] - 31, 0)));
     }
     const float read_full = p.sR * expf(l * static_cast<float>(rev ? C - 1 - r : r + 1));
-    for (int i = 0; i < nt; ++i) {
-      const int at = tile_at(i), n = min(C, sp.len - at), y = sp.row0 + at;
+    auto scores_to_p = [&](int i) {
       decay_wait(dead, &sfull[i & 1], (i >> 1) & 1, lim);
       __syncwarp();
       tc_fence_after();
@@ -666,79 +748,73 @@ __global__ void __launch_bounds__(576, 1) decay_tc_out_kernel(const __grid_const
 #pragma unroll
       for (int b2 = 0; b2 < 2; ++b2) {
         uint32_t x[32];
-        const int j0 = 64 * half + 32 * b2;
+        uint32_t pk[16];
+        if (dist[b2] >= 0) tmem_ld32(ts + 32 * b2, x);
         if (dist[b2] < 0) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) x[e] = 0u;
+          for (int e = 0; e < 16; ++e) pk[e] = 0u;
         } else if (dist[b2] == 0) {
-          tmem_ld32(ts + 32 * b2, x);
           tmem_ld_wait();
           if (rev) {
             const float* w = diag + 31 - lane;
 #pragma unroll
-            for (int e = 0; e < 32; ++e) x[e] = e >= lane ? __float_as_uint(w[e] * __uint_as_float(x[e])) : 0u;
+            for (int e = 0; e < 32; e += 2) pk[e / 2] = pack_bf16x2(mul2(pair(w[e], w[e + 1]), pair(x[e], x[e + 1])));
           } else {
             const float* w = diag + 31 + lane;
 #pragma unroll
-            for (int e = 0; e < 32; ++e) x[e] = lane >= e ? __float_as_uint(w[-e] * __uint_as_float(x[e])) : 0u;
+            for (int e = 0; e < 32; e += 2) pk[e / 2] = pack_bf16x2(mul2(pair(w[-e], w[-e - 1]), pair(x[e], x[e + 1])));
           }
         } else {
-          tmem_ld32(ts + 32 * b2, x);
-          const float rp = edge[b2];
+          const f2 rp = pair(edge[b2], edge[b2]);
           tmem_ld_wait();
 #pragma unroll
           for (int e = 0; e < 32; e += 4) {
             const float4 cp = *reinterpret_cast<const float4*>(colp + e);
-            x[e] = __float_as_uint(rp * cp.x * __uint_as_float(x[e]));
-            x[e + 1] = __float_as_uint(rp * cp.y * __uint_as_float(x[e + 1]));
-            x[e + 2] = __float_as_uint(rp * cp.z * __uint_as_float(x[e + 2]));
-            x[e + 3] = __float_as_uint(rp * cp.w * __uint_as_float(x[e + 3]));
+            pk[e / 2] = pack_bf16x2(mul2(mul2(rp, pair(cp.x, cp.y)), pair(x[e], x[e + 1])));
+            pk[e / 2 + 1] = pack_bf16x2(mul2(mul2(rp, pair(cp.z, cp.w)), pair(x[e + 2], x[e + 3])));
           }
         }
-        if (rev && j0 + 32 > n) {  // columns behind the segment's end (forward: c <= r < n)
-#pragma unroll
-          for (int e = 0; e < 32; ++e) x[e] = j0 + e < n ? x[e] : 0u;
-        }
         // over this warp's own score columns: those of the block before have been read
-        uint32_t pk[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) pk[e] = pack_bf16x2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
         tmem_st16(ts + 16 * b2, pk);
       }
       tmem_st_wait();
-      warp_arrive(pready, lane);
-
+      warp_arrive(&pready[i & 1], lane);
+    };
+    auto output = [&](int i) {
+      const int at = tile_at(i), n = min(C, sp.len - at), y = sp.row0 + at;
       float rp = read_full;
       if (rev && n < C) rp = r < n ? p.sR * expf(l * static_cast<float>(n - 1 - r)) : 0.f;
+      const f2 rp2 = pair(rp, rp);
       const uint32_t stage = sbase + (i % NST) * STAGE + 2 * TK;
       // a tile that ends inside the tensor's rows is stored row by row: a box would reach the rows behind
       const bool whole = n == C || y + n == g.T;
       decay_wait(dead, ofull, i & 1, lim);
+      decay_wait(dead, &free_qk[i % NST], (i / NST) & 1, lim);
       __syncwarp();
       tc_fence_after();
 #pragma unroll
-      for (int x = 0; x < DV / 2; x += 32) {
+      for (int x = 0; x < DV / 2; x += 16) {
         const int c0 = half * (DV / 2) + x;
-        uint32_t a[32], q[32];
-        tmem_ld32(t_o1 + lanes + c0, a);
-        tmem_ld32(t_o2 + lanes + c0, q);
+        uint32_t a[16], q[16], pk[8];
+        tmem_ld16(t_o1 + lanes + c0, a);
+        tmem_ld16(t_o2 + lanes + c0, q);
         tmem_ld_wait();
-        if (x + 32 == DV / 2) warp_arrive(ofree, lane);
+        if (x + 16 == DV / 2) warp_arrive(ofree, lane);
 #pragma unroll
-        for (int e = 0; e < 32; ++e) a[e] = __float_as_uint(fmaf(rp, __uint_as_float(q[e]), __uint_as_float(a[e])));
+        for (int e = 0; e < 8; ++e)
+          pk[e] = pack_bf16x2(fma2(rp2, pair(q[2 * e], q[2 * e + 1]), pair(a[2 * e], a[2 * e + 1])));
         if (whole) {
-          store_row32_bf16(stage, C * 128, r, c0, a);
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            st_shared_v4(stage + (c0 >> 6) * C * 128 + sw128_off(r, ((c0 & 63) >> 3) + e), pk[4 * e], pk[4 * e + 1],
+                         pk[4 * e + 2], pk[4 * e + 3]);
         } else if (r < n) {
           __nv_bfloat16* out = p.op + static_cast<size_t>(sp.batch) * p.ob + static_cast<size_t>(h) * p.oh +
                                static_cast<size_t>(y + r) * p.ot;
 #pragma unroll
-          for (int e = 0; e < 32; e += 8)
-            if (c0 + e < p.dv)
-              *reinterpret_cast<uint4*>(out + c0 + e) = make_uint4(
-                  pack_bf16x2(__uint_as_float(a[e]), __uint_as_float(a[e + 1])),
-                  pack_bf16x2(__uint_as_float(a[e + 2]), __uint_as_float(a[e + 3])),
-                  pack_bf16x2(__uint_as_float(a[e + 4]), __uint_as_float(a[e + 5])),
-                  pack_bf16x2(__uint_as_float(a[e + 6]), __uint_as_float(a[e + 7])));
+          for (int e = 0; e < 2; ++e)
+            if (c0 + 8 * e < p.dv)
+              *reinterpret_cast<uint4*>(out + c0 + 8 * e) = make_uint4(pk[4 * e], pk[4 * e + 1], pk[4 * e + 2], pk[4 * e + 3]);
         }
       }
       if (whole) {
@@ -746,7 +822,7 @@ __global__ void __launch_bounds__(576, 1) decay_tc_out_kernel(const __grid_const
         asm volatile("bar.sync 1, 256;" ::: "memory");
         if (threadIdx.x == 2 * 32) {
 #pragma unroll
-          for (int x = 0; x < DV / 64; ++x)
+          for (int x = 0; x < (dead ? 0 : DV / 64); ++x)
             tma_store_4d(&A.map[p.o], smem + (i % NST) * STAGE + 2 * TK + x * C * 128, x * 64, y, h, sp.batch);
           bulk_commit();
           bulk_wait_read0();
@@ -754,6 +830,18 @@ __global__ void __launch_bounds__(576, 1) decay_tc_out_kernel(const __grid_const
         }
       } else if (threadIdx.x == 2 * 32) {
         mbar_arrive(&empty[i % NST]);
+      }
+    };
+    if (NSB == 2) {
+      scores_to_p(0);
+      for (int i = 0; i < nt; ++i) {
+        if (i + 1 < nt) scores_to_p(i + 1);
+        output(i);
+      }
+    } else {
+      for (int i = 0; i < nt; ++i) {
+        scores_to_p(i);
+        output(i);
       }
     }
     if (threadIdx.x == 2 * 32) bulk_wait0();
@@ -804,22 +892,26 @@ __global__ void __launch_bounds__(576, 1) decay_tc_out_kernel(const __grid_const
       const int st = i % NST, n = min(C, sp.len - tile_at(i));
       const bool more = i + 1 < nt;
       decay_wait(dead, &full[st], (i / NST) & 1, lim);
-      if (n < C) decay_wait(dead, &fullv[st], (i / NST) & 1, lim);
+      uint8_t* d = smem + st * STAGE;
+      if (n < C) {
+        // what lies behind the segment's end may be anything: with zeros for keys and values it enters no sum, and the
+        // scores need no mask there (queries behind the end make rows that are not stored)
+        decay_wait(dead, &fullv[st], (i / NST) & 1, lim);
+        __syncwarp();
+        decay_zero_rows<DK>(d + TK, n, t);
+        decay_zero_rows<DV>(d + 2 * TK, n, t);
+        fence_async_smem();
+        warp_arrive(cut, lane);
+      }
       decay_wait(dead, &sfull[i & 1], (i >> 1) & 1, lim);  // K has been read for the scores
       __syncwarp();
-      uint8_t* d = smem + st * STAGE;
       float gn = g_full;
       if (n < C) {
         weights(n);
         gn = expf(l * static_cast<float>(n));
       }
       if (more) decay_scale_tile<DK, false>(d + TK, nullptr, t, wgt);
-      if (n < C) {
-        // (a thread zeroes the units that it scaled itself)
-        decay_zero_rows<DK>(d + TK, n, t);
-        decay_zero_rows<DV>(d + 2 * TK, n, t);
-        weights(C);
-      }
+      if (n < C) weights(C);
       fence_async_smem();
       warp_arrive(kready, lane);
       if (!more) break;
