@@ -5,55 +5,68 @@
 
 namespace {
 
-// Values per thread unit: the most of 16 bytes that lie in one group.
-int gn_unit(int cg, int dtype) {
-  for (int v = dtype == TTT_LA_F32 ? 4 : 8; v > 1; v /= 2)
-    if (cg % v == 0) return v;
-  return 1;
-}
-// One position a sample and a group of at most a warp's units, a power of two
-// of them: the registers-only kernels.
+int gn_unit(int dtype) { return dtype == TTT_LA_F32 ? 4 : 8; }  // values in 16 bytes
+
+// One position a sample and a group of 1, 2, 4 .. 32 units: the kernels that
+// hold a group in registers.
 int gn_row_lanes(int L, int cg, int dtype) {
-  const int v = gn_unit(cg, dtype), lanes = cg / v;
-  return L == 1 && v == (dtype == TTT_LA_F32 ? 4 : 8) && lanes <= 32 && (lanes & (lanes - 1)) == 0 ? lanes : 0;
+  const int v = gn_unit(dtype), lanes = cg / v;
+  return L == 1 && cg % v == 0 && lanes <= 32 && (lanes & (lanes - 1)) == 0 ? lanes : 0;
 }
 
 struct GnPlan {
-  int lanes;         // > 0: the one-position kernels
-  int splits, rows;  // parts of a sample and the positions in each
-  int blocks;        // row blocks of the one-position gradient
-  size_t floats;     // workspace
+  int lanes;               // > 0: the one-position kernels
+  int width, slots;        // of those: units of a row in a block, rows at a time
+  int columns, blocks;     // and their grid
+  int splits, rows;        // parts of a sample and the positions in each: sums
+  int parts, part_rows;    // the same: writing passes
+  size_t floats;           // workspace
 };
 
-// Enough parts that all samples together fill the SMs a few times over, none
-// with so few positions that a block's joins cost more than its reads.
-void gn_split(GnPlan* p, int N, int L, int C, int dtype) {
-  const long long want = std::max(1ll, (static_cast<long long>(sm_count()) * 8 + N - 1) / N);
-  const long long row_bytes = static_cast<long long>(C) * (dtype == TTT_LA_F32 ? 4 : 2);
-  const long long least = std::max(1ll, 16384 / row_bytes);
-  p->rows = static_cast<int>(std::max(least, (L + want - 1) / want));
-  p->rows = std::min(p->rows, L);
-  p->splits = (L - 1) / p->rows + 1;
+// `per_sm` parts for each SM over all samples, none with so few positions that
+// a block's sums cost more than its reads (16 KB).
+void gn_split(int N, int L, int C, int dtype, int per_sm, int* parts, int* rows) {
+  const long long want = std::max(1ll, (static_cast<long long>(sm_count()) * per_sm + N - 1) / N);
+  const long long least = std::max(1ll, 16384 / (static_cast<long long>(C) * (dtype == TTT_LA_F32 ? 4 : 2)));
+  *rows = static_cast<int>(std::min<long long>(std::max(least, (L + want - 1) / want), L));
+  *parts = (L - 1) / *rows + 1;
+}
+
+// Blocks of up to 256 threads over the units of a row (wide rows in equal
+// columns, narrow ones several at a time) and `per_sm` of them for each SM.
+void gn_row_plan(GnPlan* p, int N, int C, int dtype, int per_sm) {
+  const int cv = C / gn_unit(dtype);
+  p->columns = (cv + 255) / 256;
+  // (whole warps, so that a group's lanes stay in one)
+  p->width = p->columns == 1 ? cv : ((cv + p->columns - 1) / p->columns + 31) / 32 * 32;
+  p->columns = (cv + p->width - 1) / p->width;
+  p->slots = std::max(1, 256 / p->width);
+  const long long rows = (static_cast<long long>(N) + p->slots - 1) / p->slots;
+  p->blocks = static_cast<int>(std::min<long long>(rows, std::max(1, sm_count() * per_sm / p->columns)));
 }
 
 GnPlan gn_plan_forward(int N, int L, int C, int G, int dtype) {
   GnPlan p = {};
   p.lanes = gn_row_lanes(L, C / G, dtype);
-  if (p.lanes) return p;
-  gn_split(&p, N, L, C, dtype);
-  p.floats = static_cast<size_t>(N) * p.splits * G * 2;
+  if (p.lanes) {
+    gn_row_plan(&p, N, C, dtype, 8);
+    return p;
+  }
+  gn_split(N, L, C, dtype, 4, &p.splits, &p.rows);
+  gn_split(N, L, C, dtype, 8, &p.parts, &p.part_rows);
+  p.floats = p.splits > 1 ? static_cast<size_t>(N) * p.splits * G * 2 : 0;
   return p;
 }
 GnPlan gn_plan_backward(int N, int L, int C, int G, int dtype, bool params) {
   GnPlan p = {};
   p.lanes = gn_row_lanes(L, C / G, dtype);
   if (p.lanes) {
-    const int cv = C / gn_unit(C / G, dtype), cols = (cv + 255) / 256, slots = cv < 256 ? 256 / cv : 1;
-    p.blocks = static_cast<int>(std::min<long long>((N + slots - 1) / slots, std::max(1, sm_count() * 4 / cols)));
+    gn_row_plan(&p, N, C, dtype, 3);
     p.floats = params ? static_cast<size_t>(2) * p.blocks * C : 0;
     return p;
   }
-  gn_split(&p, N, L, C, dtype);
+  gn_split(N, L, C, dtype, 3, &p.splits, &p.rows);
+  gn_split(N, L, C, dtype, 8, &p.parts, &p.part_rows);
   p.floats = static_cast<size_t>(2) * N * p.splits * C + static_cast<size_t>(2) * N * G;
   return p;
 }
@@ -72,22 +85,20 @@ ttt_la_status check_gn(int N, int L, int C, int G, int dtype, int param_dtype, i
 bool gn_aligned(const void* p, int dtype) { return reinterpret_cast<uintptr_t>(p) % (dtype == TTT_LA_F32 ? 4 : 2) == 0; }
 
 template <typename F>
-ttt_la_status gn_dispatch(int dtype, int v, bool gate, F&& f) {
-  // f(type tag, unit, gate)
-  auto by_gate = [&](auto t, auto u) {
-    return gate ? f(t, u, std::true_type{}) : f(t, u, std::false_type{});
-  };
-  if (dtype == TTT_LA_F32) {
-    if (v == 4) return by_gate(float{}, std::integral_constant<int, 4>{});
-    if (v == 2) return by_gate(float{}, std::integral_constant<int, 2>{});
-    return by_gate(float{}, std::integral_constant<int, 1>{});
-  }
-  using bf = __nv_bfloat16;
-  if (v == 8) return by_gate(bf{}, std::integral_constant<int, 8>{});
-  if (v == 4) return by_gate(bf{}, std::integral_constant<int, 4>{});
-  if (v == 2) return by_gate(bf{}, std::integral_constant<int, 2>{});
-  return by_gate(bf{}, std::integral_constant<int, 1>{});
+ttt_la_status gn_dispatch(int dtype, bool gate, F&& f) {
+  // f(type tag, values of a unit, gate)
+  if (dtype == TTT_LA_F32)
+    return gate ? f(float{}, std::integral_constant<int, 4>{}, std::true_type{})
+                : f(float{}, std::integral_constant<int, 4>{}, std::false_type{});
+  return gate ? f(__nv_bfloat16{}, std::integral_constant<int, 8>{}, std::true_type{})
+              : f(__nv_bfloat16{}, std::integral_constant<int, 8>{}, std::false_type{});
 }
+
+void gn_fill(ttt::GnParams* p, const GnPlan& pl) {
+  p->splits = pl.splits, p->rows = pl.rows, p->parts = pl.parts, p->part_rows = pl.part_rows;
+  p->width = pl.width, p->slots = pl.slots;
+}
+int gn_row_threads(const GnPlan& pl) { return (pl.width * pl.slots + 31) / 32 * 32; }
 
 }  // namespace
 
@@ -118,25 +129,30 @@ ttt_la_status ttt_la_group_norm(const ttt_la_group_norm_args* a, void* stream) {
   p.act = a->activation, p.eps = a->eps;
   p.y = a->y, p.mean = a->mean, p.rstd = a->rstd;
   p.part = static_cast<float*>(a->workspace);
-  p.splits = pl.splits, p.rows = pl.rows;
+  gn_fill(&p, pl);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const int v = gn_unit(p.cg, a->dtype);
-  return gn_dispatch(a->dtype, v, a->gate != nullptr, [&](auto t, auto u, auto gate) -> ttt_la_status {
+  return gn_dispatch(a->dtype, a->gate != nullptr, [&](auto t, auto u, auto gate) -> ttt_la_status {
     using T = decltype(t);
     constexpr int V = decltype(u)::value;
     constexpr bool GATE = decltype(gate)::value;
     if (pl.lanes) {
-      const long long units = static_cast<long long>(a->N) * (a->C / V);
-      const int blocks = static_cast<int>(std::min<long long>((units + 255) / 256, static_cast<long long>(sm_count()) * 32));
-      return launch_kernel(ttt::gn_row_kernel<T, V, GATE>, blocks, 256, 0, st, false, p, pl.lanes);
+      ttt::gn_row_kernel<T, V, GATE><<<dim3(pl.columns, pl.blocks), gn_row_threads(pl), 0, st>>>(p, pl.lanes);
+      return launched();
     }
-    const long long blocks = static_cast<long long>(a->N) * pl.splits;
-    if (blocks >= (1ll << 31)) return TTT_LA_ERR_UNSUPPORTED;
-    const int sm1 = a->G * static_cast<int>(sizeof(ttt::Moments)), sm2 = a->G * 8;
-    if (!grant_smem(reinterpret_cast<const void*>(ttt::gn_stats_kernel<T, V>), sm1)) return TTT_LA_ERR_CUDA;
-    const ttt_la_status r = launch_kernel(ttt::gn_stats_kernel<T, V>, static_cast<int>(blocks), 256, sm1, st, false, p);
+    const long long sums = static_cast<long long>(a->N) * pl.splits, parts = static_cast<long long>(a->N) * pl.parts;
+    if (parts >= (1ll << 31) || sums >= (1ll << 31)) return TTT_LA_ERR_UNSUPPORTED;
+    const int sm = a->G * static_cast<int>(sizeof(ttt::Moments));
+    // (the kernel's own tables, 19 KB, count towards the 48 KB that need no grant)
+    if (sm > 28 * 1024 && !grant_smem(reinterpret_cast<const void*>(ttt::gn_stats_kernel<T, V>), 49 * 1024))
+      return TTT_LA_ERR_CUDA;
+    ttt_la_status r = launch_kernel(ttt::gn_stats_kernel<T, V>, static_cast<int>(sums), 256, sm, st, false, p);
     if (r != TTT_LA_OK) return r;
-    return launch_kernel(ttt::gn_apply_kernel<T, V, GATE>, static_cast<int>(blocks), 256, sm2, st, false, p);
+    if (pl.splits > 1) {
+      const long long warps = static_cast<long long>(a->N) * a->G;
+      r = launch_kernel(ttt::gn_join_kernel, static_cast<int>((warps * 32 + 255) / 256), 256, 0, st, false, p);
+      if (r != TTT_LA_OK) return r;
+    }
+    return launch_kernel(ttt::gn_apply_kernel<T, V, GATE>, static_cast<int>(parts), 256, 0, st, false, p);
   });
 }
 
@@ -172,40 +188,34 @@ ttt_la_status ttt_la_group_norm_backward(const ttt_la_group_norm_grad_args* a, v
   p.act = a->activation;
   p.mean = const_cast<float*>(a->mean), p.rstd = const_cast<float*>(a->rstd);
   p.gy = a->grad_y, p.gx = a->grad_x, p.ggate = a->grad_gate;
+  p.gw = a->grad_weight, p.gb = a->grad_bias;
   p.part = pl.floats ? static_cast<float*>(a->workspace) : nullptr;
-  p.splits = pl.splits, p.rows = pl.rows, p.blocks = pl.blocks;
+  gn_fill(&p, pl);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const int v = gn_unit(p.cg, a->dtype);
-  return gn_dispatch(a->dtype, v, a->gate != nullptr, [&](auto t, auto u, auto gate) -> ttt_la_status {
+  return gn_dispatch(a->dtype, a->gate != nullptr, [&](auto t, auto u, auto gate) -> ttt_la_status {
     using T = decltype(t);
     constexpr int V = decltype(u)::value;
     constexpr bool GATE = decltype(gate)::value;
-    ttt_la_status r = TTT_LA_OK;
-    int count = 0;
     if (pl.lanes) {
-      const dim3 grid((a->C / V + 255) / 256, pl.blocks);
-      ttt::gn_row_grad_kernel<T, V, GATE><<<grid, 256, 0, st>>>(p, pl.lanes);
-      if ((r = launched()) != TTT_LA_OK) return r;
-      count = pl.blocks;
-    } else {
-      const long long blocks = static_cast<long long>(a->N) * pl.splits;
-      if (blocks >= (1ll << 31)) return TTT_LA_ERR_UNSUPPORTED;
-      float* sums = p.part + static_cast<size_t>(2) * blocks * a->C;
-      r = launch_kernel(ttt::gn_grad_sums_kernel<T, V, GATE>, static_cast<int>(blocks), 256, 0, st, false, p);
-      if (r != TTT_LA_OK) return r;
-      const long long warps = static_cast<long long>(a->N) * a->G;
-      r = launch_kernel(ttt::gn_grad_groups_kernel, static_cast<int>((warps * 32 + 255) / 256), 256, 0, st, false, p, sums);
-      if (r != TTT_LA_OK) return r;
-      r = launch_kernel(ttt::gn_grad_apply_kernel<T, V, GATE>, static_cast<int>(blocks), 256, 0, st, false, p, sums);
-      if (r != TTT_LA_OK) return r;
-      count = static_cast<int>(blocks);
-    }
-    if (params) {
-      ttt::gn_param_grad_kernel<<<dim3((a->C + 31) / 32, 2), 256, 0, st>>>(p.part, count, a->C, a->grad_weight,
+      ttt::gn_row_grad_kernel<T, V, GATE><<<dim3(pl.columns, pl.blocks), gn_row_threads(pl), 0, st>>>(p, pl.lanes);
+      const ttt_la_status r = launched();
+      if (r != TTT_LA_OK || !params) return r;
+      ttt::gn_param_grad_kernel<<<dim3((a->C + 31) / 32, 2), 256, 0, st>>>(p.part, pl.blocks, a->C, a->grad_weight,
                                                                           a->grad_bias, p.pbf);
-      r = launched();
+      return launched();
     }
-    return r;
+    const long long rows = static_cast<long long>(a->N) * pl.splits, parts = static_cast<long long>(a->N) * pl.parts;
+    if (parts >= (1ll << 31) || rows >= (1ll << 31)) return TTT_LA_ERR_UNSUPPORTED;
+    float* sums = p.part + static_cast<size_t>(2) * rows * a->C;
+    ttt_la_status r = launch_kernel(ttt::gn_grad_sums_kernel<T, V, GATE>, static_cast<int>(rows), 256, 0, st, false, p);
+    if (r != TTT_LA_OK) return r;
+    const long long warp_blocks = (static_cast<long long>(a->N) * a->G + 7) / 8;
+    const long long blocks = warp_blocks + (params ? 2 * ((a->C + 31) / 32) : 0);
+    if (blocks >= (1ll << 31)) return TTT_LA_ERR_UNSUPPORTED;
+    r = launch_kernel(ttt::gn_grad_groups_kernel, static_cast<int>(blocks), 256, 0, st, false, p, sums,
+                      static_cast<int>(warp_blocks));
+    if (r != TTT_LA_OK) return r;
+    return launch_kernel(ttt::gn_grad_apply_kernel<T, V, GATE>, static_cast<int>(parts), 256, 0, st, false, p, sums);
   });
 }
 

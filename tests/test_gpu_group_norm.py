@@ -41,6 +41,10 @@ CASES = [
     ((2, 50, 2056), 1, "bf16", "f32", False, "silu", 4.0),      # more units than a block has threads
     ((1, 3000, 48), 16, "f32", None, True, "silu", 0.0),        # three channels a group
     ((600, 3, 64), 4, "bf16", "f32", False, "silu", 0.0),
+    ((5, 7, 8192), 4096, "bf16", "f32", True, "silu", 0.0),     # the most groups
+    ((70, 1, 3200), 25, "bf16", "f32", True, "silu", 0.0),      # a row in two columns of blocks
+    ((11, 1, 192), 8, "bf16", "f32", True, None, 0.0),          # three units a group: not a power of two
+    ((40, 1, 192), 24, "bf16", "bf16", False, "silu", 0.0),     # one unit a group, rows side by side in a block
 ]
 
 
