@@ -466,8 +466,8 @@ TTT_LA_API ttt_la_status ttt_la_decode_step_decay(const ttt_la_decay_decode_args
  *   y = act(t), or with a gate  y = t * act(gate)
  * activation: 0 none, 1 silu (silu(z) = z / (1 + exp(-z))).  weight, bias [C]
  * of param_dtype, or NULL (1, 0).  mean, rstd: fp32 [N,G], written (the
- * gradient reads them).  C a multiple of 16 bytes of x's type, G <= 4096, else
- * TTT_LA_ERR_UNSUPPORTED; any width of a group.  y must not overlap x, gate,
+ * gradient reads them).  Any C and any width of a group; G <= 4096, else
+ * TTT_LA_ERR_UNSUPPORTED.  y must not overlap x, gate,
  * weight or bias. */
 typedef struct ttt_la_group_norm_args {
   int32_t N, L, C, G;

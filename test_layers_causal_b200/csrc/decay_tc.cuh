@@ -70,34 +70,6 @@ __device__ __forceinline__ void tmem_ld_half16(uint32_t taddr, uint32_t (&r)[16]
       : "r"(taddr));
 }
 
-// Two fp32 operations in one instruction.
-struct f2 {
-  unsigned long long v;
-};
-__device__ __forceinline__ f2 pair(float lo, float hi) {
-  f2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ f2 pair(uint32_t lo, uint32_t hi) {
-  f2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "r"(lo), "r"(hi));
-  return r;
-}
-__device__ __forceinline__ float lo_of(f2 x) { return __uint_as_float(static_cast<uint32_t>(x.v)); }
-__device__ __forceinline__ float hi_of(f2 x) { return __uint_as_float(static_cast<uint32_t>(x.v >> 32)); }
-__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
-  f2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
-  f2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-  return r;
-}
-__device__ __forceinline__ uint32_t pack_bf16x2(f2 x) { return pack_bf16x2(lo_of(x), hi_of(x)); }
-
 constexpr int kDecayTcC = 128;      // tokens per tile
 constexpr int kDecayTcRuns = 3;     // the most runs in one launch
 constexpr int kDecayTcMaps = 7;

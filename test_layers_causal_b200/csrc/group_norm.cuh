@@ -22,45 +22,51 @@
 
 namespace ttt {
 
-// 16 bytes of T as floats.
+// V consecutive values of T as pairs of floats: 16 bytes, or one value (its
+// pair's other half is 0) where rows do not start on 16 bytes.
 template <typename T, int V>
 struct Unit {
-  float v[V];
+  static constexpr int P = V > 1 ? V / 2 : 1;
+  f2 v[P];
 };
 template <typename T, int V>
 __device__ __forceinline__ Unit<T, V> ld_unit(const T* p) {
-  static_assert(sizeof(T) * V == 16, "");
+  static_assert(V == 1 || sizeof(T) * V == 16, "");
   Unit<T, V> r;
-  const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  if constexpr (V == 1) {
+    r.v[0] = pair(to_f<T>(__ldg(p)), 0.f);
+  } else {
+    const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
     if constexpr (sizeof(T) == 2) {
-      r.v[2 * i] = __uint_as_float(w[i] << 16);
-      r.v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) r.v[i] = pair(w[i] << 16, w[i] & 0xffff0000u);
     } else {
-      r.v[i] = __uint_as_float(w[i]);
+      r.v[0] = pair(u.x, u.y);
+      r.v[1] = pair(u.z, u.w);
     }
   }
   return r;
 }
 template <typename T, int V>
 __device__ __forceinline__ void st_unit(T* p, const Unit<T, V>& x) {
-  uint4 u;
-  if constexpr (sizeof(T) == 2)
-    u = make_uint4(pack_bf16x2(x.v[0], x.v[1]), pack_bf16x2(x.v[2], x.v[3]), pack_bf16x2(x.v[4], x.v[5]),
-                   pack_bf16x2(x.v[6], x.v[7]));
-  else
-    u = make_uint4(__float_as_uint(x.v[0]), __float_as_uint(x.v[1]), __float_as_uint(x.v[2]), __float_as_uint(x.v[3]));
-  *reinterpret_cast<uint4*>(p) = u;
+  if constexpr (V == 1) {
+    *p = from_f<T>(lo_of(x.v[0]));
+  } else if constexpr (sizeof(T) == 2) {
+    *reinterpret_cast<uint4*>(p) =
+        make_uint4(pack_bf16x2(x.v[0]), pack_bf16x2(x.v[1]), pack_bf16x2(x.v[2]), pack_bf16x2(x.v[3]));
+  } else {
+    *reinterpret_cast<float4*>(p) = make_float4(lo_of(x.v[0]), hi_of(x.v[0]), lo_of(x.v[1]), hi_of(x.v[1]));
+  }
 }
+__device__ __forceinline__ f2 both(float x) { return pair(x, x); }
+__device__ __forceinline__ float sum_of(f2 x) { return lo_of(x) + hi_of(x); }
 
 struct GnParams {
   int N, L, C, G, cg;
   const void *x, *gate;
   const void *weight, *bias;  // [C] or nullptr
   int pbf;                    // weight and bias are bf16 (else fp32)
-  int act;                    // 0 identity, 1 silu
   float eps;
   void* y;
   float *mean, *rstd;         // [N][G]
@@ -78,31 +84,44 @@ __device__ __forceinline__ float gn_param(const void* p, int pbf, int c, float n
   if (!p) return none;
   return pbf ? __bfloat162float(__ldg(static_cast<const __nv_bfloat16*>(p) + c)) : __ldg(static_cast<const float*>(p) + c);
 }
-// (the approximate division is off by two steps at most and gives 0 for the infinite exp(-x) of x < -88)
-__device__ __forceinline__ float gn_sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
-
-// y for one value.
-template <bool GATE>
-__device__ __forceinline__ float gn_out(float t, float z, int act) {
-  if constexpr (GATE) return t * (act ? z * gn_sigmoid(z) : z);
-  return act ? t * gn_sigmoid(t) : t;
+// 1 / (1 + exp(-x)): the approximate exponential and reciprocal are off by a
+// few steps; an exp(-x) that overflows gives 0.
+__device__ __forceinline__ float gn_sigmoid1(float e) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(e));
+  return r;
 }
-// dL/dt for one value; dz: dL/dgate.
-template <bool GATE>
-__device__ __forceinline__ float gn_grad(float g, float t, float z, int act, float& dz) {
+__device__ __forceinline__ f2 gn_sigmoid(f2 x) {
+  const f2 e = mul2(x, both(-1.4426950408889634f));
+  const f2 d = add2(pair(gn_sigmoid1(lo_of(e)), gn_sigmoid1(hi_of(e))), both(1.f));
+  float a, b;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(a) : "f"(lo_of(d)));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(b) : "f"(hi_of(d)));
+  return pair(a, b);
+}
+
+// y of two values; ACT: silu, else identity.
+template <bool GATE, bool ACT>
+__device__ __forceinline__ f2 gn_out(f2 t, f2 z) {
+  if constexpr (GATE) return mul2(t, ACT ? mul2(z, gn_sigmoid(z)) : z);
+  return ACT ? mul2(t, gn_sigmoid(t)) : t;
+}
+// dL/dt of two values; dz: dL/dgate.  silu(z) = z s, silu'(z) = s + z s (1 - s).
+template <bool GATE, bool ACT>
+__device__ __forceinline__ f2 gn_grad(f2 g, f2 t, f2 z, f2& dz) {
   if constexpr (GATE) {
-    if (!act) {
-      dz = g * t;
-      return g * z;
+    if constexpr (!ACT) {
+      dz = mul2(g, t);
+      return mul2(g, z);
     }
-    const float s = gn_sigmoid(z);
-    dz = g * t * s * (1.f + z * (1.f - s));
-    return g * z * s;
+    const f2 s = gn_sigmoid(z), zs = mul2(z, s);
+    dz = mul2(mul2(g, t), fma2(zs, fma2(s, both(-1.f), both(1.f)), s));
+    return mul2(g, zs);
   }
-  dz = 0.f;
-  if (!act) return g;
-  const float s = gn_sigmoid(t);
-  return g * s * (1.f + t * (1.f - s));
+  dz = both(0.f);
+  if constexpr (!ACT) return g;
+  const f2 s = gn_sigmoid(t);
+  return mul2(g, fma2(mul2(t, s), fma2(s, both(-1.f), both(1.f)), s));
 }
 
 // Count, mean and sum of squares around it; joined exactly.
@@ -120,6 +139,27 @@ __device__ __forceinline__ Moments shfl_xor(const Moments& a, int off) {
                  __shfl_xor_sync(0xffffffffu, a.m2, off)};
 }
 
+// weight and bias of V channels from c.
+template <int V>
+struct GnParam {
+  static constexpr int P = V > 1 ? V / 2 : 1;
+  f2 w[P], b[P];
+  __device__ __forceinline__ GnParam(const GnParams& p, int c, bool on) {
+    float x[2 * P], y[2 * P];
+#pragma unroll
+    for (int e = 0; e < 2 * P; ++e) {
+      const bool has = on && (V > 1 || e == 0);
+      x[e] = has ? gn_param(p.weight, p.pbf, c + e, 1.f) : 1.f;
+      y[e] = has ? gn_param(p.bias, p.pbf, c + e, 0.f) : 0.f;
+    }
+#pragma unroll
+    for (int e = 0; e < P; ++e) {
+      w[e] = pair(x[2 * e], x[2 * e + 1]);
+      b[e] = pair(y[2 * e], y[2 * e + 1]);
+    }
+  }
+};
+
 // ------------------------------------------------- one position a sample ----
 // L = 1 and a group of 1, 2, 4 .. 32 units: the lanes of a group hold it in
 // registers, one unit a thread, so the values are read once.  A thread keeps
@@ -127,50 +167,42 @@ __device__ __forceinline__ Moments shfl_xor(const Moments& a, int off) {
 // in flight.  Block x: units [x width, (x + 1) width) of a row, `slots` rows at
 // a time where a row is narrow.
 // Measured (B200, 16384 x 2048 bf16 with a gate): 33 us, 6.1 TB/s.
-template <typename T, int V>
-struct GnParam {
-  float w[V], b[V];
-  __device__ __forceinline__ GnParam(const GnParams& p, int c, bool on) {
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      w[e] = on ? gn_param(p.weight, p.pbf, c + e, 1.f) : 1.f;
-      b[e] = on ? gn_param(p.bias, p.pbf, c + e, 0.f) : 0.f;
-    }
-  }
-};
-
-template <typename T, int V, bool GATE>
-__global__ void __launch_bounds__(256) gn_row_kernel(const GnParams p, int lanes) {
-  constexpr int R = GATE ? 4 : 6;
+template <typename T, int V, bool GATE, bool ACT>
+__global__ void __launch_bounds__(256, 4) gn_row_kernel(const GnParams p, int lanes) {
+  constexpr int R = GATE ? 2 : 3, P = V / 2;
   const int tid = threadIdx.x, slot = tid / p.width, u = blockIdx.x * p.width + tid % p.width;
   const bool on = slot < p.slots && u < p.C / V;
   const int c = on ? u * V : 0;
-  const GnParam<T, V> par(p, c, on);
+  const GnParam<V> par(p, c, on);
   const float inv = 1.f / static_cast<float>(p.cg);
-  const long long step = static_cast<long long>(gridDim.y) * p.slots;
-  const long long rounds = (p.N + step - 1) / step;  // the same for the whole block: warps meet in the shuffles
-  for (long long k0 = 0; k0 < rounds; k0 += R) {
+  const bool first = c % p.cg == 0;
+  const int g = c / p.cg, step = gridDim.y * p.slots, row0 = blockIdx.y * p.slots + slot;
+  const T* xp = static_cast<const T*>(p.x) + c;
+  const T* zp = static_cast<const T*>(p.gate) + c;
+  T* yp = static_cast<T*>(p.y) + c;
+  const int rounds = (p.N + step - 1) / step;  // the same for the whole block: warps meet in the shuffles
+  for (int k0 = 0; k0 < rounds; k0 += R) {
     Unit<T, V> x[R], z[R];
     long long n[R];
     bool ok[R];
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      n[i] = (k0 + i) * step + static_cast<long long>(blockIdx.y) * p.slots + slot;
+      n[i] = static_cast<long long>(k0 + i) * step + row0;
       ok[i] = on && n[i] < p.N;
-      if (ok[i]) {
-        x[i] = ld_unit<T, V>(static_cast<const T*>(p.x) + n[i] * p.C + c);
-        if constexpr (GATE) z[i] = ld_unit<T, V>(static_cast<const T*>(p.gate) + n[i] * p.C + c);
-      } else {
 #pragma unroll
-        for (int e = 0; e < V; ++e) x[i].v[e] = z[i].v[e] = 0.f;
+      for (int e = 0; e < P; ++e) x[i].v[e] = z[i].v[e] = both(0.f);
+      if (ok[i]) {
+        x[i] = ld_unit<T, V>(xp + n[i] * p.C);
+        if constexpr (GATE) z[i] = ld_unit<T, V>(zp + n[i] * p.C);
       }
     }
     float mean[R], q[R];
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      mean[i] = 0.f;
+      f2 s = x[i].v[0];
 #pragma unroll
-      for (int e = 0; e < V; ++e) mean[i] += x[i].v[e];
+      for (int e = 1; e < P; ++e) s = add2(s, x[i].v[e]);
+      mean[i] = sum_of(s);
     }
     for (int off = lanes >> 1; off > 0; off >>= 1)
 #pragma unroll
@@ -178,12 +210,13 @@ __global__ void __launch_bounds__(256) gn_row_kernel(const GnParams p, int lanes
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       mean[i] *= inv;
-      q[i] = 0.f;
+      f2 s = both(0.f);
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        x[i].v[e] -= mean[i];
-        q[i] = fmaf(x[i].v[e], x[i].v[e], q[i]);
+      for (int e = 0; e < P; ++e) {
+        x[i].v[e] = add2(x[i].v[e], both(-mean[i]));
+        s = fma2(x[i].v[e], x[i].v[e], s);
       }
+      q[i] = sum_of(s);
     }
     for (int off = lanes >> 1; off > 0; off >>= 1)
 #pragma unroll
@@ -194,12 +227,12 @@ __global__ void __launch_bounds__(256) gn_row_kernel(const GnParams p, int lanes
       const float rstd = rsqrtf(fmaf(q[i], inv, p.eps));
       Unit<T, V> y;
 #pragma unroll
-      for (int e = 0; e < V; ++e)
-        y.v[e] = gn_out<GATE>(fmaf(x[i].v[e] * rstd, par.w[e], par.b[e]), z[i].v[e], p.act);
-      st_unit<T, V>(static_cast<T*>(p.y) + n[i] * p.C + c, y);
-      if (c % p.cg == 0) {
-        p.mean[n[i] * p.G + c / p.cg] = mean[i];
-        p.rstd[n[i] * p.G + c / p.cg] = rstd;
+      for (int e = 0; e < P; ++e)
+        y.v[e] = gn_out<GATE, ACT>(fma2(mul2(x[i].v[e], both(rstd)), par.w[e], par.b[e]), z[i].v[e]);
+      st_unit<T, V>(yp + n[i] * p.C, y);
+      if (first) {
+        p.mean[n[i] * p.G + g] = mean[i];
+        p.rstd[n[i] * p.G + g] = rstd;
       }
     }
   }
@@ -207,59 +240,70 @@ __global__ void __launch_bounds__(256) gn_row_kernel(const GnParams p, int lanes
 
 // Its gradient: dw and db gather in registers over the thread's rows; the
 // block's sums go to part[2][gridDim.y][C].
-template <typename T, int V, bool GATE>
-__global__ void __launch_bounds__(256) gn_row_grad_kernel(const GnParams p, int lanes) {
-  constexpr int R = 2;
+template <typename T, int V, bool GATE, bool ACT>
+__global__ void __launch_bounds__(256, 3) gn_row_grad_kernel(const GnParams p, int lanes) {
+  constexpr int R = GATE ? 1 : 2, P = V / 2;
   __shared__ float red[2][256][V + 1];
   const int tid = threadIdx.x, slot = tid / p.width, u = blockIdx.x * p.width + tid % p.width;
   const bool on = slot < p.slots && u < p.C / V;
   const int c = on ? u * V : 0;
-  const GnParam<T, V> par(p, c, on);
-  float dw[V], db[V];
+  const GnParam<V> par(p, c, on);
+  f2 dw[P], db[P];
 #pragma unroll
-  for (int e = 0; e < V; ++e) dw[e] = db[e] = 0.f;
-  const int g = c / p.cg;
+  for (int e = 0; e < P; ++e) dw[e] = db[e] = both(0.f);
   const float inv = 1.f / static_cast<float>(p.cg);
-  const long long step = static_cast<long long>(gridDim.y) * p.slots;
-  const long long rounds = (p.N + step - 1) / step;
-  for (long long k0 = 0; k0 < rounds; k0 += R) {
-    Unit<T, V> x[R], z[R], gy[R];
-    float mean[R], rstd[R], s1[R], s2[R];
-    long long n[R];
-    bool ok[R];
+  const int g = c / p.cg, step = gridDim.y * p.slots, row0 = blockIdx.y * p.slots + slot;
+  const int rounds = (p.N + step - 1) / step;
+  // the rows of the round after this one, in flight
+  Unit<T, V> x[R], z[R], gy[R];
+  float mean[R], rstd[R];
+  bool ok[R];
+  auto fetch = [&](int k0) {
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      n[i] = (k0 + i) * step + static_cast<long long>(blockIdx.y) * p.slots + slot;
-      ok[i] = on && n[i] < p.N;
-      mean[i] = rstd[i] = s1[i] = s2[i] = 0.f;
+      const long long n = static_cast<long long>(k0 + i) * step + row0;
+      ok[i] = on && n < p.N;
+      mean[i] = rstd[i] = 0.f;
+#pragma unroll
+      for (int e = 0; e < P; ++e) x[i].v[e] = gy[i].v[e] = z[i].v[e] = both(0.f);
       if (ok[i]) {
-        const long long at = n[i] * p.C + c;
+        const long long at = n * p.C + c;
         x[i] = ld_unit<T, V>(static_cast<const T*>(p.x) + at);
         gy[i] = ld_unit<T, V>(static_cast<const T*>(p.gy) + at);
         if constexpr (GATE) z[i] = ld_unit<T, V>(static_cast<const T*>(p.gate) + at);
-        mean[i] = __ldg(p.mean + n[i] * p.G + g);
-        rstd[i] = __ldg(p.rstd + n[i] * p.G + g);
-      } else {
-#pragma unroll
-        for (int e = 0; e < V; ++e) x[i].v[e] = gy[i].v[e] = z[i].v[e] = 0.f;
+        mean[i] = __ldg(p.mean + n * p.G + g);
+        rstd[i] = __ldg(p.rstd + n * p.G + g);
       }
     }
+  };
+  fetch(0);
+  for (int k0 = 0; k0 < rounds; k0 += R) {
+    Unit<T, V> hat[R], dh[R];
+    float s1[R], s2[R], r[R];
+    bool now[R];
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       Unit<T, V> dz;
+      f2 a = both(0.f), b = both(0.f);
+      r[i] = rstd[i];
+      now[i] = ok[i];
+      const f2 r2 = both(rstd[i]), m2 = both(-mean[i]);
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const float hat = (x[i].v[e] - mean[i]) * rstd[i];
-        const float dt = gn_grad<GATE>(gy[i].v[e], fmaf(hat, par.w[e], par.b[e]), z[i].v[e], p.act, dz.v[e]);
-        dw[e] = fmaf(dt, hat, dw[e]);
-        db[e] += dt;
-        x[i].v[e] = hat;
-        gy[i].v[e] = dt * par.w[e];
-        s1[i] += gy[i].v[e];
-        s2[i] = fmaf(gy[i].v[e], hat, s2[i]);
+      for (int e = 0; e < P; ++e) {
+        hat[i].v[e] = mul2(add2(x[i].v[e], m2), r2);
+        const f2 dt = gn_grad<GATE, ACT>(gy[i].v[e], fma2(hat[i].v[e], par.w[e], par.b[e]), z[i].v[e], dz.v[e]);
+        dw[e] = fma2(dt, hat[i].v[e], dw[e]);
+        db[e] = add2(db[e], dt);
+        dh[i].v[e] = mul2(dt, par.w[e]);
+        a = add2(a, dh[i].v[e]);
+        b = fma2(dh[i].v[e], hat[i].v[e], b);
       }
-      if (GATE && ok[i]) st_unit<T, V>(static_cast<T*>(p.ggate) + n[i] * p.C + c, dz);
+      s1[i] = sum_of(a);
+      s2[i] = sum_of(b);
+      const long long n = static_cast<long long>(k0 + i) * step + row0;
+      if (GATE && now[i]) st_unit<T, V>(static_cast<T*>(p.ggate) + n * p.C + c, dz);
     }
+    if (k0 + R < rounds) fetch(k0 + R);
     for (int off = lanes >> 1; off > 0; off >>= 1)
 #pragma unroll
       for (int i = 0; i < R; ++i) {
@@ -268,18 +312,22 @@ __global__ void __launch_bounds__(256) gn_row_grad_kernel(const GnParams p, int 
       }
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      if (!ok[i]) continue;
+      if (!now[i]) continue;
+      const long long n = static_cast<long long>(k0 + i) * step + row0;
+      const f2 a = both(-s1[i] * inv), b = both(-s2[i] * inv), r2 = both(r[i]);
       Unit<T, V> dx;
 #pragma unroll
-      for (int e = 0; e < V; ++e) dx.v[e] = rstd[i] * (gy[i].v[e] - s1[i] * inv - x[i].v[e] * (s2[i] * inv));
-      st_unit<T, V>(static_cast<T*>(p.gx) + n[i] * p.C + c, dx);
+      for (int e = 0; e < P; ++e) dx.v[e] = mul2(r2, fma2(hat[i].v[e], b, add2(dh[i].v[e], a)));
+      st_unit<T, V>(static_cast<T*>(p.gx) + n * p.C + c, dx);
     }
   }
   if (!p.part) return;
 #pragma unroll
-  for (int e = 0; e < V; ++e) {
-    red[0][tid][e] = dw[e];
-    red[1][tid][e] = db[e];
+  for (int e = 0; e < P; ++e) {
+    red[0][tid][2 * e] = lo_of(dw[e]);
+    red[0][tid][2 * e + 1] = hi_of(dw[e]);
+    red[1][tid][2 * e] = lo_of(db[e]);
+    red[1][tid][2 * e + 1] = hi_of(db[e]);
   }
   __syncthreads();
   for (int i = tid; i < 2 * p.width * V; i += blockDim.x) {
@@ -351,44 +399,61 @@ __global__ void __launch_bounds__(256) gn_stats_kernel(const GnParams p) {
   const T* x = static_cast<const T*>(p.x) + static_cast<size_t>(n) * p.L * p.C;
   for (int u0 = 0; u0 < cv; u0 += 256) {
     const int width = min(cv - u0, 256), slots = 256 / width, slot = tid / width, u = u0 + tid % width;
-    float cnt = 0.f, mean[V], m2[V];
+    constexpr int P = Unit<T, V>::P, U = V == 8 ? 4 : 8;  // U: positions per batch, all in flight
+    float cnt = 0.f;
+    f2 mean[P], m2[P];
 #pragma unroll
-    for (int e = 0; e < V; ++e) mean[e] = m2[e] = 0.f;
+    for (int e = 0; e < P; ++e) mean[e] = m2[e] = both(0.f);
     if (slot < slots) {
-      constexpr int U = 32 / V;  // positions per batch: 128 bytes a thread in flight (fp32), 64 (bf16)
-      for (int l = l0 + slot; l < l1; l += U * slots) {
+      const T* xu = x + u * V;
+      int l = l0 + slot;
+      // `h` positions in b: their own mean and squares, joined to what is there
+      auto take = [&](const Unit<T, V>(&b)[U], int have) {
+        const float h = static_cast<float>(have), inv = 1.f / h, f = h / (cnt + h), cf = cnt * f;
+#pragma unroll
+        for (int e = 0; e < P; ++e) {
+          f2 s = b[0].v[e], q = both(0.f);
+#pragma unroll
+          for (int i = 1; i < U; ++i)
+            if (i < have) s = add2(s, b[i].v[e]);
+          s = mul2(s, both(inv));
+          const f2 neg = mul2(s, both(-1.f));
+#pragma unroll
+          for (int i = 0; i < U; ++i)
+            if (i < have) {
+              const f2 d = add2(b[i].v[e], neg);
+              q = fma2(d, d, q);
+            }
+          const f2 d = fma2(mean[e], both(-1.f), s);
+          mean[e] = fma2(d, both(f), mean[e]);
+          m2[e] = add2(m2[e], fma2(mul2(d, d), both(cf), q));
+        }
+        cnt += h;
+      };
+      for (; l + (U - 1) * slots < l1; l += U * slots) {
+        Unit<T, V> b[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) b[i] = ld_unit<T, V>(xu + static_cast<size_t>(l + i * slots) * p.C);
+        take(b, U);
+      }
+      if (l < l1) {
         Unit<T, V> b[U];
         int have = 0;
 #pragma unroll
         for (int i = 0; i < U; ++i)
           if (l + i * slots < l1) {
-            b[i] = ld_unit<T, V>(x + static_cast<size_t>(l + i * slots) * p.C + u * V);
+            b[i] = ld_unit<T, V>(xu + static_cast<size_t>(l + i * slots) * p.C);
             ++have;
           }
-        const float h = static_cast<float>(have), inv = 1.f / h, f = h / (cnt + h);
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-          float s = 0.f, q = 0.f;
-#pragma unroll
-          for (int i = 0; i < U; ++i)
-            if (i < have) s += b[i].v[e];
-          s *= inv;
-#pragma unroll
-          for (int i = 0; i < U; ++i)
-            if (i < have) q = fmaf(b[i].v[e] - s, b[i].v[e] - s, q);
-          const float d = s - mean[e];
-          mean[e] = fmaf(d, f, mean[e]);
-          m2[e] += q + d * d * cnt * f;
-        }
-        cnt += h;
+        take(b, have);
       }
     }
     __syncthreads();
     counts[tid] = cnt;
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-      each[0][tid][e] = mean[e];
-      each[1][tid][e] = m2[e];
+      each[0][tid][e] = e & 1 ? hi_of(mean[e / 2]) : lo_of(mean[e / 2]);
+      each[1][tid][e] = e & 1 ? hi_of(m2[e / 2]) : lo_of(m2[e / 2]);
     }
     __syncthreads();
     // a warp for each group that these channels touch
@@ -441,9 +506,22 @@ __global__ void __launch_bounds__(256) gn_join_kernel(const GnParams p) {
   }
 }
 
+// A sample's statistics for V channels from c, whose groups may differ.
+template <int V>
+struct GnStat {
+  static constexpr int P = V > 1 ? V / 2 : 1;
+  f2 v[P];
+  __device__ __forceinline__ GnStat(const float* s, int stride, int c, int cg) {
+#pragma unroll
+    for (int e = 0; e < P; ++e)
+      v[e] = pair(__ldg(s + stride * ((c + 2 * e) / cg)), V > 1 ? __ldg(s + stride * ((c + 2 * e + 1) / cg)) : 0.f);
+  }
+};
+
 // y from mean and rstd.
-template <typename T, int V, bool GATE>
+template <typename T, int V, bool GATE, bool ACT>
 __global__ void __launch_bounds__(256) gn_apply_kernel(const GnParams p) {
+  constexpr int P = Unit<T, V>::P;
   const int tid = threadIdx.x, n = blockIdx.x / p.parts, part = blockIdx.x % p.parts, cv = p.C / V;
   int l0, l1;
   gn_rows(p.L, p.part_rows, part, l0, l1);
@@ -452,13 +530,13 @@ __global__ void __launch_bounds__(256) gn_apply_kernel(const GnParams p) {
     const int width = min(cv - u0, 256), slots = 256 / width, slot = tid / width, u = u0 + tid % width;
     if (slot >= slots) continue;
     const int c = u * V;
-    const GnParam<T, V> par(p, c, true);
-    float k[V], mean[V];  // t = (x - mean) k + b
+    GnParam<V> par(p, c, true);  // t = (x - mean) w + b, rstd in w
+    const GnStat<V> mean(p.mean + static_cast<size_t>(n) * p.G, 1, c, p.cg), rstd(p.rstd + static_cast<size_t>(n) * p.G, 1, c, p.cg);
+    f2 neg[P];
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-      const size_t at = static_cast<size_t>(n) * p.G + (c + e) / p.cg;
-      mean[e] = __ldg(p.mean + at);
-      k[e] = __ldg(p.rstd + at) * par.w[e];
+    for (int e = 0; e < P; ++e) {
+      neg[e] = mul2(mean.v[e], both(-1.f));
+      par.w[e] = mul2(par.w[e], rstd.v[e]);
     }
 #pragma unroll 4
     for (int l = l0 + slot; l < l1; l += slots) {
@@ -467,7 +545,7 @@ __global__ void __launch_bounds__(256) gn_apply_kernel(const GnParams p) {
       Unit<T, V> z = x, y;
       if constexpr (GATE) z = ld_unit<T, V>(static_cast<const T*>(p.gate) + at);
 #pragma unroll
-      for (int e = 0; e < V; ++e) y.v[e] = gn_out<GATE>(fmaf(x.v[e] - mean[e], k[e], par.b[e]), z.v[e], p.act);
+      for (int e = 0; e < P; ++e) y.v[e] = gn_out<GATE, ACT>(fma2(add2(x.v[e], neg[e]), par.w[e], par.b[e]), z.v[e]);
       st_unit<T, V>(static_cast<T*>(p.y) + at, y);
     }
   }
@@ -475,8 +553,9 @@ __global__ void __launch_bounds__(256) gn_apply_kernel(const GnParams p) {
 
 // Gradient, first pass: part[2][N][splits][C], the sums of dt hat and of dt
 // over a split's positions; also dgate.
-template <typename T, int V, bool GATE>
+template <typename T, int V, bool GATE, bool ACT>
 __global__ void __launch_bounds__(256) gn_grad_sums_kernel(const GnParams p) {
+  constexpr int P = Unit<T, V>::P;
   __shared__ float red[2][256][V + 1];
   const int tid = threadIdx.x, n = blockIdx.x / p.splits, part = blockIdx.x % p.splits, cv = p.C / V;
   int l0, l1;
@@ -484,19 +563,13 @@ __global__ void __launch_bounds__(256) gn_grad_sums_kernel(const GnParams p) {
   const size_t base = static_cast<size_t>(n) * p.L * p.C, all = static_cast<size_t>(p.N) * p.splits * p.C;
   for (int u0 = 0; u0 < cv; u0 += 256) {
     const int width = min(cv - u0, 256), slots = 256 / width, slot = tid / width, u = u0 + tid % width;
-    float dw[V], db[V];
+    f2 dw[P], db[P];
 #pragma unroll
-    for (int e = 0; e < V; ++e) dw[e] = db[e] = 0.f;
+    for (int e = 0; e < P; ++e) dw[e] = db[e] = both(0.f);
     if (slot < slots) {
       const int c = u * V;
-      const GnParam<T, V> par(p, c, true);
-      float mean[V], rstd[V];
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const size_t at = static_cast<size_t>(n) * p.G + (c + e) / p.cg;
-        mean[e] = __ldg(p.mean + at);
-        rstd[e] = __ldg(p.rstd + at);
-      }
+      const GnParam<V> par(p, c, true);
+      const GnStat<V> mean(p.mean + static_cast<size_t>(n) * p.G, 1, c, p.cg), rstd(p.rstd + static_cast<size_t>(n) * p.G, 1, c, p.cg);
 #pragma unroll 4
       for (int l = l0 + slot; l < l1; l += slots) {
         const size_t at = base + static_cast<size_t>(l) * p.C + c;
@@ -505,11 +578,11 @@ __global__ void __launch_bounds__(256) gn_grad_sums_kernel(const GnParams p) {
         Unit<T, V> z = x, dz;
         if constexpr (GATE) z = ld_unit<T, V>(static_cast<const T*>(p.gate) + at);
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          const float hat = (x.v[e] - mean[e]) * rstd[e];
-          const float dt = gn_grad<GATE>(gy.v[e], fmaf(hat, par.w[e], par.b[e]), z.v[e], p.act, dz.v[e]);
-          dw[e] = fmaf(dt, hat, dw[e]);
-          db[e] += dt;
+        for (int e = 0; e < P; ++e) {
+          const f2 hat = mul2(fma2(mean.v[e], both(-1.f), x.v[e]), rstd.v[e]);
+          const f2 dt = gn_grad<GATE, ACT>(gy.v[e], fma2(hat, par.w[e], par.b[e]), z.v[e], dz.v[e]);
+          dw[e] = fma2(dt, hat, dw[e]);
+          db[e] = add2(db[e], dt);
         }
         if constexpr (GATE) st_unit<T, V>(static_cast<T*>(p.ggate) + at, dz);
       }
@@ -517,8 +590,8 @@ __global__ void __launch_bounds__(256) gn_grad_sums_kernel(const GnParams p) {
     __syncthreads();
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-      red[0][tid][e] = dw[e];
-      red[1][tid][e] = db[e];
+      red[0][tid][e] = e & 1 ? hi_of(dw[e / 2]) : lo_of(dw[e / 2]);
+      red[1][tid][e] = e & 1 ? hi_of(db[e / 2]) : lo_of(db[e / 2]);
     }
     __syncthreads();
     for (int i = tid; i < 2 * width * V; i += 256) {
@@ -547,15 +620,21 @@ __global__ void __launch_bounds__(256) gn_grad_groups_kernel(const GnParams p, f
   const size_t all = static_cast<size_t>(p.N) * p.splits * p.C;
   const float* at = p.part + n * p.splits * p.C + g * p.cg;
   float s1 = 0.f, s2 = 0.f;
-  const long long items = static_cast<long long>(p.splits) * p.cg;
+  // lanes over the group's channels and, where those are few, over the splits
+  const int across = min(p.cg, 32), per = 32 / across, k0 = lane / across;
+  if (k0 < per)
+    for (int c = lane % across; c < p.cg; c += across) {
+      float t1 = 0.f, t2 = 0.f;
 #pragma unroll 8
-  for (long long e = lane; e < items; e += 32) {
-    const int k = static_cast<int>(e / p.cg), c = static_cast<int>(e % p.cg);
-    const float w = gn_param(p.weight, p.pbf, g * p.cg + c, 1.f);
-    const float* q = at + static_cast<size_t>(k) * p.C + c;
-    s2 = fmaf(w, __ldg(q), s2);
-    s1 = fmaf(w, __ldg(q + all), s1);
-  }
+      for (int k = k0; k < p.splits; k += per) {
+        const float* q = at + static_cast<size_t>(k) * p.C + c;
+        t2 += __ldg(q);
+        t1 += __ldg(q + all);
+      }
+      const float w = gn_param(p.weight, p.pbf, g * p.cg + c, 1.f);
+      s1 = fmaf(w, t1, s1);
+      s2 = fmaf(w, t2, s2);
+    }
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) {
     s1 += __shfl_xor_sync(0xffffffffu, s1, off);
@@ -569,25 +648,24 @@ __global__ void __launch_bounds__(256) gn_grad_groups_kernel(const GnParams p, f
 }
 
 // Gradient, third pass: dx.
-template <typename T, int V, bool GATE>
+template <typename T, int V, bool GATE, bool ACT>
 __global__ void __launch_bounds__(256) gn_grad_apply_kernel(const GnParams p, const float* __restrict__ sums) {
+  constexpr int P = Unit<T, V>::P;
   const int tid = threadIdx.x, n = blockIdx.x / p.parts, part = blockIdx.x % p.parts, cv = p.C / V;
   int l0, l1;
   gn_rows(p.L, p.part_rows, part, l0, l1);
-  const size_t base = static_cast<size_t>(n) * p.L * p.C;
+  const size_t base = static_cast<size_t>(n) * p.L * p.C, ng = static_cast<size_t>(n) * p.G;
   for (int u0 = 0; u0 < cv; u0 += 256) {
     const int width = min(cv - u0, 256), slots = 256 / width, slot = tid / width, u = u0 + tid % width;
     if (slot >= slots) continue;
     const int c = u * V;
-    const GnParam<T, V> par(p, c, true);
-    float mean[V], rstd[V], s1[V], s2[V];
+    const GnParam<V> par(p, c, true);
+    const GnStat<V> mean(p.mean + ng, 1, c, p.cg), rstd(p.rstd + ng, 1, c, p.cg);
+    GnStat<V> s1(sums + 2 * ng, 2, c, p.cg), s2(sums + 2 * ng + 1, 2, c, p.cg);
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-      const size_t ng = static_cast<size_t>(n) * p.G + (c + e) / p.cg;
-      mean[e] = __ldg(p.mean + ng);
-      rstd[e] = __ldg(p.rstd + ng);
-      s1[e] = __ldg(sums + 2 * ng);
-      s2[e] = __ldg(sums + 2 * ng + 1);
+    for (int e = 0; e < P; ++e) {
+      s1.v[e] = mul2(s1.v[e], both(-1.f));
+      s2.v[e] = mul2(s2.v[e], both(-1.f));
     }
 #pragma unroll 2
     for (int l = l0 + slot; l < l1; l += slots) {
@@ -597,11 +675,11 @@ __global__ void __launch_bounds__(256) gn_grad_apply_kernel(const GnParams p, co
       Unit<T, V> z = x, dx;
       if constexpr (GATE) z = ld_unit<T, V>(static_cast<const T*>(p.gate) + at);
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const float hat = (x.v[e] - mean[e]) * rstd[e];
-        float dz;
-        const float dt = gn_grad<GATE>(gy.v[e], fmaf(hat, par.w[e], par.b[e]), z.v[e], p.act, dz);
-        dx.v[e] = rstd[e] * (fmaf(dt, par.w[e], -s1[e]) - hat * s2[e]);
+      for (int e = 0; e < P; ++e) {
+        const f2 hat = mul2(fma2(mean.v[e], both(-1.f), x.v[e]), rstd.v[e]);
+        f2 dz;
+        const f2 dt = gn_grad<GATE, ACT>(gy.v[e], fma2(hat, par.w[e], par.b[e]), z.v[e], dz);
+        dx.v[e] = mul2(rstd.v[e], fma2(hat, s2.v[e], fma2(dt, par.w[e], s1.v[e])));
       }
       st_unit<T, V>(static_cast<T*>(p.gx) + at, dx);
     }

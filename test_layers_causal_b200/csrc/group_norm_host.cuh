@@ -5,12 +5,17 @@
 
 namespace {
 
-int gn_unit(int dtype) { return dtype == TTT_LA_F32 ? 4 : 8; }  // values in 16 bytes
+// Values a thread reads at once: 16 bytes, or one where rows do not all start
+// on 16 bytes.
+int gn_unit(int C, int dtype) {
+  const int v = dtype == TTT_LA_F32 ? 4 : 8;
+  return C % v == 0 ? v : 1;
+}
 
 // One position a sample and a group of 1, 2, 4 .. 32 units: the kernels that
 // hold a group in registers.
 int gn_row_lanes(int L, int cg, int dtype) {
-  const int v = gn_unit(dtype), lanes = cg / v;
+  const int v = dtype == TTT_LA_F32 ? 4 : 8, lanes = cg / v;
   return L == 1 && cg % v == 0 && lanes <= 32 && (lanes & (lanes - 1)) == 0 ? lanes : 0;
 }
 
@@ -35,7 +40,7 @@ void gn_split(int N, int L, int C, int dtype, int per_sm, int* parts, int* rows)
 // Blocks of up to 256 threads over the units of a row (wide rows in equal
 // columns, narrow ones several at a time) and `per_sm` of them for each SM.
 void gn_row_plan(GnPlan* p, int N, int C, int dtype, int per_sm) {
-  const int cv = C / gn_unit(dtype);
+  const int cv = C / gn_unit(C, dtype);
   p->columns = (cv + 255) / 256;
   // (whole warps, so that a group's lanes stay in one)
   p->width = p->columns == 1 ? cv : ((cv + p->columns - 1) / p->columns + 31) / 32 * 32;
@@ -49,11 +54,11 @@ GnPlan gn_plan_forward(int N, int L, int C, int G, int dtype) {
   GnPlan p = {};
   p.lanes = gn_row_lanes(L, C / G, dtype);
   if (p.lanes) {
-    gn_row_plan(&p, N, C, dtype, 8);
+    gn_row_plan(&p, N, C, dtype, 4);
     return p;
   }
-  gn_split(N, L, C, dtype, 4, &p.splits, &p.rows);
-  gn_split(N, L, C, dtype, 8, &p.parts, &p.part_rows);
+  gn_split(N, L, C, dtype, 3, &p.splits, &p.rows);
+  gn_split(N, L, C, dtype, 6, &p.parts, &p.part_rows);
   p.floats = p.splits > 1 ? static_cast<size_t>(N) * p.splits * G * 2 : 0;
   return p;
 }
@@ -66,7 +71,7 @@ GnPlan gn_plan_backward(int N, int L, int C, int G, int dtype, bool params) {
     return p;
   }
   gn_split(N, L, C, dtype, 3, &p.splits, &p.rows);
-  gn_split(N, L, C, dtype, 8, &p.parts, &p.part_rows);
+  gn_split(N, L, C, dtype, 6, &p.parts, &p.part_rows);
   p.floats = static_cast<size_t>(2) * N * p.splits * C + static_cast<size_t>(2) * N * G;
   return p;
 }
@@ -77,21 +82,23 @@ ttt_la_status check_gn(int N, int L, int C, int G, int dtype, int param_dtype, i
     return TTT_LA_ERR_INVALID_ARG;
   if (act != 0 && act != 1) return TTT_LA_ERR_INVALID_ARG;
   if (static_cast<long long>(N) * L > (1ll << 40) / C) return TTT_LA_ERR_INVALID_ARG;
-  // rows of a sample start on 16 bytes, and a block's table of the groups fits in shared memory
-  if (C % (dtype == TTT_LA_F32 ? 4 : 8) || G > 4096) return TTT_LA_ERR_UNSUPPORTED;
+  if (G > 4096) return TTT_LA_ERR_UNSUPPORTED;  // a block's table of the groups fits in shared memory
   return TTT_LA_OK;
 }
 
 bool gn_aligned(const void* p, int dtype) { return reinterpret_cast<uintptr_t>(p) % (dtype == TTT_LA_F32 ? 4 : 2) == 0; }
 
 template <typename F>
-ttt_la_status gn_dispatch(int dtype, bool gate, F&& f) {
-  // f(type tag, values of a unit, gate)
+ttt_la_status gn_dispatch(int dtype, int unit, bool gate, bool act, F&& f) {
+  // f(type tag, values of a unit, gate, silu)
+  auto with = [&](auto t, auto u) {
+    if (gate) return act ? f(t, u, std::true_type{}, std::true_type{}) : f(t, u, std::true_type{}, std::false_type{});
+    return act ? f(t, u, std::false_type{}, std::true_type{}) : f(t, u, std::false_type{}, std::false_type{});
+  };
   if (dtype == TTT_LA_F32)
-    return gate ? f(float{}, std::integral_constant<int, 4>{}, std::true_type{})
-                : f(float{}, std::integral_constant<int, 4>{}, std::false_type{});
-  return gate ? f(__nv_bfloat16{}, std::integral_constant<int, 8>{}, std::true_type{})
-              : f(__nv_bfloat16{}, std::integral_constant<int, 8>{}, std::false_type{});
+    return unit > 1 ? with(float{}, std::integral_constant<int, 4>{}) : with(float{}, std::integral_constant<int, 1>{});
+  using bf = __nv_bfloat16;
+  return unit > 1 ? with(bf{}, std::integral_constant<int, 8>{}) : with(bf{}, std::integral_constant<int, 1>{});
 }
 
 void gn_fill(ttt::GnParams* p, const GnPlan& pl) {
@@ -126,19 +133,21 @@ ttt_la_status ttt_la_group_norm(const ttt_la_group_norm_args* a, void* stream) {
   p.N = a->N, p.L = a->L, p.C = a->C, p.G = a->G, p.cg = a->C / a->G;
   p.x = a->x, p.gate = a->gate, p.weight = a->weight, p.bias = a->bias;
   p.pbf = a->param_dtype == TTT_LA_BF16;
-  p.act = a->activation, p.eps = a->eps;
+  p.eps = a->eps;
   p.y = a->y, p.mean = a->mean, p.rstd = a->rstd;
   p.part = static_cast<float*>(a->workspace);
   gn_fill(&p, pl);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return gn_dispatch(a->dtype, a->gate != nullptr, [&](auto t, auto u, auto gate) -> ttt_la_status {
+  return gn_dispatch(a->dtype, gn_unit(a->C, a->dtype), a->gate != nullptr, a->activation == 1,
+                     [&](auto t, auto u, auto gate, auto act) -> ttt_la_status {
     using T = decltype(t);
     constexpr int V = decltype(u)::value;
-    constexpr bool GATE = decltype(gate)::value;
-    if (pl.lanes) {
-      ttt::gn_row_kernel<T, V, GATE><<<dim3(pl.columns, pl.blocks), gn_row_threads(pl), 0, st>>>(p, pl.lanes);
-      return launched();
-    }
+    constexpr bool GATE = decltype(gate)::value, ACT = decltype(act)::value;
+    if constexpr (V > 1)
+      if (pl.lanes) {
+        ttt::gn_row_kernel<T, V, GATE, ACT><<<dim3(pl.columns, pl.blocks), gn_row_threads(pl), 0, st>>>(p, pl.lanes);
+        return launched();
+      }
     const long long sums = static_cast<long long>(a->N) * pl.splits, parts = static_cast<long long>(a->N) * pl.parts;
     if (parts >= (1ll << 31) || sums >= (1ll << 31)) return TTT_LA_ERR_UNSUPPORTED;
     const int sm = a->G * static_cast<int>(sizeof(ttt::Moments));
@@ -152,7 +161,7 @@ ttt_la_status ttt_la_group_norm(const ttt_la_group_norm_args* a, void* stream) {
       r = launch_kernel(ttt::gn_join_kernel, static_cast<int>((warps * 32 + 255) / 256), 256, 0, st, false, p);
       if (r != TTT_LA_OK) return r;
     }
-    return launch_kernel(ttt::gn_apply_kernel<T, V, GATE>, static_cast<int>(parts), 256, 0, st, false, p);
+    return launch_kernel(ttt::gn_apply_kernel<T, V, GATE, ACT>, static_cast<int>(parts), 256, 0, st, false, p);
   });
 }
 
@@ -185,29 +194,30 @@ ttt_la_status ttt_la_group_norm_backward(const ttt_la_group_norm_grad_args* a, v
   p.N = a->N, p.L = a->L, p.C = a->C, p.G = a->G, p.cg = a->C / a->G;
   p.x = a->x, p.gate = a->gate, p.weight = a->weight, p.bias = a->bias;
   p.pbf = a->param_dtype == TTT_LA_BF16;
-  p.act = a->activation;
   p.mean = const_cast<float*>(a->mean), p.rstd = const_cast<float*>(a->rstd);
   p.gy = a->grad_y, p.gx = a->grad_x, p.ggate = a->grad_gate;
   p.gw = a->grad_weight, p.gb = a->grad_bias;
   p.part = pl.floats ? static_cast<float*>(a->workspace) : nullptr;
   gn_fill(&p, pl);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return gn_dispatch(a->dtype, a->gate != nullptr, [&](auto t, auto u, auto gate) -> ttt_la_status {
+  return gn_dispatch(a->dtype, gn_unit(a->C, a->dtype), a->gate != nullptr, a->activation == 1,
+                     [&](auto t, auto u, auto gate, auto act) -> ttt_la_status {
     using T = decltype(t);
     constexpr int V = decltype(u)::value;
-    constexpr bool GATE = decltype(gate)::value;
-    if (pl.lanes) {
-      ttt::gn_row_grad_kernel<T, V, GATE><<<dim3(pl.columns, pl.blocks), gn_row_threads(pl), 0, st>>>(p, pl.lanes);
-      const ttt_la_status r = launched();
-      if (r != TTT_LA_OK || !params) return r;
-      ttt::gn_param_grad_kernel<<<dim3((a->C + 31) / 32, 2), 256, 0, st>>>(p.part, pl.blocks, a->C, a->grad_weight,
-                                                                          a->grad_bias, p.pbf);
-      return launched();
-    }
+    constexpr bool GATE = decltype(gate)::value, ACT = decltype(act)::value;
+    if constexpr (V > 1)
+      if (pl.lanes) {
+        ttt::gn_row_grad_kernel<T, V, GATE, ACT><<<dim3(pl.columns, pl.blocks), gn_row_threads(pl), 0, st>>>(p, pl.lanes);
+        const ttt_la_status r = launched();
+        if (r != TTT_LA_OK || !params) return r;
+        ttt::gn_param_grad_kernel<<<dim3((a->C + 31) / 32, 2), 256, 0, st>>>(p.part, pl.blocks, a->C, a->grad_weight,
+                                                                            a->grad_bias, p.pbf);
+        return launched();
+      }
     const long long rows = static_cast<long long>(a->N) * pl.splits, parts = static_cast<long long>(a->N) * pl.parts;
     if (parts >= (1ll << 31) || rows >= (1ll << 31)) return TTT_LA_ERR_UNSUPPORTED;
     float* sums = p.part + static_cast<size_t>(2) * rows * a->C;
-    ttt_la_status r = launch_kernel(ttt::gn_grad_sums_kernel<T, V, GATE>, static_cast<int>(rows), 256, 0, st, false, p);
+    ttt_la_status r = launch_kernel(ttt::gn_grad_sums_kernel<T, V, GATE, ACT>, static_cast<int>(rows), 256, 0, st, false, p);
     if (r != TTT_LA_OK) return r;
     const long long warp_blocks = (static_cast<long long>(a->N) * a->G + 7) / 8;
     const long long blocks = warp_blocks + (params ? 2 * ((a->C + 31) / 32) : 0);
@@ -215,7 +225,7 @@ ttt_la_status ttt_la_group_norm_backward(const ttt_la_group_norm_grad_args* a, v
     r = launch_kernel(ttt::gn_grad_groups_kernel, static_cast<int>(blocks), 256, 0, st, false, p, sums,
                       static_cast<int>(warp_blocks));
     if (r != TTT_LA_OK) return r;
-    return launch_kernel(ttt::gn_grad_apply_kernel<T, V, GATE>, static_cast<int>(parts), 256, 0, st, false, p, sums);
+    return launch_kernel(ttt::gn_grad_apply_kernel<T, V, GATE, ACT>, static_cast<int>(parts), 256, 0, st, false, p, sums);
   });
 }
 

@@ -44,6 +44,11 @@ CASES = [
     ((5, 7, 8192), 4096, "bf16", "f32", True, "silu", 0.0),     # the most groups
     ((70, 1, 3200), 25, "bf16", "f32", True, "silu", 0.0),      # a row in two columns of blocks
     ((11, 1, 192), 8, "bf16", "f32", True, None, 0.0),          # three units a group: not a power of two
+    ((3, 77, 3), 1, "bf16", "bf16", True, "silu", 0.0),         # rows that do not start on 16 bytes
+    ((2, 501, 10), 2, "bf16", "f32", False, "silu", 1.0),
+    ((5, 1, 7), 7, "f32", None, False, None, 0.0),
+    ((2, 33, 2), 1, "f32", "f32", True, "silu", 0.0),
+    ((4, 2, 301), 1, "bf16", "f32", True, None, 0.0),
     ((40, 1, 192), 24, "bf16", "bf16", False, "silu", 0.0),     # one unit a group, rows side by side in a block
 ]
 
