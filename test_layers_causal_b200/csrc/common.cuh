@@ -119,6 +119,32 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint64
   }
 }
 
+// ------------------------------------------- programmatic launches ----
+// A kernel launched programmatically (launch_after on the host) starts when
+// every block of the kernel before it has called launch_next or ended.  Before
+// it touches what that kernel writes it calls wait_before, which returns when
+// that kernel is complete; every block does so before it ends, so that a
+// kernel's completion is also its predecessors'.
+__device__ __forceinline__ void launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Loads (through L2) of what that kernel wrote.  Volatile, so that they stay
+// behind the wait: the compiler may move __ldcg and __ldg across it.
+__device__ __forceinline__ float ld_after(const float* p) {
+  float x;
+  asm volatile("ld.global.cg.f32 %0, [%1];" : "=f"(x) : "l"(p));
+  return x;
+}
+__device__ __forceinline__ float2 ld_after(const float2* p) {
+  float2 x;
+  asm volatile("ld.global.cg.v2.f32 {%0, %1}, [%2];" : "=f"(x.x), "=f"(x.y) : "l"(p));
+  return x;
+}
+__device__ __forceinline__ float4 ld_after(const float4* p) {
+  float4 x;
+  asm volatile("ld.global.cg.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "l"(p));
+  return x;
+}
+
 // ------------------------------------------------------------------ TMA ----
 __device__ __forceinline__ void prefetch_tmap(const CUtensorMap* m) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
@@ -167,6 +193,14 @@ __device__ __forceinline__ void tma_store_3d_hint(const CUtensorMap* m, const vo
           reinterpret_cast<uint64_t>(m)),
       "r"(smem_u32(src)), "r"(x), "r"(y), "r"(z), "l"(policy)
       : "memory");
+}
+// Untiled copy of `bytes` contiguous bytes (a multiple of 16, as both
+// addresses) into shared memory, completion counted in bytes on `bar`.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
 }
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait_read0() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
@@ -322,6 +356,13 @@ __device__ __forceinline__ uint32_t sw128_off(uint32_t row, uint32_t c16) {
 // registers of a generic pointer).
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
+// 16-byte load from a shared-memory address, kept in place among barriers and fences.
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
+  uint4 x;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(addr) : "memory");
+  return x;
 }
 
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {

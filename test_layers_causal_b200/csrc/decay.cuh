@@ -186,6 +186,8 @@ template <bool FINAL>
 __global__ void __launch_bounds__(256) decay_scan_kernel(const DecayScans ps, const float* __restrict__ log_decay) {
   const DecayScan& p = ps.s[blockIdx.y];
   const DecayGeom& g = p.g;
+  launch_next();
+  wait_before();
   const size_t dd = static_cast<size_t>(p.dv) * p.dk;
   const int slices = static_cast<int>((dd / 4 + blockDim.x - 1) / blockDim.x);
   const int h = (blockIdx.x / slices) % g.H, n = blockIdx.x / slices / g.H;
@@ -219,7 +221,7 @@ __global__ void __launch_bounds__(256) decay_scan_kernel(const DecayScans ps, co
     for (int u = 0; u < U; ++u) {
       const int i = i0 + u, j = p.rev ? nseg - 1 - i : i;
       // (segments past the bound, of offsets that overlap, have no slot)
-      if (i < sums && first + j < g.nseg) t[u] = __ldcg(reinterpret_cast<const float4*>(w + j * pitch));
+      if (i < sums && first + j < g.nseg) t[u] = ld_after(reinterpret_cast<const float4*>(w + j * pitch));
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {

@@ -81,11 +81,7 @@ ttt_la_status decay_scan(const ttt::DecayScans& p, int n, bool final, const floa
   }
   if (blocks >= (1ll << 31)) return TTT_LA_ERR_UNSUPPORTED;
   const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(n));
-  if (final)
-    ttt::decay_scan_kernel<true><<<grid, 256, 0, st>>>(p, log_decay);
-  else
-    ttt::decay_scan_kernel<false><<<grid, 256, 0, st>>>(p, log_decay);
-  return launched();
+  return launch_after(final ? ttt::decay_scan_kernel<true> : ttt::decay_scan_kernel<false>, grid, 256, 0, st, p, log_decay);
 }
 
 ttt::DecayScan decay_scan_of(const ttt::DecayGeom& g, const ttt::DecayRun& r) {
@@ -157,28 +153,33 @@ bool decay_map(CUtensorMap* m, const ttt::DecayTensor& t, int N, int H, int T, i
 }
 
 template <int DK, int DV>
-ttt_la_status decay_tc_launch(const ttt::DecayTcArgs& a, bool totals, cudaStream_t st) {
+ttt_la_status decay_tc_launch(const ttt::DecayTcArgs& a, bool totals, bool first, cudaStream_t st) {
   using Cfg = ttt::DecayTcCfg<DK, DV>;
   const long long blocks = static_cast<long long>(a.g.nseg) * a.g.H * a.nrun;
   if (blocks >= (1ll << 31)) return TTT_LA_ERR_UNSUPPORTED;
   auto kern = totals ? ttt::decay_tc_total_kernel<DK, DV> : ttt::decay_tc_out_kernel<DK, DV>;
   const int smem = totals ? Cfg::A_SMEM : Cfg::SMEM;
   if (!grant_smem(reinterpret_cast<const void*>(kern), smem)) return TTT_LA_ERR_CUDA;
-  return launch_kernel(kern, static_cast<int>(blocks), totals ? Cfg::A_THREADS : Cfg::THREADS, smem, st, false, a);
+  const int threads = totals ? Cfg::A_THREADS : Cfg::THREADS;
+  if (first) return launch_kernel(kern, static_cast<int>(blocks), threads, smem, st, false, a);
+  return launch_after(kern, dim3(static_cast<unsigned>(blocks)), threads, smem, st, a);
 }
 // Launches the runs r[0 .. n) of `a`, those of equal tile widths together.
-ttt_la_status decay_tc_group(ttt::DecayTcArgs& a, const ttt::DecayTcRun* r, int n, bool totals, cudaStream_t st) {
+// `first`: nothing of this call was launched before.
+ttt_la_status decay_tc_group(ttt::DecayTcArgs& a, const ttt::DecayTcRun* r, int n, bool totals, bool first,
+                             cudaStream_t st) {
   auto wide = [](int d) { return d > 64; };
   for (int shape = 0; shape < 4; ++shape) {
     a.nrun = 0;
     for (int i = 0; i < n; ++i)
       if ((wide(r[i].dk) ? 1 : 0) + (wide(r[i].dv) ? 2 : 0) == shape) a.run[a.nrun++] = r[i];
     if (!a.nrun) continue;
-    const ttt_la_status s = shape == 0   ? decay_tc_launch<64, 64>(a, totals, st)
-                            : shape == 1 ? decay_tc_launch<128, 64>(a, totals, st)
-                            : shape == 2 ? decay_tc_launch<64, 128>(a, totals, st)
-                                         : decay_tc_launch<128, 128>(a, totals, st);
+    const ttt_la_status s = shape == 0   ? decay_tc_launch<64, 64>(a, totals, first, st)
+                            : shape == 1 ? decay_tc_launch<128, 64>(a, totals, first, st)
+                            : shape == 2 ? decay_tc_launch<64, 128>(a, totals, first, st)
+                                         : decay_tc_launch<128, 128>(a, totals, first, st);
     if (s != TTT_LA_OK) return s;
+    first = false;
   }
   return TTT_LA_OK;
 }
@@ -305,7 +306,7 @@ ttt_la_status ttt_la_forward_decay(const ttt_la_decay_args* a, void* stream) {
   ttt::DecayTcRun run = decay_tc_run(0, 1, 2, 3, r);
   run.ws_all = decay_in_place(a);
   if (r.ws || r.s_out) {
-    const ttt_la_status e = decay_tc_group(m, &run, 1, true, st);
+    const ttt_la_status e = decay_tc_group(m, &run, 1, true, true, st);
     if (e != TTT_LA_OK) return e;
   }
   if (r.ws) {
@@ -314,7 +315,7 @@ ttt_la_status ttt_la_forward_decay(const ttt_la_decay_args* a, void* stream) {
     const ttt_la_status e = decay_scan(ttt::DecayScans{{sc}}, 1, true, a->log_decay, st);
     if (e != TTT_LA_OK) return e;
   }
-  return decay_tc_group(m, &run, 1, false, st);
+  return decay_tc_group(m, &run, 1, false, !(r.ws || r.s_out), st);
 }
 
 size_t ttt_la_backward_decay_workspace_size(const ttt_la_decay_grad_args* a) {
@@ -385,7 +386,7 @@ ttt_la_status ttt_la_backward_decay(const ttt_la_decay_grad_args* a, void* strea
   run[2].ws = run[1].ws, run[2].ws_t = 1;
   if (need || a->grad_state_in) {
     // (without segments only dL/dW_0 is wanted)
-    const ttt_la_status e = decay_tc_group(m, need ? run : run + 1, need ? 2 : 1, true, st);
+    const ttt_la_status e = decay_tc_group(m, need ? run : run + 1, need ? 2 : 1, true, true, st);
     if (e != TTT_LA_OK) return e;
   }
   if (need) {
@@ -394,7 +395,7 @@ ttt_la_status ttt_la_backward_decay(const ttt_la_decay_grad_args* a, void* strea
     const ttt_la_status e = decay_scan(sc, 2, true, a->log_decay, st);
     if (e != TTT_LA_OK) return e;
   }
-  return decay_tc_group(m, run, 3, false, st);
+  return decay_tc_group(m, run, 3, false, !(need || a->grad_state_in), st);
 }
 
 }  // extern "C"

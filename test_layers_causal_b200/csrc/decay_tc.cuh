@@ -260,14 +260,14 @@ __device__ __forceinline__ void decay_state_in(float* buf, const float* src, boo
     for (int c = wp; c < DK; c += 8)
 #pragma unroll
       for (int v = 0; v < DV; v += 32)
-        buf[(v + lane) * LD + c] = c < dk && v + lane < dv ? __ldcg(src + static_cast<size_t>(c) * dv + v + lane) : 0.f;
+        buf[(v + lane) * LD + c] = c < dk && v + lane < dv ? ld_after(src + static_cast<size_t>(c) * dv + v + lane) : 0.f;
   } else {
     constexpr int PER = 128 / DK;  // rows a warp reads at once
     const int c = (lane % (DK / 4)) * 4;
 #pragma unroll 8
     for (int r = wp * PER + lane / (DK / 4); r < DV; r += 8 * PER) {
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (r < dv && c < dk) x = __ldcg(reinterpret_cast<const float4*>(src + static_cast<size_t>(r) * dk + c));
+      if (r < dv && c < dk) x = ld_after(reinterpret_cast<const float4*>(src + static_cast<size_t>(r) * dk + c));
       *reinterpret_cast<float4*>(buf + r * LD + c) = x;
     }
   }
@@ -327,8 +327,11 @@ __global__ void __launch_bounds__(320, 1) decay_tc_total_kernel(const __grid_con
   const int b = blockIdx.x, ri = b % A.nrun, h = (b / A.nrun) % g.H, s = b / A.nrun / g.H;
   const DecayTcRun& p = A.run[ri];
   const DecaySpan sp = decay_span_block(g, s, sh);
-  if (sp.seq < 0) return;
-  if (!p.total_last && sp.j == (p.rev ? 0 : sp.nseg - 1)) return;
+  launch_next();
+  if (sp.seq < 0 || (!p.total_last && sp.j == (p.rev ? 0 : sp.nseg - 1))) {
+    wait_before();
+    return;
+  }
   const uint64_t lim = A.limit_ns;
   const int nt = (sp.len + C - 1) / C;
   auto tile_at = [&](int i) { return p.rev ? i : nt - 1 - i; };
@@ -478,6 +481,7 @@ __global__ void __launch_bounds__(320, 1) decay_tc_total_kernel(const __grid_con
     }
     tc_fence_before();
   }
+  wait_before();  // (nothing here depends on the launch before)
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
@@ -538,7 +542,11 @@ __global__ void __launch_bounds__(608, 1) decay_tc_out_kernel(const __grid_const
   const int b = blockIdx.x, ri = b % A.nrun, h = (b / A.nrun) % g.H, s = b / A.nrun / g.H;
   const DecayTcRun& p = A.run[ri];
   const DecaySpan sp = decay_span_block(g, s, sh);
-  if (sp.seq < 0 || sp.len <= 0) return;
+  launch_next();
+  if (sp.seq < 0 || sp.len <= 0) {
+    wait_before();
+    return;
+  }
   const uint64_t lim = A.limit_ns;
   const bool rev = p.rev != 0;
   const int nt = (sp.len + C - 1) / C;
@@ -826,6 +834,7 @@ __global__ void __launch_bounds__(608, 1) decay_tc_out_kernel(const __grid_const
     float w[NW];
     {
       const size_t dd = static_cast<size_t>(p.dk) * p.dv;
+      wait_before();  // the scan's states
       const bool via = p.ws && (sp.nseg > 1 || p.ws_all);
       const float* src = via ? p.ws + (static_cast<size_t>(s) * g.H + h) * dd
                              : p.s_in ? p.s_in + (static_cast<size_t>(sp.seq) * g.H + h) * dd : nullptr;

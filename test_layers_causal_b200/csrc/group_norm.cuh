@@ -11,8 +11,8 @@
 // Gradient, with dt = dL/dt and dh = dt w, the means over the (sample, group):
 //   dx = rstd (dh - mean(dh) - hat mean(dh hat)) ,  dw = sum dt hat ,  db = sum dt.
 //
-// All of it is bound by memory: values are read in 16-byte units, several in
-// flight a thread, and the statistics are taken in fp32 from registers, mean
+// All of it is bound by memory: values come in 16-byte units through a ring of
+// bulk copies (below), and the statistics are taken in fp32 from registers, mean
 // first and then squares around it (of a channel over a batch of positions;
 // batches, channels, threads and blocks are joined by the exact two-set
 // formula), so a mean far from zero costs no digits.  Every sum has a fixed
@@ -30,25 +30,6 @@ struct Unit {
   f2 v[P];
 };
 template <typename T, int V>
-__device__ __forceinline__ Unit<T, V> ld_unit(const T* p) {
-  static_assert(V == 1 || sizeof(T) * V == 16, "");
-  Unit<T, V> r;
-  if constexpr (V == 1) {
-    r.v[0] = pair(to_f<T>(__ldg(p)), 0.f);
-  } else {
-    const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
-    if constexpr (sizeof(T) == 2) {
-      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) r.v[i] = pair(w[i] << 16, w[i] & 0xffff0000u);
-    } else {
-      r.v[0] = pair(u.x, u.y);
-      r.v[1] = pair(u.z, u.w);
-    }
-  }
-  return r;
-}
-template <typename T, int V>
 __device__ __forceinline__ void st_unit(T* p, const Unit<T, V>& x) {
   if constexpr (V == 1) {
     *p = from_f<T>(lo_of(x.v[0]));
@@ -58,6 +39,20 @@ __device__ __forceinline__ void st_unit(T* p, const Unit<T, V>& x) {
   } else {
     *reinterpret_cast<float4*>(p) = make_float4(lo_of(x.v[0]), hi_of(x.v[0]), lo_of(x.v[1]), hi_of(x.v[1]));
   }
+}
+// A bulk copy's units as they lie in shared memory.
+template <typename T, int V>
+__device__ __forceinline__ Unit<T, V> unit_of(const uint4 u) {
+  Unit<T, V> r;
+  if constexpr (sizeof(T) == 2) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.v[i] = pair(w[i] << 16, w[i] & 0xffff0000u);
+  } else {
+    r.v[0] = pair(u.x, u.y);
+    r.v[1] = pair(u.z, u.w);
+  }
+  return r;
 }
 __device__ __forceinline__ f2 both(float x) { return pair(x, x); }
 __device__ __forceinline__ float sum_of(f2 x) { return lo_of(x) + hi_of(x); }
@@ -74,6 +69,8 @@ struct GnParams {
   int splits, rows;           // parts of a sample for the statistics and the gradient's sums, positions in each
   int parts, part_rows;       // the same for the passes that write y or dx
   int width, slots;           // one-position kernels: units of a row in a block, rows at a time
+  int per;                    // of those: rows in a block
+  uint64_t limit_ns;
   // gradient
   const void* gy;
   void *gx, *ggate;
@@ -131,13 +128,90 @@ struct Moments {
 __device__ __forceinline__ Moments join(const Moments& a, const Moments& b) {
   const float n = a.n + b.n;
   if (n == 0.f) return a;
-  const float f = b.n / n, d = b.mean - a.mean;
+  const float f = __fdividef(b.n, n), d = b.mean - a.mean;  // (counts: far from the division's limits)
   return Moments{n, fmaf(d, f, a.mean), a.m2 + b.m2 + d * d * a.n * f};
 }
 __device__ __forceinline__ Moments shfl_xor(const Moments& a, int off) {
   return Moments{__shfl_xor_sync(0xffffffffu, a.n, off), __shfl_xor_sync(0xffffffffu, a.mean, off),
                  __shfl_xor_sync(0xffffffffu, a.m2, off)};
 }
+
+// Walks rows of C values in memory, `slots` rows at a time, a thread one unit of
+// each: thread slot * width + u has unit u of row `slot`.  What the slots' rows
+// hold of the block's units is contiguous (a narrow row is held whole, a wide
+// one alone), so each tensor's share of a step is one bulk copy (cp.async.bulk)
+// of up to 4 KB into a ring of S steps, issued S steps ahead by one thread:
+// memory stays busy without registers or occupancy (measured, gated rows
+// 16384 x 2048 bf16: 55 us with two rows of plain loads a thread).
+// Waits are bounded; after one runs out nothing more is copied or waited for.
+constexpr int kGnStage = 4096;
+template <int NT, int S>
+struct GnRing {
+  uint8_t* buf;       // [S][NT][4096]
+  uint64_t* full;     // [S]
+  uint64_t limit_ns;
+  int used;           // steps so far
+  bool dead;
+
+  __device__ __forceinline__ void init(uint8_t* smem, uint64_t* bars, uint64_t limit) {
+    buf = smem, full = bars, limit_ns = limit, used = 0, dead = false;
+    if (threadIdx.x == 0) {
+      for (int i = 0; i < S; ++i) mbar_init(&full[i], 1);
+      fence_mbar_init();
+    }
+    __syncthreads();
+  }
+
+  // f(row, units[NT], ok) for this thread's row of every step, by all threads.
+  // src: row 0's first unit of the block's; `units`: the block's of a row.
+  template <typename T, int V, typename F>
+  __device__ __forceinline__ void walk(const T* const (&src)[NT], int rows, int C, int units, int slots, F&& f) {
+    const int steps = (rows + slots - 1) / slots, tid = threadIdx.x, slot = tid / units, u = tid % units;
+    const bool on = slot < slots;
+    if constexpr (V == 1) {  // rows at any address: plain loads
+      for (int k = 0; k < steps; ++k) {
+        const int row = k * slots + slot;
+        const bool ok = on && row < rows;
+        Unit<T, V> x[NT];
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+          x[i].v[0] = pair(ok ? to_f<T>(__ldg(src[i] + static_cast<size_t>(row) * C + u)) : 0.f, 0.f);
+        f(row, x, ok);
+      }
+    } else {
+      auto issue = [&](int k) {
+        const int st = (used + k) % S, n = min(slots, rows - k * slots);
+        const uint32_t bytes = static_cast<uint32_t>(n * units) * 16u;
+        mbar_arrive_expect_tx(&full[st], bytes * NT);
+  #pragma unroll
+        for (int i = 0; i < NT; ++i)
+          bulk_load(buf + (st * NT + i) * kGnStage, src[i] + static_cast<size_t>(k) * slots * C, bytes, &full[st]);
+      };
+      int sent = 0;
+      if (tid == 0 && !dead)
+        for (; sent < min(S, steps); ++sent) issue(sent);
+      for (int k = 0; k < steps; ++k) {
+        const int st = (used + k) % S;
+        if (!dead) dead = !mbar_wait(&full[st], ((used + k) / S) & 1, limit_ns);
+        uint4 raw[NT];
+  #pragma unroll
+        for (int i = 0; i < NT; ++i) raw[i] = ld_shared_v4(smem_u32(buf) + (st * NT + i) * kGnStage + tid * 16);
+        // read by all, the reads ordered before the copy into the same place S steps later
+        fence_async_smem();
+        __syncthreads();
+        if (tid == 0 && !dead && sent < steps) issue(sent++);
+        const int row = k * slots + slot;
+        Unit<T, V> x[NT];
+  #pragma unroll
+        for (int i = 0; i < NT; ++i) x[i] = unit_of<T, V>(raw[i]);
+        f(row, x, on && row < rows);
+      }
+      if (dead && tid == 0)  // what is still on its way lands before the block ends
+        for (int k = max(0, sent - S); k < sent; ++k) mbar_wait(&full[(used + k) % S], ((used + k) / S) & 1, limit_ns);
+      used += steps;
+    }
+  }
+};
 
 // weight and bias of V channels from c.
 template <int V>
@@ -163,164 +237,118 @@ struct GnParam {
 // ------------------------------------------------- one position a sample ----
 // L = 1 and a group of 1, 2, 4 .. 32 units: the lanes of a group hold it in
 // registers, one unit a thread, so the values are read once.  A thread keeps
-// its channels over all its rows (weight and bias in registers) and has R rows
-// in flight.  Block x: units [x width, (x + 1) width) of a row, `slots` rows at
-// a time where a row is narrow.
-// Measured (B200, 16384 x 2048 bf16 with a gate): 33 us, 6.1 TB/s.
+// its channels over all its rows, with weight and bias in registers.  Block
+// (x, y): units [x width, (x + 1) width) of rows [y per, (y + 1) per).
 template <typename T, int V, bool GATE, bool ACT>
 __global__ void __launch_bounds__(256, 4) gn_row_kernel(const GnParams p, int lanes) {
-  constexpr int R = GATE ? 2 : 3, P = V / 2;
-  const int tid = threadIdx.x, slot = tid / p.width, u = blockIdx.x * p.width + tid % p.width;
-  const bool on = slot < p.slots && u < p.C / V;
-  const int c = on ? u * V : 0;
+  constexpr int P = V / 2, NT = GATE ? 2 : 1, S = 12 / NT;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ __align__(8) uint64_t bars[S];
+  const int tid = threadIdx.x, u0 = blockIdx.x * p.width, units = min(p.width, p.C / V - u0);
+  const int row0 = blockIdx.y * p.per, rows = min(p.per, p.N - row0);
+  const bool on = tid < units * p.slots;
+  const int c = (u0 + (on ? tid % units : 0)) * V, g = c / p.cg;
   const GnParam<V> par(p, c, on);
   const float inv = 1.f / static_cast<float>(p.cg);
   const bool first = c % p.cg == 0;
-  const int g = c / p.cg, step = gridDim.y * p.slots, row0 = blockIdx.y * p.slots + slot;
-  const T* xp = static_cast<const T*>(p.x) + c;
-  const T* zp = static_cast<const T*>(p.gate) + c;
-  T* yp = static_cast<T*>(p.y) + c;
-  const int rounds = (p.N + step - 1) / step;  // the same for the whole block: warps meet in the shuffles
-  for (int k0 = 0; k0 < rounds; k0 += R) {
-    Unit<T, V> x[R], z[R];
-    long long n[R];
-    bool ok[R];
+  const size_t base = static_cast<size_t>(row0) * p.C;
+  T* yp = static_cast<T*>(p.y) + base + c;
+  float *mp = p.mean + static_cast<size_t>(row0) * p.G + g, *rp = p.rstd + static_cast<size_t>(row0) * p.G + g;
+  GnRing<NT, S> ring;
+  ring.init(smem, bars, p.limit_ns);
+  const T* src[NT];
+  src[0] = static_cast<const T*>(p.x) + base + u0 * V;
+  if constexpr (GATE) src[1] = static_cast<const T*>(p.gate) + base + u0 * V;
+  ring.template walk<T, V>(src, rows, p.C, units, p.slots, [&](int row, Unit<T, V>(&in)[NT], bool ok) {
+    Unit<T, V>& x = in[0];
+    f2 s = x.v[0];
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-      n[i] = static_cast<long long>(k0 + i) * step + row0;
-      ok[i] = on && n[i] < p.N;
+    for (int e = 1; e < P; ++e) s = add2(s, x.v[e]);
+    float mean = sum_of(s);
+    for (int off = lanes >> 1; off > 0; off >>= 1) mean += __shfl_xor_sync(0xffffffffu, mean, off);
+    mean *= inv;
+    s = both(0.f);
 #pragma unroll
-      for (int e = 0; e < P; ++e) x[i].v[e] = z[i].v[e] = both(0.f);
-      if (ok[i]) {
-        x[i] = ld_unit<T, V>(xp + n[i] * p.C);
-        if constexpr (GATE) z[i] = ld_unit<T, V>(zp + n[i] * p.C);
-      }
+    for (int e = 0; e < P; ++e) {
+      x.v[e] = add2(x.v[e], both(-mean));
+      s = fma2(x.v[e], x.v[e], s);
     }
-    float mean[R], q[R];
+    float q = sum_of(s);
+    for (int off = lanes >> 1; off > 0; off >>= 1) q += __shfl_xor_sync(0xffffffffu, q, off);
+    if (!ok) return;
+    const float rstd = rsqrtf(fmaf(q, inv, p.eps));
+    Unit<T, V> y;
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-      f2 s = x[i].v[0];
-#pragma unroll
-      for (int e = 1; e < P; ++e) s = add2(s, x[i].v[e]);
-      mean[i] = sum_of(s);
+    for (int e = 0; e < P; ++e)
+      y.v[e] = gn_out<GATE, ACT>(fma2(mul2(x.v[e], both(rstd)), par.w[e], par.b[e]), in[NT - 1].v[e]);
+    st_unit<T, V>(yp + static_cast<size_t>(row) * p.C, y);
+    if (first) {
+      mp[static_cast<size_t>(row) * p.G] = mean;
+      rp[static_cast<size_t>(row) * p.G] = rstd;
     }
-    for (int off = lanes >> 1; off > 0; off >>= 1)
-#pragma unroll
-      for (int i = 0; i < R; ++i) mean[i] += __shfl_xor_sync(0xffffffffu, mean[i], off);
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-      mean[i] *= inv;
-      f2 s = both(0.f);
-#pragma unroll
-      for (int e = 0; e < P; ++e) {
-        x[i].v[e] = add2(x[i].v[e], both(-mean[i]));
-        s = fma2(x[i].v[e], x[i].v[e], s);
-      }
-      q[i] = sum_of(s);
-    }
-    for (int off = lanes >> 1; off > 0; off >>= 1)
-#pragma unroll
-      for (int i = 0; i < R; ++i) q[i] += __shfl_xor_sync(0xffffffffu, q[i], off);
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-      if (!ok[i]) continue;
-      const float rstd = rsqrtf(fmaf(q[i], inv, p.eps));
-      Unit<T, V> y;
-#pragma unroll
-      for (int e = 0; e < P; ++e)
-        y.v[e] = gn_out<GATE, ACT>(fma2(mul2(x[i].v[e], both(rstd)), par.w[e], par.b[e]), z[i].v[e]);
-      st_unit<T, V>(yp + n[i] * p.C, y);
-      if (first) {
-        p.mean[n[i] * p.G + g] = mean[i];
-        p.rstd[n[i] * p.G + g] = rstd;
-      }
-    }
-  }
+  });
 }
 
 // Its gradient: dw and db gather in registers over the thread's rows; the
 // block's sums go to part[2][gridDim.y][C].
 template <typename T, int V, bool GATE, bool ACT>
 __global__ void __launch_bounds__(256, 3) gn_row_grad_kernel(const GnParams p, int lanes) {
-  constexpr int R = GATE ? 1 : 2, P = V / 2;
+  constexpr int P = V / 2, NT = GATE ? 3 : 2, S = 12 / NT;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ __align__(8) uint64_t bars[S];
   __shared__ float red[2][256][V + 1];
-  const int tid = threadIdx.x, slot = tid / p.width, u = blockIdx.x * p.width + tid % p.width;
-  const bool on = slot < p.slots && u < p.C / V;
-  const int c = on ? u * V : 0;
+  const int tid = threadIdx.x, u0 = blockIdx.x * p.width, units = min(p.width, p.C / V - u0);
+  const int row0 = blockIdx.y * p.per, rows = min(p.per, p.N - row0);
+  const bool on = tid < units * p.slots;
+  const int c = (u0 + (on ? tid % units : 0)) * V, g = c / p.cg;
   const GnParam<V> par(p, c, on);
   f2 dw[P], db[P];
 #pragma unroll
   for (int e = 0; e < P; ++e) dw[e] = db[e] = both(0.f);
   const float inv = 1.f / static_cast<float>(p.cg);
-  const int g = c / p.cg, step = gridDim.y * p.slots, row0 = blockIdx.y * p.slots + slot;
-  const int rounds = (p.N + step - 1) / step;
-  // the rows of the round after this one, in flight
-  Unit<T, V> x[R], z[R], gy[R];
-  float mean[R], rstd[R];
-  bool ok[R];
-  auto fetch = [&](int k0) {
+  const size_t base = static_cast<size_t>(row0) * p.C;
+  T *gxp = static_cast<T*>(p.gx) + base + c, *gzp = static_cast<T*>(p.ggate) + base + c;
+  const float *mp = p.mean + static_cast<size_t>(row0) * p.G + g, *rp = p.rstd + static_cast<size_t>(row0) * p.G + g;
+  // the next row's statistics, a step ahead
+  auto stat = [&](const float* q, int row) { return on && row < rows ? __ldg(q + static_cast<size_t>(row) * p.G) : 0.f; };
+  float mean = stat(mp, tid / units), rstd = stat(rp, tid / units);
+  launch_next();
+  GnRing<NT, S> ring;
+  ring.init(smem, bars, p.limit_ns);
+  const T* src[NT];
+  src[0] = static_cast<const T*>(p.x) + base + u0 * V;
+  src[1] = static_cast<const T*>(p.gy) + base + u0 * V;
+  if constexpr (GATE) src[2] = static_cast<const T*>(p.gate) + base + u0 * V;
+  ring.template walk<T, V>(src, rows, p.C, units, p.slots, [&](int row, Unit<T, V>(&in)[NT], bool ok) {
+    const f2 m2 = both(-mean), r2 = both(rstd);
+    mean = stat(mp, row + p.slots), rstd = stat(rp, row + p.slots);
+    Unit<T, V> dz;
+    f2 a = both(0.f), b = both(0.f);
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-      const long long n = static_cast<long long>(k0 + i) * step + row0;
-      ok[i] = on && n < p.N;
-      mean[i] = rstd[i] = 0.f;
-#pragma unroll
-      for (int e = 0; e < P; ++e) x[i].v[e] = gy[i].v[e] = z[i].v[e] = both(0.f);
-      if (ok[i]) {
-        const long long at = n * p.C + c;
-        x[i] = ld_unit<T, V>(static_cast<const T*>(p.x) + at);
-        gy[i] = ld_unit<T, V>(static_cast<const T*>(p.gy) + at);
-        if constexpr (GATE) z[i] = ld_unit<T, V>(static_cast<const T*>(p.gate) + at);
-        mean[i] = __ldg(p.mean + n * p.G + g);
-        rstd[i] = __ldg(p.rstd + n * p.G + g);
-      }
+    for (int e = 0; e < P; ++e) {
+      const f2 hat = mul2(add2(in[0].v[e], m2), r2);
+      f2 dt = gn_grad<GATE, ACT>(in[1].v[e], fma2(hat, par.w[e], par.b[e]), in[NT - 1].v[e], dz.v[e]);
+      if (!ok) dt = both(0.f);
+      dw[e] = fma2(dt, ok ? hat : both(0.f), dw[e]);
+      db[e] = add2(db[e], dt);
+      in[0].v[e] = hat;
+      in[1].v[e] = mul2(dt, par.w[e]);
+      a = add2(a, in[1].v[e]);
+      b = fma2(in[1].v[e], hat, b);
     }
-  };
-  fetch(0);
-  for (int k0 = 0; k0 < rounds; k0 += R) {
-    Unit<T, V> hat[R], dh[R];
-    float s1[R], s2[R], r[R];
-    bool now[R];
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-      Unit<T, V> dz;
-      f2 a = both(0.f), b = both(0.f);
-      r[i] = rstd[i];
-      now[i] = ok[i];
-      const f2 r2 = both(rstd[i]), m2 = both(-mean[i]);
-#pragma unroll
-      for (int e = 0; e < P; ++e) {
-        hat[i].v[e] = mul2(add2(x[i].v[e], m2), r2);
-        const f2 dt = gn_grad<GATE, ACT>(gy[i].v[e], fma2(hat[i].v[e], par.w[e], par.b[e]), z[i].v[e], dz.v[e]);
-        dw[e] = fma2(dt, hat[i].v[e], dw[e]);
-        db[e] = add2(db[e], dt);
-        dh[i].v[e] = mul2(dt, par.w[e]);
-        a = add2(a, dh[i].v[e]);
-        b = fma2(dh[i].v[e], hat[i].v[e], b);
-      }
-      s1[i] = sum_of(a);
-      s2[i] = sum_of(b);
-      const long long n = static_cast<long long>(k0 + i) * step + row0;
-      if (GATE && now[i]) st_unit<T, V>(static_cast<T*>(p.ggate) + n * p.C + c, dz);
+    float s1 = sum_of(a), s2 = sum_of(b);
+    for (int off = lanes >> 1; off > 0; off >>= 1) {
+      s1 += __shfl_xor_sync(0xffffffffu, s1, off);
+      s2 += __shfl_xor_sync(0xffffffffu, s2, off);
     }
-    if (k0 + R < rounds) fetch(k0 + R);
-    for (int off = lanes >> 1; off > 0; off >>= 1)
+    if (!ok) return;
+    if constexpr (GATE) st_unit<T, V>(gzp + static_cast<size_t>(row) * p.C, dz);
+    Unit<T, V> dx;
 #pragma unroll
-      for (int i = 0; i < R; ++i) {
-        s1[i] += __shfl_xor_sync(0xffffffffu, s1[i], off);
-        s2[i] += __shfl_xor_sync(0xffffffffu, s2[i], off);
-      }
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-      if (!now[i]) continue;
-      const long long n = static_cast<long long>(k0 + i) * step + row0;
-      const f2 a = both(-s1[i] * inv), b = both(-s2[i] * inv), r2 = both(r[i]);
-      Unit<T, V> dx;
-#pragma unroll
-      for (int e = 0; e < P; ++e) dx.v[e] = mul2(r2, fma2(hat[i].v[e], b, add2(dh[i].v[e], a)));
-      st_unit<T, V>(static_cast<T*>(p.gx) + n * p.C + c, dx);
-    }
-  }
+    for (int e = 0; e < P; ++e)
+      dx.v[e] = mul2(r2, fma2(in[0].v[e], both(-s2 * inv), add2(in[1].v[e], both(-s1 * inv))));
+    st_unit<T, V>(gxp + static_cast<size_t>(row) * p.C, dx);
+  });
   if (!p.part) return;
 #pragma unroll
   for (int e = 0; e < P; ++e) {
@@ -330,13 +358,11 @@ __global__ void __launch_bounds__(256, 3) gn_row_grad_kernel(const GnParams p, i
     red[1][tid][2 * e + 1] = hi_of(db[e]);
   }
   __syncthreads();
-  for (int i = tid; i < 2 * p.width * V; i += blockDim.x) {
-    const int which = i / (p.width * V), ch = i % (p.width * V), un = ch / V, e = ch % V;
-    const int at = blockIdx.x * p.width * V + ch;
-    if (at >= p.C) continue;
+  for (int i = tid; i < 2 * units * V; i += blockDim.x) {
+    const int which = i / (units * V), ch = i % (units * V), un = ch / V, e = ch % V;
     float s = 0.f;
-    for (int k = 0; k < p.slots; ++k) s += red[which][k * p.width + un][e];
-    p.part[(static_cast<size_t>(which) * gridDim.y + blockIdx.y) * p.C + at] = s;
+    for (int k = 0; k < p.slots; ++k) s += red[which][k * units + un][e];
+    p.part[(static_cast<size_t>(which) * gridDim.y + blockIdx.y) * p.C + u0 * V + ch] = s;
   }
 }
 
@@ -350,15 +376,13 @@ __device__ __forceinline__ void gn_param_sum(const float* __restrict__ part, int
   float s = 0.f;
   if (c < C) {
     const float* at = part + static_cast<size_t>(which) * count * C + c;
-    int k = warp;
-    for (; k + 56 < count; k += 64) {
+    for (int k = warp; k < count; k += 64) {
       float t[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) t[i] = __ldg(at + static_cast<size_t>(k + 8 * i) * C);
+      for (int i = 0; i < 8; ++i) t[i] = k + 8 * i < count ? ld_after(at + static_cast<size_t>(k + 8 * i) * C) : 0.f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) s += t[i];
     }
-    for (; k < count; k += 8) s += __ldg(at + static_cast<size_t>(k) * C);
   }
   red[warp][lane] = s;
   __syncthreads();
@@ -373,6 +397,7 @@ __device__ __forceinline__ void gn_param_sum(const float* __restrict__ part, int
 }
 __global__ void __launch_bounds__(256) gn_param_grad_kernel(const float* __restrict__ part, int count, int C, void* gw,
                                                             void* gb, int pbf) {
+  wait_before();
   gn_param_sum(part, count, C, blockIdx.y ? gb : gw, pbf, blockIdx.x, blockIdx.y);
 }
 
@@ -388,66 +413,60 @@ __device__ __forceinline__ void gn_rows(int L, int rows, int k, int& l0, int& l1
 // where a sample is one split, mean and rstd.  Dynamic shared memory: G
 // Moments.
 template <typename T, int V>
-__global__ void __launch_bounds__(256) gn_stats_kernel(const GnParams p) {
-  extern __shared__ Moments group[];  // [G]
+__global__ void __launch_bounds__(256, 4) gn_stats_kernel(const GnParams p) {
+  constexpr int P = Unit<T, V>::P, U = 8, S = 8;  // U: positions in a batch
+  extern __shared__ __align__(128) uint8_t smem[];
+  Moments* group = reinterpret_cast<Moments*>(smem + S * kGnStage);  // [G]
+  __shared__ __align__(8) uint64_t bars[S];
   __shared__ float each[2][256][V + 1];
   __shared__ float counts[256];
   const int tid = threadIdx.x, n = blockIdx.x / p.splits, part = blockIdx.x % p.splits, cv = p.C / V;
   int l0, l1;
   gn_rows(p.L, p.rows, part, l0, l1);
   for (int g = tid; g < p.G; g += 256) group[g] = Moments{0.f, 0.f, 0.f};
-  const T* x = static_cast<const T*>(p.x) + static_cast<size_t>(n) * p.L * p.C;
+  const T* x = static_cast<const T*>(p.x) + (static_cast<size_t>(n) * p.L + l0) * p.C;
+  launch_next();
+  GnRing<1, S> ring;
+  ring.init(smem, bars, p.limit_ns);
   for (int u0 = 0; u0 < cv; u0 += 256) {
-    const int width = min(cv - u0, 256), slots = 256 / width, slot = tid / width, u = u0 + tid % width;
-    constexpr int P = Unit<T, V>::P, U = V == 8 ? 4 : 8;  // U: positions per batch, all in flight
-    float cnt = 0.f;
-    f2 mean[P], m2[P];
+    const int width = min(cv - u0, 256), slots = cv > 256 ? 1 : 256 / width;
+    // a batch's sums relative to its first value, joined to the mean and squares so far
+    float cnt = 0.f, have = 0.f;
+    f2 mean[P], m2[P], at[P], s[P], q[P];
 #pragma unroll
-    for (int e = 0; e < P; ++e) mean[e] = m2[e] = both(0.f);
-    if (slot < slots) {
-      const T* xu = x + u * V;
-      int l = l0 + slot;
-      // `h` positions in b: their own mean and squares, joined to what is there
-      auto take = [&](const Unit<T, V>(&b)[U], int have) {
-        const float h = static_cast<float>(have), inv = 1.f / h, f = h / (cnt + h), cf = cnt * f;
+    for (int e = 0; e < P; ++e) mean[e] = m2[e] = at[e] = s[e] = q[e] = both(0.f);
+    auto close = [&]() {
+      if (have == 0.f) return;
+      const float f = __fdividef(have, cnt + have), inv = __frcp_rn(have), cf = cnt * f;
 #pragma unroll
-        for (int e = 0; e < P; ++e) {
-          f2 s = b[0].v[e], q = both(0.f);
-#pragma unroll
-          for (int i = 1; i < U; ++i)
-            if (i < have) s = add2(s, b[i].v[e]);
-          s = mul2(s, both(inv));
-          const f2 neg = mul2(s, both(-1.f));
-#pragma unroll
-          for (int i = 0; i < U; ++i)
-            if (i < have) {
-              const f2 d = add2(b[i].v[e], neg);
-              q = fma2(d, d, q);
-            }
-          const f2 d = fma2(mean[e], both(-1.f), s);
-          mean[e] = fma2(d, both(f), mean[e]);
-          m2[e] = add2(m2[e], fma2(mul2(d, d), both(cf), q));
-        }
-        cnt += h;
-      };
-      for (; l + (U - 1) * slots < l1; l += U * slots) {
-        Unit<T, V> b[U];
-#pragma unroll
-        for (int i = 0; i < U; ++i) b[i] = ld_unit<T, V>(xu + static_cast<size_t>(l + i * slots) * p.C);
-        take(b, U);
+      for (int e = 0; e < P; ++e) {
+        const f2 d0 = mul2(s[e], both(inv));  // batch mean - at
+        const f2 sq = fma2(mul2(s[e], both(-1.f)), d0, q[e]);
+        const f2 d = fma2(mean[e], both(-1.f), add2(at[e], d0));
+        mean[e] = fma2(d, both(f), mean[e]);
+        m2[e] = add2(m2[e], fma2(mul2(d, d), both(cf), sq));
+        s[e] = q[e] = both(0.f);
       }
-      if (l < l1) {
-        Unit<T, V> b[U];
-        int have = 0;
+      cnt += have;
+      have = 0.f;
+    };
+    const T* src[1] = {x + u0 * V};
+    ring.template walk<T, V>(src, l1 - l0, p.C, width, slots, [&](int, Unit<T, V>(&in)[1], bool ok) {
+      if (!ok) return;
+      if (have == 0.f) {
 #pragma unroll
-        for (int i = 0; i < U; ++i)
-          if (l + i * slots < l1) {
-            b[i] = ld_unit<T, V>(xu + static_cast<size_t>(l + i * slots) * p.C);
-            ++have;
-          }
-        take(b, have);
+        for (int e = 0; e < P; ++e) at[e] = in[0].v[e];
       }
-    }
+#pragma unroll
+      for (int e = 0; e < P; ++e) {
+        const f2 d = fma2(at[e], both(-1.f), in[0].v[e]);
+        s[e] = add2(s[e], d);
+        q[e] = fma2(d, d, q[e]);
+      }
+      have += 1.f;
+      if (have == static_cast<float>(U)) close();
+    });
+    close();
     __syncthreads();
     counts[tid] = cnt;
 #pragma unroll
@@ -486,17 +505,24 @@ __global__ void __launch_bounds__(256) gn_stats_kernel(const GnParams p) {
 // mean and rstd from the splits' statistics, a warp per (sample, group).
 __global__ void __launch_bounds__(256) gn_join_kernel(const GnParams p) {
   const long long i = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) >> 5;
+  launch_next();
+  wait_before();
   if (i >= static_cast<long long>(p.N) * p.G) return;
   const long long n = i / p.G;
   const int g = static_cast<int>(i % p.G);
   const float2* d = reinterpret_cast<const float2*>(p.part) + n * p.splits * p.G + g;
   Moments m{0.f, 0.f, 0.f};
-#pragma unroll 4
-  for (int k = threadIdx.x & 31; k < p.splits; k += 32) {
-    const float2 x = __ldg(d + static_cast<size_t>(k) * p.G);
-    int a, b;
-    gn_rows(p.L, p.rows, k, a, b);
-    if (b > a) m = join(m, Moments{static_cast<float>(b - a) * static_cast<float>(p.cg), x.x, x.y});
+  for (int k0 = threadIdx.x & 31; k0 < p.splits; k0 += 128) {
+    float2 x[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (k0 + 32 * j < p.splits) x[j] = ld_after(d + static_cast<size_t>(k0 + 32 * j) * p.G);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      int a, b;
+      gn_rows(p.L, p.rows, k0 + 32 * j, a, b);
+      if (b > a) m = join(m, Moments{static_cast<float>(b - a) * static_cast<float>(p.cg), x[j].x, x[j].y});
+    }
   }
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) m = join(m, shfl_xor(m, off));
@@ -514,22 +540,25 @@ struct GnStat {
   __device__ __forceinline__ GnStat(const float* s, int stride, int c, int cg) {
 #pragma unroll
     for (int e = 0; e < P; ++e)
-      v[e] = pair(__ldg(s + stride * ((c + 2 * e) / cg)), V > 1 ? __ldg(s + stride * ((c + 2 * e + 1) / cg)) : 0.f);
+      v[e] = pair(ld_after(s + stride * ((c + 2 * e) / cg)), V > 1 ? ld_after(s + stride * ((c + 2 * e + 1) / cg)) : 0.f);
   }
 };
 
 // y from mean and rstd.
 template <typename T, int V, bool GATE, bool ACT>
-__global__ void __launch_bounds__(256) gn_apply_kernel(const GnParams p) {
-  constexpr int P = Unit<T, V>::P;
+__global__ void __launch_bounds__(256, 4) gn_apply_kernel(const GnParams p) {
+  constexpr int P = Unit<T, V>::P, NT = GATE ? 2 : 1, S = 12 / NT;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ __align__(8) uint64_t bars[S];
   const int tid = threadIdx.x, n = blockIdx.x / p.parts, part = blockIdx.x % p.parts, cv = p.C / V;
   int l0, l1;
   gn_rows(p.L, p.part_rows, part, l0, l1);
-  const size_t base = static_cast<size_t>(n) * p.L * p.C;
+  const size_t base = (static_cast<size_t>(n) * p.L + l0) * p.C;
+  GnRing<NT, S> ring;
+  ring.init(smem, bars, p.limit_ns);
+  wait_before();
   for (int u0 = 0; u0 < cv; u0 += 256) {
-    const int width = min(cv - u0, 256), slots = 256 / width, slot = tid / width, u = u0 + tid % width;
-    if (slot >= slots) continue;
-    const int c = u * V;
+    const int width = min(cv - u0, 256), slots = cv > 256 ? 1 : 256 / width, c = (u0 + tid % width) * V;
     GnParam<V> par(p, c, true);  // t = (x - mean) w + b, rstd in w
     const GnStat<V> mean(p.mean + static_cast<size_t>(n) * p.G, 1, c, p.cg), rstd(p.rstd + static_cast<size_t>(n) * p.G, 1, c, p.cg);
     f2 neg[P];
@@ -538,55 +567,60 @@ __global__ void __launch_bounds__(256) gn_apply_kernel(const GnParams p) {
       neg[e] = mul2(mean.v[e], both(-1.f));
       par.w[e] = mul2(par.w[e], rstd.v[e]);
     }
-#pragma unroll 4
-    for (int l = l0 + slot; l < l1; l += slots) {
-      const size_t at = base + static_cast<size_t>(l) * p.C + c;
-      const Unit<T, V> x = ld_unit<T, V>(static_cast<const T*>(p.x) + at);
-      Unit<T, V> z = x, y;
-      if constexpr (GATE) z = ld_unit<T, V>(static_cast<const T*>(p.gate) + at);
+    const T* src[NT];
+    src[0] = static_cast<const T*>(p.x) + base + u0 * V;
+    if constexpr (GATE) src[1] = static_cast<const T*>(p.gate) + base + u0 * V;
+    T* yp = static_cast<T*>(p.y) + base + c;
+    ring.template walk<T, V>(src, l1 - l0, p.C, width, slots, [&](int row, Unit<T, V>(&in)[NT], bool ok) {
+      if (!ok) return;
+      Unit<T, V> y;
 #pragma unroll
-      for (int e = 0; e < P; ++e) y.v[e] = gn_out<GATE, ACT>(fma2(add2(x.v[e], neg[e]), par.w[e], par.b[e]), z.v[e]);
-      st_unit<T, V>(static_cast<T*>(p.y) + at, y);
-    }
+      for (int e = 0; e < P; ++e)
+        y.v[e] = gn_out<GATE, ACT>(fma2(add2(in[0].v[e], neg[e]), par.w[e], par.b[e]), in[NT - 1].v[e]);
+      st_unit<T, V>(yp + static_cast<size_t>(row) * p.C, y);
+    });
   }
 }
 
 // Gradient, first pass: part[2][N][splits][C], the sums of dt hat and of dt
 // over a split's positions; also dgate.
 template <typename T, int V, bool GATE, bool ACT>
-__global__ void __launch_bounds__(256) gn_grad_sums_kernel(const GnParams p) {
-  constexpr int P = Unit<T, V>::P;
+__global__ void __launch_bounds__(256, 3) gn_grad_sums_kernel(const GnParams p) {
+  constexpr int P = Unit<T, V>::P, NT = GATE ? 3 : 2, S = 12 / NT;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ __align__(8) uint64_t bars[S];
   __shared__ float red[2][256][V + 1];
   const int tid = threadIdx.x, n = blockIdx.x / p.splits, part = blockIdx.x % p.splits, cv = p.C / V;
   int l0, l1;
   gn_rows(p.L, p.rows, part, l0, l1);
-  const size_t base = static_cast<size_t>(n) * p.L * p.C, all = static_cast<size_t>(p.N) * p.splits * p.C;
+  const size_t base = (static_cast<size_t>(n) * p.L + l0) * p.C, all = static_cast<size_t>(p.N) * p.splits * p.C;
+  launch_next();
+  GnRing<NT, S> ring;
+  ring.init(smem, bars, p.limit_ns);
   for (int u0 = 0; u0 < cv; u0 += 256) {
-    const int width = min(cv - u0, 256), slots = 256 / width, slot = tid / width, u = u0 + tid % width;
+    const int width = min(cv - u0, 256), slots = cv > 256 ? 1 : 256 / width, c = (u0 + tid % width) * V;
     f2 dw[P], db[P];
 #pragma unroll
     for (int e = 0; e < P; ++e) dw[e] = db[e] = both(0.f);
-    if (slot < slots) {
-      const int c = u * V;
-      const GnParam<V> par(p, c, true);
-      const GnStat<V> mean(p.mean + static_cast<size_t>(n) * p.G, 1, c, p.cg), rstd(p.rstd + static_cast<size_t>(n) * p.G, 1, c, p.cg);
-#pragma unroll 4
-      for (int l = l0 + slot; l < l1; l += slots) {
-        const size_t at = base + static_cast<size_t>(l) * p.C + c;
-        const Unit<T, V> x = ld_unit<T, V>(static_cast<const T*>(p.x) + at);
-        const Unit<T, V> gy = ld_unit<T, V>(static_cast<const T*>(p.gy) + at);
-        Unit<T, V> z = x, dz;
-        if constexpr (GATE) z = ld_unit<T, V>(static_cast<const T*>(p.gate) + at);
+    const GnParam<V> par(p, c, true);
+    const GnStat<V> mean(p.mean + static_cast<size_t>(n) * p.G, 1, c, p.cg), rstd(p.rstd + static_cast<size_t>(n) * p.G, 1, c, p.cg);
+    const T* src[NT];
+    src[0] = static_cast<const T*>(p.x) + base + u0 * V;
+    src[1] = static_cast<const T*>(p.gy) + base + u0 * V;
+    if constexpr (GATE) src[2] = static_cast<const T*>(p.gate) + base + u0 * V;
+    T* gzp = static_cast<T*>(p.ggate) + base + c;
+    ring.template walk<T, V>(src, l1 - l0, p.C, width, slots, [&](int row, Unit<T, V>(&in)[NT], bool ok) {
+      if (!ok) return;
+      Unit<T, V> dz;
 #pragma unroll
-        for (int e = 0; e < P; ++e) {
-          const f2 hat = mul2(fma2(mean.v[e], both(-1.f), x.v[e]), rstd.v[e]);
-          const f2 dt = gn_grad<GATE, ACT>(gy.v[e], fma2(hat, par.w[e], par.b[e]), z.v[e], dz.v[e]);
-          dw[e] = fma2(dt, hat, dw[e]);
-          db[e] = add2(db[e], dt);
-        }
-        if constexpr (GATE) st_unit<T, V>(static_cast<T*>(p.ggate) + at, dz);
+      for (int e = 0; e < P; ++e) {
+        const f2 hat = mul2(fma2(mean.v[e], both(-1.f), in[0].v[e]), rstd.v[e]);
+        const f2 dt = gn_grad<GATE, ACT>(in[1].v[e], fma2(hat, par.w[e], par.b[e]), in[NT - 1].v[e], dz.v[e]);
+        dw[e] = fma2(dt, hat, dw[e]);
+        db[e] = add2(db[e], dt);
       }
-    }
+      if constexpr (GATE) st_unit<T, V>(gzp + static_cast<size_t>(row) * p.C, dz);
+    });
     __syncthreads();
 #pragma unroll
     for (int e = 0; e < V; ++e) {
@@ -608,6 +642,8 @@ __global__ void __launch_bounds__(256) gn_grad_sums_kernel(const GnParams p) {
 // w dw.  The others: dw, then db, 32 channels a block.
 __global__ void __launch_bounds__(256) gn_grad_groups_kernel(const GnParams p, float* __restrict__ sums,
                                                              int warp_blocks) {
+  launch_next();
+  wait_before();
   if (static_cast<int>(blockIdx.x) >= warp_blocks) {
     const int b = blockIdx.x - warp_blocks, per = (p.C + 31) / 32;
     gn_param_sum(p.part, p.N * p.splits, p.C, b / per ? p.gb : p.gw, p.pbf, b % per, b / per);
@@ -628,8 +664,8 @@ __global__ void __launch_bounds__(256) gn_grad_groups_kernel(const GnParams p, f
 #pragma unroll 8
       for (int k = k0; k < p.splits; k += per) {
         const float* q = at + static_cast<size_t>(k) * p.C + c;
-        t2 += __ldg(q);
-        t1 += __ldg(q + all);
+        t2 += ld_after(q);
+        t1 += ld_after(q + all);
       }
       const float w = gn_param(p.weight, p.pbf, g * p.cg + c, 1.f);
       s1 = fmaf(w, t1, s1);
@@ -649,16 +685,19 @@ __global__ void __launch_bounds__(256) gn_grad_groups_kernel(const GnParams p, f
 
 // Gradient, third pass: dx.
 template <typename T, int V, bool GATE, bool ACT>
-__global__ void __launch_bounds__(256) gn_grad_apply_kernel(const GnParams p, const float* __restrict__ sums) {
-  constexpr int P = Unit<T, V>::P;
+__global__ void __launch_bounds__(256, 3) gn_grad_apply_kernel(const GnParams p, const float* __restrict__ sums) {
+  constexpr int P = Unit<T, V>::P, NT = GATE ? 3 : 2, S = 12 / NT;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ __align__(8) uint64_t bars[S];
   const int tid = threadIdx.x, n = blockIdx.x / p.parts, part = blockIdx.x % p.parts, cv = p.C / V;
   int l0, l1;
   gn_rows(p.L, p.part_rows, part, l0, l1);
-  const size_t base = static_cast<size_t>(n) * p.L * p.C, ng = static_cast<size_t>(n) * p.G;
+  const size_t base = (static_cast<size_t>(n) * p.L + l0) * p.C, ng = static_cast<size_t>(n) * p.G;
+  GnRing<NT, S> ring;
+  ring.init(smem, bars, p.limit_ns);
+  wait_before();
   for (int u0 = 0; u0 < cv; u0 += 256) {
-    const int width = min(cv - u0, 256), slots = 256 / width, slot = tid / width, u = u0 + tid % width;
-    if (slot >= slots) continue;
-    const int c = u * V;
+    const int width = min(cv - u0, 256), slots = cv > 256 ? 1 : 256 / width, c = (u0 + tid % width) * V;
     const GnParam<V> par(p, c, true);
     const GnStat<V> mean(p.mean + ng, 1, c, p.cg), rstd(p.rstd + ng, 1, c, p.cg);
     GnStat<V> s1(sums + 2 * ng, 2, c, p.cg), s2(sums + 2 * ng + 1, 2, c, p.cg);
@@ -667,22 +706,23 @@ __global__ void __launch_bounds__(256) gn_grad_apply_kernel(const GnParams p, co
       s1.v[e] = mul2(s1.v[e], both(-1.f));
       s2.v[e] = mul2(s2.v[e], both(-1.f));
     }
-#pragma unroll 2
-    for (int l = l0 + slot; l < l1; l += slots) {
-      const size_t at = base + static_cast<size_t>(l) * p.C + c;
-      const Unit<T, V> x = ld_unit<T, V>(static_cast<const T*>(p.x) + at);
-      const Unit<T, V> gy = ld_unit<T, V>(static_cast<const T*>(p.gy) + at);
-      Unit<T, V> z = x, dx;
-      if constexpr (GATE) z = ld_unit<T, V>(static_cast<const T*>(p.gate) + at);
+    const T* src[NT];
+    src[0] = static_cast<const T*>(p.x) + base + u0 * V;
+    src[1] = static_cast<const T*>(p.gy) + base + u0 * V;
+    if constexpr (GATE) src[2] = static_cast<const T*>(p.gate) + base + u0 * V;
+    T* gxp = static_cast<T*>(p.gx) + base + c;
+    ring.template walk<T, V>(src, l1 - l0, p.C, width, slots, [&](int row, Unit<T, V>(&in)[NT], bool ok) {
+      if (!ok) return;
+      Unit<T, V> dx;
 #pragma unroll
       for (int e = 0; e < P; ++e) {
-        const f2 hat = mul2(fma2(mean.v[e], both(-1.f), x.v[e]), rstd.v[e]);
+        const f2 hat = mul2(fma2(mean.v[e], both(-1.f), in[0].v[e]), rstd.v[e]);
         f2 dz;
-        const f2 dt = gn_grad<GATE, ACT>(gy.v[e], fma2(hat, par.w[e], par.b[e]), z.v[e], dz);
+        const f2 dt = gn_grad<GATE, ACT>(in[1].v[e], fma2(hat, par.w[e], par.b[e]), in[NT - 1].v[e], dz);
         dx.v[e] = mul2(rstd.v[e], fma2(hat, s2.v[e], fma2(dt, par.w[e], s1.v[e])));
       }
-      st_unit<T, V>(static_cast<T*>(p.gx) + at, dx);
-    }
+      st_unit<T, V>(gxp + static_cast<size_t>(row) * p.C, dx);
+    });
   }
 }
 

@@ -23,6 +23,7 @@ struct GnPlan {
   int lanes;               // > 0: the one-position kernels
   int width, slots;        // of those: units of a row in a block, rows at a time
   int columns, blocks;     // and their grid
+  int per;                 // rows of a block
   int splits, rows;        // parts of a sample and the positions in each: sums
   int parts, part_rows;    // the same: writing passes
   size_t floats;           // workspace
@@ -31,7 +32,7 @@ struct GnPlan {
 // `per_sm` parts for each SM over all samples, none with so few positions that
 // a block's sums cost more than its reads (16 KB).
 void gn_split(int N, int L, int C, int dtype, int per_sm, int* parts, int* rows) {
-  const long long want = std::max(1ll, (static_cast<long long>(sm_count()) * per_sm + N - 1) / N);
+  const long long want = std::max(1ll, static_cast<long long>(sm_count()) * per_sm / N);  // (one wave of blocks)
   const long long least = std::max(1ll, 16384 / (static_cast<long long>(C) * (dtype == TTT_LA_F32 ? 4 : 2)));
   *rows = static_cast<int>(std::min<long long>(std::max(least, (L + want - 1) / want), L));
   *parts = (L - 1) / *rows + 1;
@@ -46,8 +47,11 @@ void gn_row_plan(GnPlan* p, int N, int C, int dtype, int per_sm) {
   p->width = p->columns == 1 ? cv : ((cv + p->columns - 1) / p->columns + 31) / 32 * 32;
   p->columns = (cv + p->width - 1) / p->width;
   p->slots = std::max(1, 256 / p->width);
-  const long long rows = (static_cast<long long>(N) + p->slots - 1) / p->slots;
-  p->blocks = static_cast<int>(std::min<long long>(rows, std::max(1, sm_count() * per_sm / p->columns)));
+  // rows of a block: whole steps of `slots`, in one wave of `per_sm` blocks a SM
+  const long long steps = (static_cast<long long>(N) + p->slots - 1) / p->slots;
+  const long long want = std::max(1, sm_count() * per_sm / p->columns);
+  p->per = static_cast<int>(std::min<long long>((steps + want - 1) / want * p->slots, N));
+  p->blocks = (N - 1) / p->per + 1;
 }
 
 GnPlan gn_plan_forward(int N, int L, int C, int G, int dtype) {
@@ -57,8 +61,8 @@ GnPlan gn_plan_forward(int N, int L, int C, int G, int dtype) {
     gn_row_plan(&p, N, C, dtype, 4);
     return p;
   }
-  gn_split(N, L, C, dtype, 3, &p.splits, &p.rows);
-  gn_split(N, L, C, dtype, 6, &p.parts, &p.part_rows);
+  gn_split(N, L, C, dtype, 4, &p.splits, &p.rows);
+  gn_split(N, L, C, dtype, 4, &p.parts, &p.part_rows);
   p.floats = p.splits > 1 ? static_cast<size_t>(N) * p.splits * G * 2 : 0;
   return p;
 }
@@ -71,7 +75,7 @@ GnPlan gn_plan_backward(int N, int L, int C, int G, int dtype, bool params) {
     return p;
   }
   gn_split(N, L, C, dtype, 3, &p.splits, &p.rows);
-  gn_split(N, L, C, dtype, 6, &p.parts, &p.part_rows);
+  gn_split(N, L, C, dtype, 3, &p.parts, &p.part_rows);
   p.floats = static_cast<size_t>(2) * N * p.splits * C + static_cast<size_t>(2) * N * G;
   return p;
 }
@@ -103,7 +107,14 @@ ttt_la_status gn_dispatch(int dtype, int unit, bool gate, bool act, F&& f) {
 
 void gn_fill(ttt::GnParams* p, const GnPlan& pl) {
   p->splits = pl.splits, p->rows = pl.rows, p->parts = pl.parts, p->part_rows = pl.part_rows;
-  p->width = pl.width, p->slots = pl.slots;
+  p->width = pl.width, p->slots = pl.slots, p->per = pl.per;
+  p->limit_ns = g_limit_ns;
+}
+constexpr int kGnRing = 12 * ttt::kGnStage;  // dynamic shared memory of every ring but the statistics' (8 steps)
+// (granted with the kernels' own tables of up to 20 KB in mind, which count towards the 48 KB that need none)
+template <typename K>
+bool gn_grant(K kern, int bytes = kGnRing) {
+  return grant_smem(reinterpret_cast<const void*>(kern), std::max(bytes, 49 * 1024));
 }
 int gn_row_threads(const GnPlan& pl) { return (pl.width * pl.slots + 31) / 32 * 32; }
 
@@ -145,23 +156,23 @@ ttt_la_status ttt_la_group_norm(const ttt_la_group_norm_args* a, void* stream) {
     constexpr bool GATE = decltype(gate)::value, ACT = decltype(act)::value;
     if constexpr (V > 1)
       if (pl.lanes) {
-        ttt::gn_row_kernel<T, V, GATE, ACT><<<dim3(pl.columns, pl.blocks), gn_row_threads(pl), 0, st>>>(p, pl.lanes);
+        if (!gn_grant(ttt::gn_row_kernel<T, V, GATE, ACT>)) return TTT_LA_ERR_CUDA;
+        ttt::gn_row_kernel<T, V, GATE, ACT>
+            <<<dim3(pl.columns, pl.blocks), gn_row_threads(pl), kGnRing, st>>>(p, pl.lanes);
         return launched();
       }
     const long long sums = static_cast<long long>(a->N) * pl.splits, parts = static_cast<long long>(a->N) * pl.parts;
     if (parts >= (1ll << 31) || sums >= (1ll << 31)) return TTT_LA_ERR_UNSUPPORTED;
-    const int sm = a->G * static_cast<int>(sizeof(ttt::Moments));
-    // (the kernel's own tables, 19 KB, count towards the 48 KB that need no grant)
-    if (sm > 28 * 1024 && !grant_smem(reinterpret_cast<const void*>(ttt::gn_stats_kernel<T, V>), 49 * 1024))
-      return TTT_LA_ERR_CUDA;
+    const int sm = 8 * ttt::kGnStage + a->G * static_cast<int>(sizeof(ttt::Moments));
+    if (!gn_grant(ttt::gn_stats_kernel<T, V>, sm) || !gn_grant(ttt::gn_apply_kernel<T, V, GATE, ACT>)) return TTT_LA_ERR_CUDA;
     ttt_la_status r = launch_kernel(ttt::gn_stats_kernel<T, V>, static_cast<int>(sums), 256, sm, st, false, p);
     if (r != TTT_LA_OK) return r;
     if (pl.splits > 1) {
       const long long warps = static_cast<long long>(a->N) * a->G;
-      r = launch_kernel(ttt::gn_join_kernel, static_cast<int>((warps * 32 + 255) / 256), 256, 0, st, false, p);
+      r = launch_after(ttt::gn_join_kernel, dim3(static_cast<unsigned>((warps + 7) / 8)), 256, 0, st, p);
       if (r != TTT_LA_OK) return r;
     }
-    return launch_kernel(ttt::gn_apply_kernel<T, V, GATE, ACT>, static_cast<int>(parts), 256, 0, st, false, p);
+    return launch_after(ttt::gn_apply_kernel<T, V, GATE, ACT>, dim3(static_cast<unsigned>(parts)), 256, kGnRing, st, p);
   });
 }
 
@@ -207,25 +218,30 @@ ttt_la_status ttt_la_group_norm_backward(const ttt_la_group_norm_grad_args* a, v
     constexpr bool GATE = decltype(gate)::value, ACT = decltype(act)::value;
     if constexpr (V > 1)
       if (pl.lanes) {
-        ttt::gn_row_grad_kernel<T, V, GATE, ACT><<<dim3(pl.columns, pl.blocks), gn_row_threads(pl), 0, st>>>(p, pl.lanes);
+        if (!gn_grant(ttt::gn_row_grad_kernel<T, V, GATE, ACT>)) return TTT_LA_ERR_CUDA;
+        ttt::gn_row_grad_kernel<T, V, GATE, ACT>
+            <<<dim3(pl.columns, pl.blocks), gn_row_threads(pl), kGnRing, st>>>(p, pl.lanes);
         const ttt_la_status r = launched();
         if (r != TTT_LA_OK || !params) return r;
-        ttt::gn_param_grad_kernel<<<dim3((a->C + 31) / 32, 2), 256, 0, st>>>(p.part, pl.blocks, a->C, a->grad_weight,
-                                                                            a->grad_bias, p.pbf);
-        return launched();
+        return launch_after(ttt::gn_param_grad_kernel, dim3((a->C + 31) / 32, 2), 256, 0, st,
+                            static_cast<const float*>(p.part), pl.blocks, static_cast<int>(a->C), a->grad_weight,
+                            a->grad_bias, p.pbf);
       }
     const long long rows = static_cast<long long>(a->N) * pl.splits, parts = static_cast<long long>(a->N) * pl.parts;
     if (parts >= (1ll << 31) || rows >= (1ll << 31)) return TTT_LA_ERR_UNSUPPORTED;
     float* sums = p.part + static_cast<size_t>(2) * rows * a->C;
-    ttt_la_status r = launch_kernel(ttt::gn_grad_sums_kernel<T, V, GATE, ACT>, static_cast<int>(rows), 256, 0, st, false, p);
+    if (!gn_grant(ttt::gn_grad_sums_kernel<T, V, GATE, ACT>) || !gn_grant(ttt::gn_grad_apply_kernel<T, V, GATE, ACT>))
+      return TTT_LA_ERR_CUDA;
+    ttt_la_status r = launch_kernel(ttt::gn_grad_sums_kernel<T, V, GATE, ACT>, static_cast<int>(rows), 256, kGnRing, st, false, p);
     if (r != TTT_LA_OK) return r;
     const long long warp_blocks = (static_cast<long long>(a->N) * a->G + 7) / 8;
     const long long blocks = warp_blocks + (params ? 2 * ((a->C + 31) / 32) : 0);
     if (blocks >= (1ll << 31)) return TTT_LA_ERR_UNSUPPORTED;
-    r = launch_kernel(ttt::gn_grad_groups_kernel, static_cast<int>(blocks), 256, 0, st, false, p, sums,
-                      static_cast<int>(warp_blocks));
+    r = launch_after(ttt::gn_grad_groups_kernel, dim3(static_cast<unsigned>(blocks)), 256, 0, st, p, sums,
+                     static_cast<int>(warp_blocks));
     if (r != TTT_LA_OK) return r;
-    return launch_kernel(ttt::gn_grad_apply_kernel<T, V, GATE, ACT>, static_cast<int>(parts), 256, 0, st, false, p, sums);
+    return launch_after(ttt::gn_grad_apply_kernel<T, V, GATE, ACT>, dim3(static_cast<unsigned>(parts)), 256, kGnRing, st, p,
+                        static_cast<const float*>(sums));
   });
 }
 

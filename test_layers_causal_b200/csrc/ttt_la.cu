@@ -142,6 +142,27 @@ ttt_la_status launch_kernel(void (*kern)(P...), int grid, int threads, int smem,
   return TTT_LA_OK;
 }
 
+// Launches `kern` behind a kernel of the same call on the same stream, whose
+// end it overlaps with its own start (see wait_before in common.cuh).
+template <typename... P, typename... A>
+ttt_la_status launch_after(void (*kern)(P...), dim3 grid, int threads, int smem, cudaStream_t st, A&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kern, std::forward<A>(args)...) != cudaSuccess) {
+    cudaGetLastError();
+    return TTT_LA_ERR_CUDA;
+  }
+  return TTT_LA_OK;
+}
+
 // ------------------------------------------------------------ TMA maps ----
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
