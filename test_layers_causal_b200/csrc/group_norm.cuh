@@ -54,6 +54,17 @@ __device__ __forceinline__ Unit<T, V> unit_of(const uint4 u) {
   }
   return r;
 }
+// The same from memory, or one value.
+template <typename T, int V>
+__device__ __forceinline__ Unit<T, V> ld_unit(const T* p) {
+  if constexpr (V == 1) {
+    Unit<T, V> r;
+    r.v[0] = pair(to_f<T>(__ldg(p)), 0.f);
+    return r;
+  } else {
+    return unit_of<T, V>(__ldg(reinterpret_cast<const uint4*>(p)));
+  }
+}
 __device__ __forceinline__ f2 both(float x) { return pair(x, x); }
 __device__ __forceinline__ float sum_of(f2 x) { return lo_of(x) + hi_of(x); }
 
@@ -137,16 +148,18 @@ __device__ __forceinline__ Moments shfl_xor(const Moments& a, int off) {
 }
 
 // Walks rows of C values in memory, `slots` rows at a time, a thread one unit of
-// each: thread slot * width + u has unit u of row `slot`.  What the slots' rows
-// hold of the block's units is contiguous (a narrow row is held whole, a wide
-// one alone), so each tensor's share of a step is one bulk copy (cp.async.bulk)
-// of up to 4 KB into a ring of S steps, issued S steps ahead by one thread:
-// memory stays busy without registers or occupancy (measured, gated rows
-// 16384 x 2048 bf16: 55 us with two rows of plain loads a thread).
+// each: thread slot * units + u has unit u of row `slot`.  What a step reads of
+// the block's units is contiguous (narrow rows are held whole, a wide one
+// alone), so it is one bulk copy (cp.async.bulk) of up to 4 KB a tensor into a
+// ring of S steps, issued S steps ahead by one thread: memory stays busy
+// without registers or occupancy.  Measured (gated rows 16384 x 2048 bf16): 55
+// us with two rows of plain loads a thread, 46 us with the ring, 50 us with
+// steps of two rows a thread; their gradient 114, 76 and 100 us.
 // Waits are bounded; after one runs out nothing more is copied or waited for.
-constexpr int kGnStage = 4096;
-template <int NT, int S>
+constexpr int kGnStage = 4096, kGnRingBytes = 12 * kGnStage;
+template <int NT>
 struct GnRing {
+  static constexpr int S = 12 / NT;
   uint8_t* buf;       // [S][NT][4096]
   uint64_t* full;     // [S]
   uint64_t limit_ns;
@@ -162,13 +175,14 @@ struct GnRing {
     __syncthreads();
   }
 
-  // f(row, units[NT], ok) for this thread's row of every step, by all threads.
+  // f(row, units[NT], ok) for this thread's rows of every step, by all threads.
   // src: row 0's first unit of the block's; `units`: the block's of a row.
   template <typename T, int V, typename F>
   __device__ __forceinline__ void walk(const T* const (&src)[NT], int rows, int C, int units, int slots, F&& f) {
-    const int steps = (rows + slots - 1) / slots, tid = threadIdx.x, slot = tid / units, u = tid % units;
+    const int tid = threadIdx.x, slot = tid / units, u = tid % units;
     const bool on = slot < slots;
     if constexpr (V == 1) {  // rows at any address: plain loads
+      const int steps = (rows + slots - 1) / slots;
       for (int k = 0; k < steps; ++k) {
         const int row = k * slots + slot;
         const bool ok = on && row < rows;
@@ -179,11 +193,12 @@ struct GnRing {
         f(row, x, ok);
       }
     } else {
+      const int steps = (rows + slots - 1) / slots;
       auto issue = [&](int k) {
         const int st = (used + k) % S, n = min(slots, rows - k * slots);
         const uint32_t bytes = static_cast<uint32_t>(n * units) * 16u;
         mbar_arrive_expect_tx(&full[st], bytes * NT);
-  #pragma unroll
+#pragma unroll
         for (int i = 0; i < NT; ++i)
           bulk_load(buf + (st * NT + i) * kGnStage, src[i] + static_cast<size_t>(k) * slots * C, bytes, &full[st]);
       };
@@ -194,7 +209,7 @@ struct GnRing {
         const int st = (used + k) % S;
         if (!dead) dead = !mbar_wait(&full[st], ((used + k) / S) & 1, limit_ns);
         uint4 raw[NT];
-  #pragma unroll
+#pragma unroll
         for (int i = 0; i < NT; ++i) raw[i] = ld_shared_v4(smem_u32(buf) + (st * NT + i) * kGnStage + tid * 16);
         // read by all, the reads ordered before the copy into the same place S steps later
         fence_async_smem();
@@ -202,7 +217,7 @@ struct GnRing {
         if (tid == 0 && !dead && sent < steps) issue(sent++);
         const int row = k * slots + slot;
         Unit<T, V> x[NT];
-  #pragma unroll
+#pragma unroll
         for (int i = 0; i < NT; ++i) x[i] = unit_of<T, V>(raw[i]);
         f(row, x, on && row < rows);
       }
@@ -241,9 +256,9 @@ struct GnParam {
 // (x, y): units [x width, (x + 1) width) of rows [y per, (y + 1) per).
 template <typename T, int V, bool GATE, bool ACT>
 __global__ void __launch_bounds__(256, 4) gn_row_kernel(const GnParams p, int lanes) {
-  constexpr int P = V / 2, NT = GATE ? 2 : 1, S = 12 / NT;
+  constexpr int P = V / 2, NT = GATE ? 2 : 1;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ __align__(8) uint64_t bars[S];
+  __shared__ __align__(8) uint64_t bars[12];
   const int tid = threadIdx.x, u0 = blockIdx.x * p.width, units = min(p.width, p.C / V - u0);
   const int row0 = blockIdx.y * p.per, rows = min(p.per, p.N - row0);
   const bool on = tid < units * p.slots;
@@ -254,7 +269,7 @@ __global__ void __launch_bounds__(256, 4) gn_row_kernel(const GnParams p, int la
   const size_t base = static_cast<size_t>(row0) * p.C;
   T* yp = static_cast<T*>(p.y) + base + c;
   float *mp = p.mean + static_cast<size_t>(row0) * p.G + g, *rp = p.rstd + static_cast<size_t>(row0) * p.G + g;
-  GnRing<NT, S> ring;
+  GnRing<NT> ring;
   ring.init(smem, bars, p.limit_ns);
   const T* src[NT];
   src[0] = static_cast<const T*>(p.x) + base + u0 * V;
@@ -293,9 +308,9 @@ __global__ void __launch_bounds__(256, 4) gn_row_kernel(const GnParams p, int la
 // block's sums go to part[2][gridDim.y][C].
 template <typename T, int V, bool GATE, bool ACT>
 __global__ void __launch_bounds__(256, 3) gn_row_grad_kernel(const GnParams p, int lanes) {
-  constexpr int P = V / 2, NT = GATE ? 3 : 2, S = 12 / NT;
+  constexpr int P = V / 2, NT = GATE ? 3 : 2;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ __align__(8) uint64_t bars[S];
+  __shared__ __align__(8) uint64_t bars[12];
   __shared__ float red[2][256][V + 1];
   const int tid = threadIdx.x, u0 = blockIdx.x * p.width, units = min(p.width, p.C / V - u0);
   const int row0 = blockIdx.y * p.per, rows = min(p.per, p.N - row0);
@@ -313,7 +328,7 @@ __global__ void __launch_bounds__(256, 3) gn_row_grad_kernel(const GnParams p, i
   auto stat = [&](const float* q, int row) { return on && row < rows ? __ldg(q + static_cast<size_t>(row) * p.G) : 0.f; };
   float mean = stat(mp, tid / units), rstd = stat(rp, tid / units);
   launch_next();
-  GnRing<NT, S> ring;
+  GnRing<NT> ring;
   ring.init(smem, bars, p.limit_ns);
   const T* src[NT];
   src[0] = static_cast<const T*>(p.x) + base + u0 * V;
@@ -379,9 +394,9 @@ __device__ __forceinline__ void gn_param_sum(const float* __restrict__ part, int
     for (int k = warp; k < count; k += 64) {
       float t[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) t[i] = k + 8 * i < count ? ld_after(at + static_cast<size_t>(k + 8 * i) * C) : 0.f;
+      for (int i = 0; i < 8; ++i) t[i] = ld_after(at + static_cast<size_t>(min(k + 8 * i, count - 1)) * C);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s += t[i];
+      for (int i = 0; i < 8; ++i) s += k + 8 * i < count ? t[i] : 0.f;
     }
   }
   red[warp][lane] = s;
@@ -414,10 +429,10 @@ __device__ __forceinline__ void gn_rows(int L, int rows, int k, int& l0, int& l1
 // Moments.
 template <typename T, int V>
 __global__ void __launch_bounds__(256, 4) gn_stats_kernel(const GnParams p) {
-  constexpr int P = Unit<T, V>::P, U = 8, S = 8;  // U: positions in a batch
+  constexpr int P = Unit<T, V>::P, U = 8;  // U: positions in a batch
   extern __shared__ __align__(128) uint8_t smem[];
-  Moments* group = reinterpret_cast<Moments*>(smem + S * kGnStage);  // [G]
-  __shared__ __align__(8) uint64_t bars[S];
+  Moments* group = reinterpret_cast<Moments*>(smem + kGnRingBytes);  // [G]
+  __shared__ __align__(8) uint64_t bars[12];
   __shared__ float each[2][256][V + 1];
   __shared__ float counts[256];
   const int tid = threadIdx.x, n = blockIdx.x / p.splits, part = blockIdx.x % p.splits, cv = p.C / V;
@@ -426,7 +441,7 @@ __global__ void __launch_bounds__(256, 4) gn_stats_kernel(const GnParams p) {
   for (int g = tid; g < p.G; g += 256) group[g] = Moments{0.f, 0.f, 0.f};
   const T* x = static_cast<const T*>(p.x) + (static_cast<size_t>(n) * p.L + l0) * p.C;
   launch_next();
-  GnRing<1, S> ring;
+  GnRing<1> ring;
   ring.init(smem, bars, p.limit_ns);
   for (int u0 = 0; u0 < cv; u0 += 256) {
     const int width = min(cv - u0, 256), slots = cv > 256 ? 1 : 256 / width;
@@ -544,21 +559,21 @@ struct GnStat {
   }
 };
 
-// y from mean and rstd.
+// y from mean and rstd.  x is in L2 from the statistics where it fits, and a
+// step's work is small: plain loads, four in flight a thread (measured, 6 x
+// 4225 x 320 fp32: 12 us; through the ring, whose steps cost a barrier, 18).
 template <typename T, int V, bool GATE, bool ACT>
-__global__ void __launch_bounds__(256, 4) gn_apply_kernel(const GnParams p) {
-  constexpr int P = Unit<T, V>::P, NT = GATE ? 2 : 1, S = 12 / NT;
-  extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ __align__(8) uint64_t bars[S];
+__global__ void __launch_bounds__(256) gn_apply_kernel(const GnParams p) {
+  constexpr int P = Unit<T, V>::P;
   const int tid = threadIdx.x, n = blockIdx.x / p.parts, part = blockIdx.x % p.parts, cv = p.C / V;
   int l0, l1;
   gn_rows(p.L, p.part_rows, part, l0, l1);
-  const size_t base = (static_cast<size_t>(n) * p.L + l0) * p.C;
-  GnRing<NT, S> ring;
-  ring.init(smem, bars, p.limit_ns);
+  const size_t base = static_cast<size_t>(n) * p.L * p.C;
   wait_before();
   for (int u0 = 0; u0 < cv; u0 += 256) {
-    const int width = min(cv - u0, 256), slots = cv > 256 ? 1 : 256 / width, c = (u0 + tid % width) * V;
+    const int width = min(cv - u0, 256), slots = 256 / width, slot = tid / width, u = u0 + tid % width;
+    if (slot >= slots) continue;
+    const int c = u * V;
     GnParam<V> par(p, c, true);  // t = (x - mean) w + b, rstd in w
     const GnStat<V> mean(p.mean + static_cast<size_t>(n) * p.G, 1, c, p.cg), rstd(p.rstd + static_cast<size_t>(n) * p.G, 1, c, p.cg);
     f2 neg[P];
@@ -567,18 +582,16 @@ __global__ void __launch_bounds__(256, 4) gn_apply_kernel(const GnParams p) {
       neg[e] = mul2(mean.v[e], both(-1.f));
       par.w[e] = mul2(par.w[e], rstd.v[e]);
     }
-    const T* src[NT];
-    src[0] = static_cast<const T*>(p.x) + base + u0 * V;
-    if constexpr (GATE) src[1] = static_cast<const T*>(p.gate) + base + u0 * V;
-    T* yp = static_cast<T*>(p.y) + base + c;
-    ring.template walk<T, V>(src, l1 - l0, p.C, width, slots, [&](int row, Unit<T, V>(&in)[NT], bool ok) {
-      if (!ok) return;
-      Unit<T, V> y;
+#pragma unroll 4
+    for (int l = l0 + slot; l < l1; l += slots) {
+      const size_t at = base + static_cast<size_t>(l) * p.C + c;
+      const Unit<T, V> x = ld_unit<T, V>(static_cast<const T*>(p.x) + at);
+      Unit<T, V> z = x, y;
+      if constexpr (GATE) z = ld_unit<T, V>(static_cast<const T*>(p.gate) + at);
 #pragma unroll
-      for (int e = 0; e < P; ++e)
-        y.v[e] = gn_out<GATE, ACT>(fma2(add2(in[0].v[e], neg[e]), par.w[e], par.b[e]), in[NT - 1].v[e]);
-      st_unit<T, V>(yp + static_cast<size_t>(row) * p.C, y);
-    });
+      for (int e = 0; e < P; ++e) y.v[e] = gn_out<GATE, ACT>(fma2(add2(x.v[e], neg[e]), par.w[e], par.b[e]), z.v[e]);
+      st_unit<T, V>(static_cast<T*>(p.y) + at, y);
+    }
   }
 }
 
@@ -586,16 +599,16 @@ __global__ void __launch_bounds__(256, 4) gn_apply_kernel(const GnParams p) {
 // over a split's positions; also dgate.
 template <typename T, int V, bool GATE, bool ACT>
 __global__ void __launch_bounds__(256, 3) gn_grad_sums_kernel(const GnParams p) {
-  constexpr int P = Unit<T, V>::P, NT = GATE ? 3 : 2, S = 12 / NT;
+  constexpr int P = Unit<T, V>::P, NT = GATE ? 3 : 2;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ __align__(8) uint64_t bars[S];
+  __shared__ __align__(8) uint64_t bars[12];
   __shared__ float red[2][256][V + 1];
   const int tid = threadIdx.x, n = blockIdx.x / p.splits, part = blockIdx.x % p.splits, cv = p.C / V;
   int l0, l1;
   gn_rows(p.L, p.rows, part, l0, l1);
   const size_t base = (static_cast<size_t>(n) * p.L + l0) * p.C, all = static_cast<size_t>(p.N) * p.splits * p.C;
   launch_next();
-  GnRing<NT, S> ring;
+  GnRing<NT> ring;
   ring.init(smem, bars, p.limit_ns);
   for (int u0 = 0; u0 < cv; u0 += 256) {
     const int width = min(cv - u0, 256), slots = cv > 256 ? 1 : 256 / width, c = (u0 + tid % width) * V;
@@ -661,11 +674,19 @@ __global__ void __launch_bounds__(256) gn_grad_groups_kernel(const GnParams p, f
   if (k0 < per)
     for (int c = lane % across; c < p.cg; c += across) {
       float t1 = 0.f, t2 = 0.f;
-#pragma unroll 8
-      for (int k = k0; k < p.splits; k += per) {
-        const float* q = at + static_cast<size_t>(k) * p.C + c;
-        t2 += ld_after(q);
-        t1 += ld_after(q + all);
+      for (int k = k0; k < p.splits; k += 8 * per) {
+        float x[8], y[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float* q = at + static_cast<size_t>(min(k + j * per, p.splits - 1)) * p.C + c;
+          x[j] = ld_after(q);
+          y[j] = ld_after(q + all);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          t2 += k + j * per < p.splits ? x[j] : 0.f;
+          t1 += k + j * per < p.splits ? y[j] : 0.f;
+        }
       }
       const float w = gn_param(p.weight, p.pbf, g * p.cg + c, 1.f);
       s1 = fmaf(w, t1, s1);
@@ -686,14 +707,14 @@ __global__ void __launch_bounds__(256) gn_grad_groups_kernel(const GnParams p, f
 // Gradient, third pass: dx.
 template <typename T, int V, bool GATE, bool ACT>
 __global__ void __launch_bounds__(256, 3) gn_grad_apply_kernel(const GnParams p, const float* __restrict__ sums) {
-  constexpr int P = Unit<T, V>::P, NT = GATE ? 3 : 2, S = 12 / NT;
+  constexpr int P = Unit<T, V>::P, NT = GATE ? 3 : 2;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ __align__(8) uint64_t bars[S];
+  __shared__ __align__(8) uint64_t bars[12];
   const int tid = threadIdx.x, n = blockIdx.x / p.parts, part = blockIdx.x % p.parts, cv = p.C / V;
   int l0, l1;
   gn_rows(p.L, p.part_rows, part, l0, l1);
   const size_t base = (static_cast<size_t>(n) * p.L + l0) * p.C, ng = static_cast<size_t>(n) * p.G;
-  GnRing<NT, S> ring;
+  GnRing<NT> ring;
   ring.init(smem, bars, p.limit_ns);
   wait_before();
   for (int u0 = 0; u0 < cv; u0 += 256) {

@@ -61,8 +61,8 @@ GnPlan gn_plan_forward(int N, int L, int C, int G, int dtype) {
     gn_row_plan(&p, N, C, dtype, 4);
     return p;
   }
-  gn_split(N, L, C, dtype, 4, &p.splits, &p.rows);
-  gn_split(N, L, C, dtype, 4, &p.parts, &p.part_rows);
+  gn_split(N, L, C, dtype, 3, &p.splits, &p.rows);
+  gn_split(N, L, C, dtype, 6, &p.parts, &p.part_rows);
   p.floats = p.splits > 1 ? static_cast<size_t>(N) * p.splits * G * 2 : 0;
   return p;
 }
@@ -110,7 +110,7 @@ void gn_fill(ttt::GnParams* p, const GnPlan& pl) {
   p->width = pl.width, p->slots = pl.slots, p->per = pl.per;
   p->limit_ns = g_limit_ns;
 }
-constexpr int kGnRing = 12 * ttt::kGnStage;  // dynamic shared memory of every ring but the statistics' (8 steps)
+constexpr int kGnRing = ttt::kGnRingBytes;
 // (granted with the kernels' own tables of up to 20 KB in mind, which count towards the 48 KB that need none)
 template <typename K>
 bool gn_grant(K kern, int bytes = kGnRing) {
@@ -163,8 +163,8 @@ ttt_la_status ttt_la_group_norm(const ttt_la_group_norm_args* a, void* stream) {
       }
     const long long sums = static_cast<long long>(a->N) * pl.splits, parts = static_cast<long long>(a->N) * pl.parts;
     if (parts >= (1ll << 31) || sums >= (1ll << 31)) return TTT_LA_ERR_UNSUPPORTED;
-    const int sm = 8 * ttt::kGnStage + a->G * static_cast<int>(sizeof(ttt::Moments));
-    if (!gn_grant(ttt::gn_stats_kernel<T, V>, sm) || !gn_grant(ttt::gn_apply_kernel<T, V, GATE, ACT>)) return TTT_LA_ERR_CUDA;
+    const int sm = kGnRing + a->G * static_cast<int>(sizeof(ttt::Moments));
+    if (!gn_grant(ttt::gn_stats_kernel<T, V>, sm)) return TTT_LA_ERR_CUDA;
     ttt_la_status r = launch_kernel(ttt::gn_stats_kernel<T, V>, static_cast<int>(sums), 256, sm, st, false, p);
     if (r != TTT_LA_OK) return r;
     if (pl.splits > 1) {
@@ -172,7 +172,7 @@ ttt_la_status ttt_la_group_norm(const ttt_la_group_norm_args* a, void* stream) {
       r = launch_after(ttt::gn_join_kernel, dim3(static_cast<unsigned>((warps + 7) / 8)), 256, 0, st, p);
       if (r != TTT_LA_OK) return r;
     }
-    return launch_after(ttt::gn_apply_kernel<T, V, GATE, ACT>, dim3(static_cast<unsigned>(parts)), 256, kGnRing, st, p);
+    return launch_after(ttt::gn_apply_kernel<T, V, GATE, ACT>, dim3(static_cast<unsigned>(parts)), 256, 0, st, p);
   });
 }
 
