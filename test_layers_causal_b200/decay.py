@@ -13,74 +13,17 @@ default the current stream of that device.
 """
 from __future__ import annotations
 
-import contextlib
-import ctypes
 import math
 
 import torch
 
 from . import _abi
+from ._call import FORMATS, check, check_distinct_rows, check_rows, launch_on, on_stream, run, run_with_workspace
 from .norm import group_norm
 
-_I3 = ctypes.c_int64 * 3
-_I2 = ctypes.c_int64 * 2
-_byref = ctypes.byref
-
-
-@contextlib.contextmanager
-def on_stream(device, stream):
-    """The tensors' device and the call's stream made current, so that what the
-    call allocates belongs to the stream that uses it; yields the handle."""
-    if stream is None:
-        with torch.cuda.device(device):
-            yield torch.cuda.current_stream(device).cuda_stream
-    else:
-        if stream.device != device:
-            raise ValueError("stream belongs to another device than the tensors")
-        with torch.cuda.stream(stream):
-            yield stream.cuda_stream
-
-
-def launch_on(device, stream, call):
-    """call(handle) with the tensors' device and the call's stream current
-    (on_stream without its cost where they already are)."""
-    if stream is None and torch.cuda.current_device() == device.index:
-        return call(torch.cuda.current_stream().cuda_stream)
-    with on_stream(device, stream) as handle:
-        return call(handle)
-
-
-def need(t, name, dtype, device, shape=None, contiguous=True):
-    """Refuses a tensor that is not what the library would read or write."""
-    if t is None:
-        return None
-    if t.device != device or not t.is_cuda:
-        raise ValueError(f"{name}: all tensors must be on one CUDA device")
-    if t.dtype != dtype:
-        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
-    if contiguous and not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
-
-
-def _rows(t, name, dtype, device, shape):
-    """Pointer and strides of a [.., d] tensor whose features are contiguous;
-    the strides of dimensions of size 1 are not read."""
-    p = need(t, name, dtype, device, shape, contiguous=False)
-    if shape[-1] > 1 and t.stride(-1) != 1:
-        raise ValueError(f"{name}: the last dimension must be contiguous")
-    return p
-
-
-def _distinct_rows(t, name):
-    """An output whose rows overlap would be written twice."""
-    size, at = t.shape[:-1], 1
-    for stride, n in sorted((t.stride(i), n) for i, n in enumerate(size) if n > 1):
-        if stride < at * (t.shape[-1] if at == 1 else 1):
-            raise ValueError(f"{name}: rows overlap")
-        at = stride * n
+_FORWARD = FORMATS["ttt_la_decay_args"].pack
+_BACKWARD = FORMATS["ttt_la_decay_grad_args"].pack
+_STEP = FORMATS["ttt_la_decay_decode_args"].pack
 
 
 def _shapes(q, k, v, log_decay, cu_seqlens):
@@ -92,21 +35,13 @@ def _shapes(q, k, v, log_decay, cu_seqlens):
         if B != 1 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
             raise ValueError("packed sequences: B = 1 and cu_seqlens of N + 1 offsets")
         N = cu_seqlens.numel() - 1
-        need(cu_seqlens, "cu_seqlens", torch.int32, dev)
-    need(log_decay, "log_decay", torch.float32, dev, (H,))
+        check(cu_seqlens, "cu_seqlens", torch.int32, dev)
+    check(log_decay, "log_decay", torch.float32, dev, (H,))
     return N, H, T, dk, v.shape[-1], dev
 
 
 def _default_eta(eta_const, dk):
     return 1.0 / math.sqrt(dk) if eta_const is None else float(eta_const)
-
-
-def _workspace(workspace, nbytes, device):
-    if workspace is not None:
-        need(workspace, "workspace", workspace.dtype, device)
-    if workspace is None or workspace.numel() * workspace.element_size() < nbytes:
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    return workspace
 
 
 def forward_decay(q, k, v, log_decay, eta_const=None, ascent=False, cu_seqlens=None, state_in=None,
@@ -124,23 +59,17 @@ def forward_decay(q, k, v, log_decay, eta_const=None, ascent=False, cu_seqlens=N
         if out is None:
             out = torch.empty_like(v)
         else:
-            _distinct_rows(out, "out")
+            check_distinct_rows(out, "out")
         if return_state and state_out is None:
             state_out = torch.empty(state_shape, device=dev, dtype=torch.float32)
-        a = _abi.TttDecayArgs(
-            N, H, T, dk, dv, code, _rows(q, "q", dt, dev, q.shape), _rows(k, "k", dt, dev, q.shape),
-            _rows(v, "v", dt, dev, v.shape), _rows(out, "out", dt, dev, v.shape),
-            _I3(*q.stride()[:3]), _I3(*k.stride()[:3]), _I3(*v.stride()[:3]), _I3(*out.stride()[:3]),
-            log_decay.data_ptr(), None if cu_seqlens is None else cu_seqlens.data_ptr(), _default_eta(eta_const, dk),
-            1 if ascent else 0, need(state_in, "state_in", torch.float32, dev, state_shape),
-            need(state_out, "state_out", torch.float32, dev, state_shape) if return_state else None,
-            int(segment_tokens))
-        L = _abi.lib()
-        nbytes = L.ttt_la_decay_workspace_size(_byref(a))
-        if nbytes:
-            w = _workspace(workspace, nbytes, dev)
-            a.workspace, a.workspace_bytes = w.data_ptr(), w.numel() * w.element_size()
-        _abi._check("ttt_la_forward_decay", L.ttt_la_forward_decay(_byref(a), handle))
+        (pq, sq), (pk, sk) = check_rows(q, "q", dt, dev, q.shape), check_rows(k, "k", dt, dev, q.shape)
+        (pv, sv), (po, so) = check_rows(v, "v", dt, dev, v.shape), check_rows(out, "out", dt, dev, v.shape)
+        block = _FORWARD(
+            N, H, T, dk, dv, code, pq, pk, pv, po, *sq[:3], *sk[:3], *sv[:3], *so[:3], log_decay.data_ptr(),
+            0 if cu_seqlens is None else cu_seqlens.data_ptr(), _default_eta(eta_const, dk), 1 if ascent else 0,
+            check(state_in, "state_in", torch.float32, dev, state_shape),
+            check(state_out, "state_out", torch.float32, dev, state_shape) if return_state else 0, int(segment_tokens))
+        run_with_workspace("ttt_la_forward_decay", "ttt_la_decay_workspace_size", block, workspace, dev, handle)
 
     launch_on(dev, stream, call)
     return out, state_out if return_state else None
@@ -156,22 +85,17 @@ def backward_decay(q, k, v, grad_o, log_decay, eta_const=None, ascent=False, cu_
     g = {}
 
     def call(handle):
-        ins = (_rows(q, "q", dt, dev, q.shape), _rows(k, "k", dt, dev, q.shape), _rows(v, "v", dt, dev, v.shape),
-               _rows(grad_o, "grad_o", dt, dev, v.shape))
+        ins = [check_rows(*x) for x in ((q, "q", dt, dev, q.shape), (k, "k", dt, dev, q.shape),
+                                        (v, "v", dt, dev, v.shape), (grad_o, "grad_o", dt, dev, v.shape))]
         g.update(dq=torch.empty_like(q), dk=torch.empty_like(k), dv=torch.empty_like(v),
                  dW0=torch.empty(state_shape, device=dev, dtype=torch.float32))
-        a = _abi.TttDecayGradArgs(
-            N, H, T, dk, dv, code, *ins, g["dq"].data_ptr(), g["dk"].data_ptr(), g["dv"].data_ptr(),
-            *(_I3(*t.stride()[:3]) for t in (q, k, v, grad_o, g["dq"], g["dk"], g["dv"])),
-            log_decay.data_ptr(), None if cu_seqlens is None else cu_seqlens.data_ptr(), _default_eta(eta_const, dk),
-            1 if ascent else 0, need(state_in, "state_in", torch.float32, dev, state_shape),
-            need(grad_state, "grad_state", torch.float32, dev, state_shape), g["dW0"].data_ptr(), int(segment_tokens))
-        L = _abi.lib()
-        nbytes = L.ttt_la_backward_decay_workspace_size(_byref(a))
-        if nbytes:
-            w = _workspace(workspace, nbytes, dev)
-            a.workspace, a.workspace_bytes = w.data_ptr(), w.numel() * w.element_size()
-        _abi._check("ttt_la_backward_decay", L.ttt_la_backward_decay(_byref(a), handle))
+        ts = ins + [(g[n].data_ptr(), g[n].stride()) for n in ("dq", "dk", "dv")]
+        block = _BACKWARD(
+            N, H, T, dk, dv, code, *(p for p, _ in ts), *(x for _, st in ts for x in st[:3]), log_decay.data_ptr(),
+            0 if cu_seqlens is None else cu_seqlens.data_ptr(), _default_eta(eta_const, dk), 1 if ascent else 0,
+            check(state_in, "state_in", torch.float32, dev, state_shape),
+            check(grad_state, "grad_state", torch.float32, dev, state_shape), g["dW0"].data_ptr(), int(segment_tokens))
+        run_with_workspace("ttt_la_backward_decay", "ttt_la_backward_decay_workspace_size", block, workspace, dev, handle)
 
     launch_on(dev, stream, call)
     return g
@@ -192,14 +116,13 @@ def decode_step_decay(q, k, v, log_decay, state, eta_const=None, ascent=False, o
         if out is None:
             out = torch.empty_like(v)
         else:
-            _distinct_rows(out, "out")
-        a = _abi.TttDecayDecodeArgs(
-            N, H, dk, dv, code, _rows(q, "q", dt, dev, q.shape), _rows(k, "k", dt, dev, q.shape),
-            _rows(v, "v", dt, dev, v.shape), _rows(out, "out", dt, dev, v.shape),
-            _I2(*q.stride()[:2]), _I2(*k.stride()[:2]), _I2(*v.stride()[:2]), _I2(*out.stride()[:2]),
-            need(log_decay, "log_decay", torch.float32, dev, (H,)), _default_eta(eta_const, dk), 1 if ascent else 0,
-            need(state, "state", torch.float32, dev, (N, H, dv, dk)))
-        _abi._check("ttt_la_decode_step_decay", _abi.lib().ttt_la_decode_step_decay(_byref(a), handle))
+            check_distinct_rows(out, "out")
+        (pq, sq), (pk, sk) = check_rows(q, "q", dt, dev, q.shape), check_rows(k, "k", dt, dev, q.shape)
+        (pv, sv), (po, so) = check_rows(v, "v", dt, dev, v.shape), check_rows(out, "out", dt, dev, v.shape)
+        run("ttt_la_decode_step_decay", _STEP(
+            N, H, dk, dv, code, pq, pk, pv, po, *sq[:2], *sk[:2], *sv[:2], *so[:2],
+            check(log_decay, "log_decay", torch.float32, dev, (H,)), _default_eta(eta_const, dk), 1 if ascent else 0,
+            check(state, "state", torch.float32, dev, (N, H, dv, dk))), handle)
 
     launch_on(dev, stream, call)
     return out

@@ -2,18 +2,17 @@
 ttt_la_group_norm and ttt_la_group_norm_backward (include/ttt_la.h)."""
 from __future__ import annotations
 
-import ctypes
-
 import torch
 
 from . import _abi
+from ._call import FORMATS, check, launch_on, run_with_workspace
 
-_byref = ctypes.byref
+_FORWARD = FORMATS["ttt_la_group_norm_args"].pack
+_BACKWARD = FORMATS["ttt_la_group_norm_grad_args"].pack
 _ACTIVATIONS = {None: 0, "none": 0, "silu": 1}
 
 
 def _describe(x, num_groups, weight, bias, gate, activation):
-    from .decay import need
     if x.dim() < 2:
         raise ValueError("x: [N, ..., C], channels last")
     if activation not in _ACTIVATIONS:
@@ -29,8 +28,8 @@ def _describe(x, num_groups, weight, bias, gate, activation):
     pdt = params[0].dtype if params else torch.float32
     if pdt not in (torch.float32, dt):
         raise TypeError("weight and bias: fp32 or the dtype of x")
-    pointers = (need(x, "x", dt, dev), need(gate, "gate", dt, dev, tuple(x.shape)),
-                need(weight, "weight", pdt, dev, (C,)), need(bias, "bias", pdt, dev, (C,)))
+    pointers = (check(x, "x", dt, dev), check(gate, "gate", dt, dev, x.shape),
+                check(weight, "weight", pdt, dev, (C,)), check(bias, "bias", pdt, dev, (C,)))
     return N, x.numel() // (N * C), C, G, _abi._dtype_code(x), _abi.BF16 if pdt == torch.bfloat16 else _abi.F32, \
         _ACTIVATIONS[activation], pointers, pdt
 
@@ -41,7 +40,6 @@ def group_norm(x, num_groups, weight=None, bias=None, gate=None, activation="sil
     the statistics over each (sample, group) of x [N, ..., C]
     (ttt_la_group_norm).  activation: "silu" or None.  Returns (y, mean, rstd)
     with mean, rstd fp32 [N,G], which the gradient takes."""
-    from .decay import _workspace, launch_on, need
     N, L, C, G, code, pcode, act, (px, pg, pw, pb), _ = _describe(x, num_groups, weight, bias, gate, activation)
     dev = x.device
     stats = None
@@ -51,18 +49,14 @@ def group_norm(x, num_groups, weight=None, bias=None, gate=None, activation="sil
         if out is None:
             out = torch.empty_like(x)
         stats = torch.empty((2, N, G), device=dev, dtype=torch.float32)
-        a = _abi.TttGroupNormArgs(N, L, C, G, code, pcode, act, float(eps), px, pg, pw, pb,
-                                  need(out, "out", x.dtype, dev, tuple(x.shape)), stats[0].data_ptr(),
-                                  stats[1].data_ptr())
-        lib = _abi.lib()
-        nbytes = lib.ttt_la_group_norm_workspace_size(_byref(a))
-        if nbytes:
-            w = _workspace(workspace, nbytes, dev)
-            a.workspace, a.workspace_bytes = w.data_ptr(), w.numel() * w.element_size()
-        _abi._check("ttt_la_group_norm", lib.ttt_la_group_norm(_byref(a), handle))
+        mean = stats.data_ptr()
+        block = _FORWARD(N, L, C, G, code, pcode, act, eps, px, pg, pw, pb, check(out, "out", x.dtype, dev, x.shape), mean,
+                         mean + 4 * N * G)
+        run_with_workspace("ttt_la_group_norm", "ttt_la_group_norm_workspace_size", block, workspace, dev, handle)
 
     launch_on(dev, stream, call)
-    return out, stats[0], stats[1]
+    mean, rstd = stats.unbind(0)
+    return out, mean, rstd
 
 
 def group_norm_backward(grad_y, x, num_groups, mean, rstd, weight=None, bias=None, gate=None, activation="silu",
@@ -70,26 +64,21 @@ def group_norm_backward(grad_y, x, num_groups, mean, rstd, weight=None, bias=Non
     """Gradients of group_norm (ttt_la_group_norm_backward) from what the
     forward took and its mean and rstd: a dict with dx, dgate (None without a
     gate), dweight and dbias (None without the parameter)."""
-    from .decay import _workspace, launch_on, need
     N, L, C, G, code, pcode, act, (px, pg, pw, pb), pdt = _describe(x, num_groups, weight, bias, gate, activation)
     dev = x.device
     out = {}
 
     def call(handle):
-        pgy = need(grad_y, "grad_y", x.dtype, dev, tuple(x.shape))
-        pm = need(mean, "mean", torch.float32, dev, (N, G))
-        pr = need(rstd, "rstd", torch.float32, dev, (N, G))
+        pgy = check(grad_y, "grad_y", x.dtype, dev, x.shape)
+        pm = check(mean, "mean", torch.float32, dev, (N, G))
+        pr = check(rstd, "rstd", torch.float32, dev, (N, G))
         new = lambda like: None if like is None else torch.empty_like(like)  # noqa: E731
         out.update(dx=new(x), dgate=new(gate), dweight=new(weight), dbias=new(bias))
-        ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
-        a = _abi.TttGroupNormGradArgs(N, L, C, G, code, pcode, act, pgy, px, pg, pw, pb, pm, pr, ptr(out["dx"]),
-                                      ptr(out["dgate"]), ptr(out["dweight"]), ptr(out["dbias"]))
-        lib = _abi.lib()
-        nbytes = lib.ttt_la_group_norm_backward_workspace_size(_byref(a))
-        if nbytes:
-            w = _workspace(workspace, nbytes, dev)
-            a.workspace, a.workspace_bytes = w.data_ptr(), w.numel() * w.element_size()
-        _abi._check("ttt_la_group_norm_backward", lib.ttt_la_group_norm_backward(_byref(a), handle))
+        ptr = lambda t: 0 if t is None else t.data_ptr()  # noqa: E731
+        block = _BACKWARD(N, L, C, G, code, pcode, act, pgy, px, pg, pw, pb, pm, pr, ptr(out["dx"]), ptr(out["dgate"]),
+                          ptr(out["dweight"]), ptr(out["dbias"]))
+        run_with_workspace("ttt_la_group_norm_backward", "ttt_la_group_norm_backward_workspace_size", block, workspace, dev,
+                           handle)
 
     launch_on(dev, stream, call)
     return out

@@ -44,6 +44,33 @@ def test_struct_layouts_match_c(abi):
             assert ctypes.sizeof(pairs[key]) == int(v), key
 
 
+def test_packed_blocks_are_the_structs(abi):
+    """The struct formats the bindings pack, against the ctypes mirrors (which
+    the test above holds to the C layout)."""
+    from test_layers_causal_b200._call import FORMATS
+    mirrors = {"ttt_la_decay_args": abi.TttDecayArgs, "ttt_la_decay_grad_args": abi.TttDecayGradArgs,
+               "ttt_la_decay_decode_args": abi.TttDecayDecodeArgs, "ttt_la_group_norm_args": abi.TttGroupNormArgs,
+               "ttt_la_group_norm_grad_args": abi.TttGroupNormGradArgs}
+    assert set(FORMATS) == set(mirrors)
+    for name, fmt in FORMATS.items():
+        cls = mirrors[name]
+        fields = [f for f, _ in cls._fields_ if f not in ("workspace", "workspace_bytes")]
+        has_workspace = len(fields) < len(cls._fields_)
+        assert fmt.size + (16 if has_workspace else 0) == ctypes.sizeof(cls)
+        flat, n = [], 0
+        for f, t in cls._fields_:
+            if f in fields:
+                count = t._length_ if hasattr(t, "_length_") else 1
+                base = t._type_ if count > 1 else t
+                values = [0.5] if base is ctypes.c_float else list(range(n + 1, n + 1 + count))
+                flat.append((f, values))
+                n += count
+        block = cls.from_buffer_copy(fmt.pack(*(x for _, v in flat for x in v)) + b"\0" * (16 if has_workspace else 0))
+        for f, v in flat:
+            got = getattr(block, f)
+            assert (list(got) if hasattr(got, "__len__") else [got]) == v, (name, f)
+
+
 I3, I2 = ctypes.c_int64 * 3, ctypes.c_int64 * 2
 
 
@@ -191,7 +218,7 @@ def test_binding_refuses_host_tensors_and_wrong_shapes():
 
 
 def test_output_rows_that_overlap_are_refused():
-    from test_layers_causal_b200.decay import _distinct_rows
+    from test_layers_causal_b200._call import check_distinct_rows as _distinct_rows
     x = torch.zeros(2, 3, 4, 8)
     for good in (x, x.transpose(1, 2), x.transpose(0, 2), x[:, :1], x[..., :4], torch.zeros(1, 1, 1, 8).expand(1, 1, 1, 8)):
         _distinct_rows(good, "out")
