@@ -13,7 +13,7 @@ namespace {
 // tiles).  Packed sequences are planned as one of their total length, since
 // the host does not see where they end.
 constexpr int kDecayTile = 64;
-constexpr double kDecayTotalCost = 0.5, kDecayScanTiles = 6.0;
+constexpr double kDecayTotalCost = 0.5, kDecayScanTiles = 0.75;
 int decay_plan_tokens(long long heads, int rows, int slots) {
   const int tiles = (rows + kDecayTile - 1) / kDecayTile;
   int best = tiles;
@@ -403,17 +403,20 @@ ttt_la_status ttt_la_backward_decay(const ttt_la_decay_grad_args* a, void* strea
 namespace {
 template <int DK, typename T>
 ttt_la_status launch_decay_step(const ttt::DecayStep& p, cudaStream_t st) {
+  // Accesses per lane: 8 where that leaves every SM 16 warps or more, 2 where
+  // those do, else 1 (latency counts: small blocks over all SMs).  A warp takes
+  // its rows and ends.  Measured (256 sequences x 16 heads x 128 x 128, 544 MB):
+  // 8 a lane 83 us, 4 a lane 99, 2 a lane 95; resident blocks that walk on 87
+  // to 113.
   constexpr int RPW = 32 / (DK / 4);
-  const long long rows = static_cast<long long>(p.N) * p.H * p.dv;
-  const long long slots = static_cast<long long>(sm_count()) * 8;  // blocks of 256 threads
-  constexpr int U = 4;
-  if (rows <= slots * 8 * RPW * U) {
-    // less than one wave of the deep kernel: one row group a warp, small blocks over all SMs
-    const long long warps = (rows + RPW - 1) / RPW;
-    ttt::decay_step_kernel<DK, T, 1><<<static_cast<int>((warps + 3) / 4), 128, 0, st>>>(p);
-  } else {
-    ttt::decay_step_kernel<DK, T, U><<<static_cast<int>(slots), 256, 0, st>>>(p);
-  }
+  const long long groups = (static_cast<long long>(p.N) * p.H * p.dv + RPW - 1) / RPW;  // of one access a lane
+  const long long enough = static_cast<long long>(sm_count()) * 16;
+  if (groups / 8 >= enough)
+    ttt::decay_step_kernel<DK, T, 8><<<static_cast<int>((groups + 63) / 64), 256, 0, st>>>(p);
+  else if (groups / 2 >= enough)
+    ttt::decay_step_kernel<DK, T, 2><<<static_cast<int>((groups + 15) / 16), 256, 0, st>>>(p);
+  else
+    ttt::decay_step_kernel<DK, T, 1><<<static_cast<int>((groups + 3) / 4), 128, 0, st>>>(p);
   return launched();
 }
 template <typename T>
@@ -433,7 +436,7 @@ extern "C" ttt_la_status ttt_la_decode_step_decay(const ttt_la_decay_decode_args
   if (a->dtype != TTT_LA_F32 && a->dtype != TTT_LA_BF16) return TTT_LA_ERR_INVALID_ARG;
   if (!a->log_decay || (reinterpret_cast<uintptr_t>(a->log_decay) & 3) || !a->state || !aligned16(a->state))
     return TTT_LA_ERR_INVALID_ARG;
-  if (static_cast<long long>(a->N) * a->H * a->d_v >= (1ll << 31)) return TTT_LA_ERR_INVALID_ARG;
+  if (static_cast<long long>(a->N) * a->H * a->d_v >= (1ll << 31) - (1 << 20)) return TTT_LA_ERR_INVALID_ARG;
   const void* t[4] = {a->q, a->k, a->v, a->o};
   const int64_t* stride[4] = {a->q_stride, a->k_stride, a->v_stride, a->o_stride};
   const int unit = a->dtype == TTT_LA_F32 ? 4 : 8;
