@@ -136,8 +136,8 @@ int decay_tc_plan_tokens(long long heads, int rows, int runs, int slots) {
 }
 
 // [N][H][T][d] bf16 in the order of `t`'s strides, boxes of 64 features x 128
-// tokens; features behind d read as zeros and are not written.
-bool decay_map(CUtensorMap* m, const ttt::DecayTensor& t, int N, int H, int T, int d) {
+// tokens (or `rows`); features behind d read as zeros and are not written.
+bool decay_map(CUtensorMap* m, const ttt::DecayTensor& t, int N, int H, int T, int d, int rows = ttt::kDecayTcC) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
   cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(T), static_cast<cuuint64_t>(H),
@@ -146,7 +146,7 @@ bool decay_map(CUtensorMap* m, const ttt::DecayTensor& t, int N, int H, int T, i
   const long long s[3] = {T > 1 ? t.st : d, H > 1 ? t.sh : d, N > 1 ? t.sb : d};
   cuuint64_t strides[3];
   for (int i = 0; i < 3; ++i) strides[i] = static_cast<cuuint64_t>(s[i]) * 2;
-  cuuint32_t box[4] = {64, ttt::kDecayTcC, 1, 1}, es[4] = {1, 1, 1, 1};
+  cuuint32_t box[4] = {64, static_cast<cuuint32_t>(rows), 1, 1}, es[4] = {1, 1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(t.p), dims, strides, box, es,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -184,9 +184,9 @@ ttt_la_status decay_tc_group(ttt::DecayTcArgs& a, const ttt::DecayTcRun* r, int 
   return TTT_LA_OK;
 }
 
-ttt::DecayTcRun decay_tc_run(int q, int k, int v, int o, const ttt::DecayRun& r) {
+ttt::DecayTcRun decay_tc_run(int q, int k, int v, int o, int kt, int vt, const ttt::DecayRun& r) {
   ttt::DecayTcRun t = {};
-  t.q = q, t.k = k, t.v = v, t.o = o;
+  t.q = q, t.k = k, t.v = v, t.o = o, t.kt = kt, t.vt = vt;
   t.dk = r.dk, t.dv = r.dv, t.rev = r.rev;
   t.sP = r.sP, t.sR = r.sR, t.sU = r.sU;
   t.s_in = r.s_in, t.s_in_t = r.s_in_t, t.s_out = r.s_out, t.ws = r.ws;
@@ -300,10 +300,12 @@ ttt_la_status ttt_la_forward_decay(const ttt_la_decay_args* a, void* stream) {
   ttt::DecayTcArgs m = {};
   const int batch = packed ? 1 : a->N;
   if (!decay_map(&m.map[0], r.q, batch, a->H, a->T, a->d_k) || !decay_map(&m.map[1], r.k, batch, a->H, a->T, a->d_k) ||
-      !decay_map(&m.map[2], r.v, batch, a->H, a->T, a->d_v) || !decay_map(&m.map[3], r.o, batch, a->H, a->T, a->d_v))
+      !decay_map(&m.map[2], r.v, batch, a->H, a->T, a->d_v) || !decay_map(&m.map[3], r.o, batch, a->H, a->T, a->d_v) ||
+      !decay_map(&m.map[4], r.k, batch, a->H, a->T, a->d_k, ttt::kDecayTotC) ||
+      !decay_map(&m.map[5], r.v, batch, a->H, a->T, a->d_v, ttt::kDecayTotC))
     return TTT_LA_ERR_CUDA;
   m.g = l.g, m.log_decay = a->log_decay, m.limit_ns = g_limit_ns;
-  ttt::DecayTcRun run = decay_tc_run(0, 1, 2, 3, r);
+  ttt::DecayTcRun run = decay_tc_run(0, 1, 2, 3, 4, 5, r);
   run.ws_all = decay_in_place(a);
   if (r.ws || r.s_out) {
     const ttt_la_status e = decay_tc_group(m, &run, 1, true, true, st);
@@ -378,11 +380,16 @@ ttt_la_status ttt_la_backward_decay(const ttt_la_decay_grad_args* a, void* strea
   ttt::DecayTcArgs m = {};
   const ttt::DecayTensor x[7] = {q, k, v, dO, r[0].o, r[1].o, r[2].o};
   const bool values[7] = {false, false, true, true, false, false, true};  // d_v wide
-  for (int i = 0; i < 7; ++i)
-    if (!decay_map(&m.map[i], x[i], packed ? 1 : a->N, a->H, a->T, values[i] ? a->d_v : a->d_k)) return TTT_LA_ERR_CUDA;
+  for (int i = 0; i < 11; ++i) {  // the inputs once more in the totals' tiles
+    const int j = i < 7 ? i : i - 7;
+    if (!decay_map(&m.map[i], x[j], packed ? 1 : a->N, a->H, a->T, values[j] ? a->d_v : a->d_k,
+                   i < 7 ? ttt::kDecayTcC : ttt::kDecayTotC))
+      return TTT_LA_ERR_CUDA;
+  }
   m.g = l.g, m.log_decay = a->log_decay, m.limit_ns = g_limit_ns;
   // dk reads the transpose of dv's states
-  ttt::DecayTcRun run[3] = {decay_tc_run(3, 2, 1, 4, r[0]), decay_tc_run(1, 0, 3, 6, r[2]), decay_tc_run(2, 3, 0, 5, r[1])};
+  ttt::DecayTcRun run[3] = {decay_tc_run(3, 2, 1, 4, 9, 8, r[0]), decay_tc_run(1, 0, 3, 6, 7, 10, r[2]),
+                            decay_tc_run(2, 3, 0, 5, 10, 7, r[1])};
   run[2].ws = run[1].ws, run[2].ws_t = 1;
   if (need || a->grad_state_in) {
     // (without segments only dL/dW_0 is wanted)

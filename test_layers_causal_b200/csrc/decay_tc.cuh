@@ -6,7 +6,7 @@
 // the powers of decay.cuh:
 //   Sc = Q K^T                       M = C,  N = C,  K = DK
 //   O2 = Q Wbf^T                     M = C,  N = DV, K = DK   Wbf = bf16(X)
-//   D  = V^T K~ , K~_c = w_c k_c     M = DV, N = DK, K = C
+//   D  = V^T K~ , K~_c = w_c k_c     M = DV, N = DK, K = C    K~ = bf16 pair hi + lo
 //   O1 = P V , P = bf16(weights * Sc) M = C,  N = DV, K = C
 //   o_r = O1 + (read power of r) O2 ,  X <- gamma^n X + D
 // The state X stays in registers in fp32: D is a fresh product every tile, so
@@ -15,14 +15,16 @@
 //
 // Three launches where a sequence has several segments or its final state is
 // wanted:
-//   decay_tc_total_kernel   every segment's own contribution to the state,
-//       summed over the segment in one TMEM accumulator (each token weighted
-//       by its distance to the segment's end, so nothing is rescaled), K~ as a
-//       bf16 pair hi + lo whose sum carries it to 2^-16: the states that the
-//       caller sees take no rounding to 8 bits.
+//   decay_tc_total_kernel   every segment's own contribution to the state, by
+//       tiles of 64 tokens whose products are added in fp32 registers, K~ as
+//       three bf16 parts that carry it to 2^-24: the states that the caller
+//       sees are fp32 sums of unrounded products.
 //   decay_scan_kernel       contributions -> start states and final states.
-//   decay_tc_out_kernel     the outputs.  Its X takes bf16(K~) alone, since X
-//       is read for the outputs only, as bf16.
+//   decay_tc_out_kernel     the outputs.  Rounded to bf16 on the way, once
+//       each: P (the weighted scores) and the state where it is read for O2;
+//       with the output's own rounding an output is off by 2.3e-3 of its norm,
+//       where one rounding alone costs 1.7e-3.  K~ takes two parts, since its
+//       error would come on top of the state's (2.7e-3 with one).
 //
 // Weights gamma^(r-c) <= 1 come as products of a row's and a column's power,
 // each with a distance >= 0 to the edge of a 32-column block, so no power
@@ -70,13 +72,15 @@ __device__ __forceinline__ void tmem_ld_half16(uint32_t taddr, uint32_t (&r)[16]
       : "r"(taddr));
 }
 
-constexpr int kDecayTcC = 128;      // tokens per tile
+constexpr int kDecayTcC = 128;      // tokens per tile of the outputs
+constexpr int kDecayTotC = 64;       // tokens per tile of the totals
 constexpr int kDecayTcRuns = 3;     // the most runs in one launch
-constexpr int kDecayTcMaps = 7;
+constexpr int kDecayTcMaps = 11;
 
 // One run: indices of its tensors' maps, and the recurrence's parameters.
 struct DecayTcRun {
   int q, k, v, o;           // indices into DecayTcArgs::map
+  int kt, vt;               // k and v in the totals' tiles
   int dk, dv;
   int rev;
   float sP, sR, sU;
@@ -167,10 +171,10 @@ struct DecayTcCfg {
   static constexpr int T_O1 = NSB * C, T_O2 = T_O1 + DV, T_D = T_O2 + DV;
   static_assert(DV * (DK + 4) * 4 <= STAGE, "the start state's buffer");
   static_assert(NST >= 2 && T_D + DK <= 512, "shared and tensor memory");
-  // total kernel: K (then hi) and V per stage, one lo
-  static constexpr int A_STAGE = TK + TV;
-  static constexpr int A_NST = (232448 - 2048 - TK) / A_STAGE > 6 ? 6 : (232448 - 2048 - TK) / A_STAGE;
-  static constexpr int A_SMEM = A_NST * A_STAGE + TK + 1024 + 1024;
+  // total kernel: K (then its first part) and V per stage; the other two parts twice
+  static constexpr int CT = kDecayTotC, A_TK = CT * DK * 2, A_TV = CT * DV * 2, A_STAGE = A_TK + A_TV;
+  static constexpr int A_NST = (232448 - 2048 - 4 * A_TK) / A_STAGE > 8 ? 8 : (232448 - 2048 - 4 * A_TK) / A_STAGE;
+  static constexpr int A_SMEM = A_NST * A_STAGE + 4 * A_TK + 1024 + 1024;
   static constexpr int A_THREADS = 320;                    // TMA, MMA, 8 warps
   static_assert(A_SMEM <= 232448, "shared memory");
 };
@@ -202,39 +206,43 @@ __device__ __forceinline__ void decay_state_ld(uint32_t t_d, int quad, int half,
     tmem_ld_half16(at, r);
 }
 
-// Scales the rows of a K tile (64-column blocks of C rows of 128 bytes) in
-// place by w[i], the weight of row (t >> 3) + 32 i, for thread t of 256.  LO:
-// the rest K~ - bf16(K~) goes to the tile `lo`.  (A unit's place in its row
-// does not matter here, so the swizzle is left alone.)
-template <int DK, bool LO>
-__device__ __forceinline__ void decay_scale_tile(uint8_t* kt, uint8_t* lo, int t, const float (&w)[4]) {
+// Splits a K tile (64-column blocks of C rows of 128 bytes) scaled by w[i], the
+// weight of row (t >> 3) + 32 i, for thread t of 256, into PARTS bf16 tiles of
+// decreasing size whose sum it is: the first over the tile itself, the others
+// at `rest`, `rest` + one tile.  (A unit's place in its row does not matter
+// here, so the swizzle is left alone.)
+template <int DK, int C, int PARTS>
+__device__ __forceinline__ void decay_scale_tile(uint8_t* kt, uint8_t* rest, int t, const float (&w)[C / 32]) {
 #pragma unroll
-  for (int i = 0; i < DK / 16; ++i) {
+  for (int i = 0; i < C * DK / 2048; ++i) {
     const int u = i * 256 + t;
-    uint4 x = *reinterpret_cast<const uint4*>(kt + u * 16);
-    uint32_t* xs = reinterpret_cast<uint32_t*>(&x);
-    uint4 l;
-    uint32_t* ls = reinterpret_cast<uint32_t*>(&l);
-    const f2 wt = pair(w[i & 3], w[i & 3]);
+    const uint4 x = *reinterpret_cast<const uint4*>(kt + u * 16);
+    const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+    uint32_t out[PARTS][4];
+    const f2 wt = pair(w[i % (C / 32)], w[i % (C / 32)]);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const f2 y = mul2(pair(xs[e] << 16, xs[e] & 0xffff0000u), wt);
-      xs[e] = pack_bf16x2(y);
-      if constexpr (LO)
-        ls[e] = pack_bf16x2(lo_of(y) - __uint_as_float(xs[e] << 16), hi_of(y) - __uint_as_float(xs[e] & 0xffff0000u));
+      f2 y = mul2(pair(xs[e] << 16, xs[e] & 0xffff0000u), wt);
+#pragma unroll
+      for (int r = 0; r < PARTS; ++r) {
+        out[r][e] = pack_bf16x2(y);
+        if (r + 1 < PARTS) y = add2(y, pair((out[r][e] << 16) ^ 0x80000000u, (out[r][e] & 0xffff0000u) ^ 0x80000000u));
+      }
     }
-    *reinterpret_cast<uint4*>(kt + u * 16) = x;
-    if constexpr (LO) *reinterpret_cast<uint4*>(lo + u * 16) = l;
+    *reinterpret_cast<uint4*>(kt + u * 16) = make_uint4(out[0][0], out[0][1], out[0][2], out[0][3]);
+#pragma unroll
+    for (int r = 1; r < PARTS; ++r)
+      *reinterpret_cast<uint4*>(rest + (r - 1) * (C * DK * 2) + u * 16) = make_uint4(out[r][0], out[r][1], out[r][2], out[r][3]);
   }
 }
 // Zeroes the rows >= n of a tile of D features: what is in memory behind a
 // segment's end, whatever it holds, then enters no sum.
-template <int D>
+template <int D, int C>
 __device__ __forceinline__ void decay_zero_rows(uint8_t* tile, int n, int t) {
   const uint4 z = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll 1
-  for (int u = t; u < kDecayTcC * D / 8; u += 256)
-    if (((u >> 3) & (kDecayTcC - 1)) >= n) *reinterpret_cast<uint4*>(tile + u * 16) = z;
+  for (int u = t; u < C * D / 8; u += 256)
+    if (((u >> 3) & (C - 1)) >= n) *reinterpret_cast<uint4*>(tile + u * 16) = z;
 }
 
 // try_wait that may suspend the thread for up to `hint_ns` instead of polling.
@@ -308,17 +316,17 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
 template <int DK, int DV>
 __global__ void __launch_bounds__(320, 1) decay_tc_total_kernel(const __grid_constant__ DecayTcArgs A) {
   using Cfg = DecayTcCfg<DK, DV>;
-  constexpr int C = Cfg::C, NST = Cfg::A_NST, STAGE = Cfg::A_STAGE, TK = Cfg::TK, TV = Cfg::TV, NW = Cfg::NW;
+  constexpr int C = Cfg::CT, NST = Cfg::A_NST, STAGE = Cfg::A_STAGE, TK = Cfg::A_TK, TV = Cfg::A_TV, NW = Cfg::NW;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  uint8_t* lo = smem + NST * STAGE;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(lo + TK);
+  uint8_t* rest = smem + NST * STAGE;  // [2][2] second and third parts of K~
+  uint64_t* bars = reinterpret_cast<uint64_t*>(rest + 4 * TK);
   uint64_t* full = bars;               // [NST] tile landed
   uint64_t* ready = bars + NST;        // [NST] K~ written; the product two tiles before read out
   uint64_t* empty = bars + 2 * NST;    // [NST] stage read
   uint64_t* dfull = bars + 3 * NST;    // [2] product complete
-  uint64_t* lofree = dfull + 2;        // lo read
-  uint64_t* drain = dfull + 3;
+  uint64_t* lofree = dfull + 2;        // [2] second and third parts read
+  uint64_t* drain = dfull + 4;
   uint32_t* holder = reinterpret_cast<uint32_t*>(drain + 1);
   int* sh = reinterpret_cast<int*>(holder + 1);
 
@@ -344,7 +352,8 @@ __global__ void __launch_bounds__(320, 1) decay_tc_total_kernel(const __grid_con
     }
     mbar_init(&dfull[0], 1);
     mbar_init(&dfull[1], 1);
-    mbar_init(lofree, 1);
+    mbar_init(&lofree[0], 1);
+    mbar_init(&lofree[1], 1);
     mbar_init(drain, 1);
     fence_mbar_init();
   }
@@ -369,10 +378,10 @@ __global__ void __launch_bounds__(320, 1) decay_tc_total_kernel(const __grid_con
         mbar_arrive_expect_tx(&full[st], TK + TV);
         uint8_t* d = smem + st * STAGE;
 #pragma unroll
-        for (int x = 0; x < DK / 64; ++x) tma_load_4d(&A.map[p.k], &full[st], d + x * C * 128, x * 64, y, h, sp.batch, pol);
+        for (int x = 0; x < DK / 64; ++x) tma_load_4d(&A.map[p.kt], &full[st], d + x * C * 128, x * 64, y, h, sp.batch, pol);
 #pragma unroll
         for (int x = 0; x < DV / 64; ++x)
-          tma_load_4d(&A.map[p.v], &full[st], d + TK + x * C * 128, x * 64, y, h, sp.batch, pol);
+          tma_load_4d(&A.map[p.vt], &full[st], d + TK + x * C * 128, x * 64, y, h, sp.batch, pol);
         sent = i + 1;
       }
       for (int i = max(0, sent - NST); i < sent; ++i) mbar_wait(&full[i % NST], (i / NST) & 1, lim);
@@ -381,22 +390,23 @@ __global__ void __launch_bounds__(320, 1) decay_tc_total_kernel(const __grid_con
     if (lane == 0) {
       bool dead = false;
       constexpr uint32_t ID = idesc_bf16_f32(DV, DK, true, true);
-      const uint64_t dl = sdesc_sw128(smem_u32(lo), C * 128, 1024);
       for (int i = 0; i < nt; ++i) {
         const int st = i % NST;
         const uint32_t base = smem_u32(smem) + st * STAGE;
         const uint64_t dk = sdesc_sw128(base, C * 128, 1024), dv = sdesc_sw128(base + TK, C * 128, 1024);
+        // the smallest part first, so that the sums lose least
+        const uint64_t parts[3] = {sdesc_sw128(smem_u32(rest) + ((i & 1) * 2 + 1) * TK, C * 128, 1024),
+                                   sdesc_sw128(smem_u32(rest) + (i & 1) * 2 * TK, C * 128, 1024), dk};
         decay_wait(dead, &ready[st], (i / NST) & 1, lim);
         tc_fence_after();
-        if (!dead) {
 #pragma unroll
-          for (int kk = 0; kk < C / 16; ++kk)
-            mma_bf16_ss(tmem + (i & 1) * DK, dv + mn_step(kk), dl + mn_step(kk), ID, kk > 0);
-        }
-        tc_commit(lofree);
-        if (!dead) {
+        for (int r = 0; r < 3; ++r) {
+          if (!dead) {
 #pragma unroll
-          for (int kk = 0; kk < C / 16; ++kk) mma_bf16_ss(tmem + (i & 1) * DK, dv + mn_step(kk), dk + mn_step(kk), ID, 1);
+            for (int kk = 0; kk < C / 16; ++kk)
+              mma_bf16_ss(tmem + (i & 1) * DK, dv + mn_step(kk), parts[r] + mn_step(kk), ID, r > 0 || kk > 0);
+          }
+          if (r == 1) tc_commit(&lofree[i & 1]);
         }
         tc_commit(&empty[st]);
         tc_commit(&dfull[i & 1]);
@@ -409,10 +419,10 @@ __global__ void __launch_bounds__(320, 1) decay_tc_total_kernel(const __grid_con
     const int t = static_cast<int>(threadIdx.x) - 64, quad = warp & 3, half = (warp - 2) >> 2;
     const float l = decay_log(A.log_decay, h);
     // row weights inside a tile: distance to its end (reverse: to before its start)
-    float wgt[4], acc[NW];
+    float wgt[C / 32], acc[NW];
     auto weights = [&](int n) {
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
+      for (int x = 0; x < C / 32; ++x) {
         const int r = (t >> 3) + 32 * x;
         wgt[x] = p.sU * expf(l * static_cast<float>(p.rev ? r + 1 : max(n - 1 - r, 0)));
       }
@@ -442,13 +452,15 @@ __global__ void __launch_bounds__(320, 1) decay_tc_total_kernel(const __grid_con
       decay_wait(dead, &full[st], (i / NST) & 1, lim);
       uint8_t* d = smem + st * STAGE;
       if (n < C) weights(n);
-      if (i > 0) decay_wait(dead, lofree, (i - 1) & 1, lim);
-      decay_scale_tile<DK, true>(d, lo, t, wgt);
+      if (i > 1) decay_wait(dead, &lofree[i & 1], ((i >> 1) - 1) & 1, lim);
+      uint8_t* parts = rest + (i & 1) * 2 * TK;
+      decay_scale_tile<DK, C, 3>(d, parts, t, wgt);
       if (n < C) {
         // (a thread zeroes the units that it scaled itself)
-        decay_zero_rows<DK>(d, n, t);
-        decay_zero_rows<DK>(lo, n, t);
-        decay_zero_rows<DV>(d + TK, n, t);
+        decay_zero_rows<DK, C>(d, n, t);
+        decay_zero_rows<DK, C>(parts, n, t);
+        decay_zero_rows<DK, C>(parts + TK, n, t);
+        decay_zero_rows<DV, C>(d + TK, n, t);
         weights(C);
       }
       fence_async_smem();
@@ -505,7 +517,7 @@ __global__ void __launch_bounds__(320, 1) decay_tc_total_kernel(const __grid_con
 // which run a tile ahead, have two.
 //
 // Shared memory is the next bound after HBM: an MMA reads both operands of 128
-// bytes a clock, so a tile of 128 x 128 x 128 moves about 500 KB through it;
+// bytes a clock, so a tile of 128 x 128 x 128 moves about 600 KB through it;
 // P in tensor memory saves 64 KB of that.
 template <int DK, int DV>
 __global__ void __launch_bounds__(608, 1) decay_tc_out_kernel(const __grid_constant__ DecayTcArgs A) {
@@ -689,12 +701,15 @@ __global__ void __launch_bounds__(608, 1) decay_tc_out_kernel(const __grid_const
         if (i + 1 < nt) {
           const uint32_t base = sbase + (i % NST) * STAGE;
           const uint64_t dkm = sdesc_sw128(base + TK, C * 128, 1024), dvm = sdesc_sw128(base + 2 * TK, C * 128, 1024);
+          const uint64_t dlm = sdesc_sw128(base, C * 128, 1024);  // K~'s second part, where Q was
           decay_wait(dead, &fullv[i % NST], (i / NST) & 1, lim);
           decay_wait(dead, kready, i & 1, lim);
           tc_fence_after();
           if (!dead) {
 #pragma unroll
-            for (int kk = 0; kk < C / 16; ++kk) mma_bf16_ss(t_d, dvm + mn_step(kk), dkm + mn_step(kk), ID_D, kk > 0);
+            for (int kk = 0; kk < C / 16; ++kk) mma_bf16_ss(t_d, dvm + mn_step(kk), dlm + mn_step(kk), ID_D, kk > 0);
+#pragma unroll
+            for (int kk = 0; kk < C / 16; ++kk) mma_bf16_ss(t_d, dvm + mn_step(kk), dkm + mn_step(kk), ID_D, 1);
           }
           tc_commit(dfull);
         }
@@ -879,8 +894,8 @@ __global__ void __launch_bounds__(608, 1) decay_tc_out_kernel(const __grid_const
         // scores need no mask there (queries behind the end make rows that are not stored)
         decay_wait(dead, &fullv[st], (i / NST) & 1, lim);
         __syncwarp();
-        decay_zero_rows<DK>(d + TK, n, t);
-        decay_zero_rows<DV>(d + 2 * TK, n, t);
+        decay_zero_rows<DK, C>(d + TK, n, t);
+        decay_zero_rows<DV, C>(d + 2 * TK, n, t);
         fence_async_smem();
         warp_arrive(cut, lane);
       }
@@ -891,7 +906,11 @@ __global__ void __launch_bounds__(608, 1) decay_tc_out_kernel(const __grid_const
         weights(n);
         gn = expf(l * static_cast<float>(n));
       }
-      if (more) decay_scale_tile<DK, false>(d + TK, nullptr, t, wgt);
+      if (more) {
+        decay_wait(dead, qdone, i & 1, lim);  // Q, whose place K~'s second part takes, and Wbf have been read
+        __syncwarp();
+        decay_scale_tile<DK, C, 2>(d + TK, d, t, wgt);
+      }
       if (n < C) weights(C);
       fence_async_smem();
       warp_arrive(kready, lane);
@@ -908,8 +927,6 @@ __global__ void __launch_bounds__(608, 1) decay_tc_out_kernel(const __grid_const
 #pragma unroll
         for (int e = 0; e < PIECE; ++e) w[x + e] = fmaf(gn, w[x + e], __uint_as_float(y[e]));
       }
-      decay_wait(dead, qdone, i & 1, lim);  // Wbf has been read
-      __syncwarp();
       put_w();
     }
     tc_fence_before();

@@ -179,6 +179,8 @@ def outputs(nt, nst, nsb, ragged, seed, warps=2):
                 yield "wait", fullv[st], i // nst
                 yield "arrive", cut
             yield "wait", sfull[i & 1], i // 2
+            if i + 1 < nt:
+                yield "wait", qdone, i  # K~'s second part goes where Q was
             yield "arrive", kready
             if i + 1 == nt:
                 return
@@ -186,7 +188,6 @@ def outputs(nt, nst, nsb, ragged, seed, warps=2):
             read_d[i] = read_d.get(i, 0) + 1
             if read_d[i] == warps:
                 k.drop("D")
-            yield "wait", qdone, i
             yield "arrive", wready
 
     done_o, meet, read_d = {}, {}, {}
@@ -197,7 +198,7 @@ def outputs(nt, nst, nsb, ragged, seed, warps=2):
 def totals(nt, nst, seed, warps=2):
     k = Block(seed)
     arr = lambda n, c: [Bar(c) for _ in range(n)]  # noqa: E731
-    full, ready, empty, dfull, lofree = arr(nst, 1), arr(nst, warps), arr(nst, 1), arr(2, 1), Bar(1)
+    full, ready, empty, dfull, lofree = arr(nst, 1), arr(nst, warps), arr(nst, 1), arr(2, 1), arr(2, 1)
     read = {}
 
     def load():
@@ -213,8 +214,8 @@ def totals(nt, nst, seed, warps=2):
             k.hold(("D", i & 1), f"d {i}")
 
             def lo(i=i):
-                k.drop("lo")
-                lofree.arrive()
+                k.drop(("lo", i & 1))
+                lofree[i & 1].arrive()
             yield "later", "M", lo
 
             def done(i=i):
@@ -231,10 +232,10 @@ def totals(nt, nst, seed, warps=2):
                 k.drop(("D", i & 1))
         for i in range(nt):
             yield "wait", full[i % nst], i // nst
-            if i:
-                yield "wait", lofree, i - 1
+            if i > 1:
+                yield "wait", lofree[i & 1], i // 2 - 1
             if ("lo", i) not in read:
-                k.hold("lo", f"scale {i}")
+                k.hold(("lo", i & 1), f"scale {i}")
                 read["lo", i] = 1
             yield "arrive", ready[i % nst]
             if i:
