@@ -301,8 +301,8 @@ ttt_la_status ttt_la_forward_decay(const ttt_la_decay_args* a, void* stream) {
   const int batch = packed ? 1 : a->N;
   if (!decay_map(&m.map[0], r.q, batch, a->H, a->T, a->d_k) || !decay_map(&m.map[1], r.k, batch, a->H, a->T, a->d_k) ||
       !decay_map(&m.map[2], r.v, batch, a->H, a->T, a->d_v) || !decay_map(&m.map[3], r.o, batch, a->H, a->T, a->d_v) ||
-      !decay_map(&m.map[4], r.k, batch, a->H, a->T, a->d_k, ttt::kDecayTotC) ||
-      !decay_map(&m.map[5], r.v, batch, a->H, a->T, a->d_v, ttt::kDecayTotC))
+      !decay_map(&m.map[4], r.k, batch, a->H, a->T, a->d_k, ttt::decay_total_tile(a->d_k)) ||
+      !decay_map(&m.map[5], r.v, batch, a->H, a->T, a->d_v, ttt::decay_total_tile(a->d_k)))
     return TTT_LA_ERR_CUDA;
   m.g = l.g, m.log_decay = a->log_decay, m.limit_ns = g_limit_ns;
   ttt::DecayTcRun run = decay_tc_run(0, 1, 2, 3, 4, 5, r);
@@ -380,10 +380,10 @@ ttt_la_status ttt_la_backward_decay(const ttt_la_decay_grad_args* a, void* strea
   ttt::DecayTcArgs m = {};
   const ttt::DecayTensor x[7] = {q, k, v, dO, r[0].o, r[1].o, r[2].o};
   const bool values[7] = {false, false, true, true, false, false, true};  // d_v wide
-  for (int i = 0; i < 11; ++i) {  // the inputs once more in the totals' tiles
+  for (int i = 0; i < 11; ++i) {  // the inputs once more in the totals' tiles: q and do for dv's run, k and v for dq's
     const int j = i < 7 ? i : i - 7;
     if (!decay_map(&m.map[i], x[j], packed ? 1 : a->N, a->H, a->T, values[j] ? a->d_v : a->d_k,
-                   i < 7 ? ttt::kDecayTcC : ttt::kDecayTotC))
+                   i < 7 ? ttt::kDecayTcC : ttt::decay_total_tile(j == 0 || j == 3 ? a->d_k : a->d_v)))
       return TTT_LA_ERR_CUDA;
   }
   m.g = l.g, m.log_decay = a->log_decay, m.limit_ns = g_limit_ns;

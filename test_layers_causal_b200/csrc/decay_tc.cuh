@@ -16,7 +16,7 @@
 // Three launches where a sequence has several segments or its final state is
 // wanted:
 //   decay_tc_total_kernel   every segment's own contribution to the state, by
-//       tiles of 64 tokens whose products are added in fp32 registers, K~ as
+//       tiles of 64 or 128 tokens whose products are added in fp32 registers, K~ as
 //       three bf16 parts that carry it to 2^-24: the states that the caller
 //       sees are fp32 sums of unrounded products.
 //   decay_scan_kernel       contributions -> start states and final states.
@@ -73,7 +73,9 @@ __device__ __forceinline__ void tmem_ld_half16(uint32_t taddr, uint32_t (&r)[16]
 }
 
 constexpr int kDecayTcC = 128;      // tokens per tile of the outputs
-constexpr int kDecayTotC = 64;       // tokens per tile of the totals
+// Tokens per tile of the totals, for keys of d features (padded): 64 where three
+// parts of 128 tokens would leave no room to load ahead.
+__host__ __device__ constexpr int decay_total_tile(int d) { return d <= 64 ? 128 : 64; }
 constexpr int kDecayTcRuns = 3;     // the most runs in one launch
 constexpr int kDecayTcMaps = 11;
 
@@ -161,8 +163,11 @@ struct DecayTcCfg {
   static constexpr int TK = C * DK * 2, TV = C * DV * 2;   // bytes of a tile
   static constexpr int STAGE = 2 * TK + TV;                // Q, K, V
   static constexpr int WBF = DK * DV * 2;
-  static constexpr int NST = (232448 - 2048 - WBF) / STAGE > 4 ? 4 : (232448 - 2048 - WBF) / STAGE;
-  static constexpr int BIG = NST * STAGE + WBF;
+  // K~'s second part beside the stages where two stages still fit; else over Q once that has been read
+  static constexpr bool LSEP = 2 * STAGE + WBF + TK <= 232448 - 2048;
+  static constexpr int LO = LSEP ? TK : 0, ROOM = (232448 - 2048 - WBF - LO) / STAGE;
+  static constexpr int NST = ROOM > 4 ? 4 : ROOM;
+  static constexpr int BIG = NST * STAGE + WBF + LO;
   static constexpr int SMEM = BIG + 1024 + 1024;           // + barriers and tables, + alignment
   static constexpr int THREADS = 608;                      // TMA, MMA, 8 warps P and outputs, 8 warps state, MMA
   static constexpr int NW = DK * DV / 256;                 // elements of X per state thread
@@ -172,10 +177,10 @@ struct DecayTcCfg {
   static_assert(DV * (DK + 4) * 4 <= STAGE, "the start state's buffer");
   static_assert(NST >= 2 && T_D + DK <= 512, "shared and tensor memory");
   // total kernel: K (then its first part) and V per stage; the other two parts twice
-  static constexpr int CT = kDecayTotC, A_TK = CT * DK * 2, A_TV = CT * DV * 2, A_STAGE = A_TK + A_TV;
+  static constexpr int CT = decay_total_tile(DK), A_TK = CT * DK * 2, A_TV = CT * DV * 2, A_STAGE = A_TK + A_TV;
   static constexpr int A_NST = (232448 - 2048 - 4 * A_TK) / A_STAGE > 8 ? 8 : (232448 - 2048 - 4 * A_TK) / A_STAGE;
   static constexpr int A_SMEM = A_NST * A_STAGE + 4 * A_TK + 1024 + 1024;
-  static constexpr int A_THREADS = 320;                    // TMA, MMA, 8 warps
+  static constexpr int A_THREADS = 576;                    // TMA, MMA, 8 warps that split K~, 8 that add products
   static_assert(A_SMEM <= 232448, "shared memory");
 };
 
@@ -314,7 +319,7 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
 // the walking order to its start, so that the tiles the output kernel reads
 // first are the ones last left in L2.
 template <int DK, int DV>
-__global__ void __launch_bounds__(320, 1) decay_tc_total_kernel(const __grid_constant__ DecayTcArgs A) {
+__global__ void __launch_bounds__(576, 1) decay_tc_total_kernel(const __grid_constant__ DecayTcArgs A) {
   using Cfg = DecayTcCfg<DK, DV>;
   constexpr int C = Cfg::CT, NST = Cfg::A_NST, STAGE = Cfg::A_STAGE, TK = Cfg::A_TK, TV = Cfg::A_TV, NW = Cfg::NW;
   extern __shared__ uint8_t smem_raw[];
@@ -322,11 +327,12 @@ __global__ void __launch_bounds__(320, 1) decay_tc_total_kernel(const __grid_con
   uint8_t* rest = smem + NST * STAGE;  // [2][2] second and third parts of K~
   uint64_t* bars = reinterpret_cast<uint64_t*>(rest + 4 * TK);
   uint64_t* full = bars;               // [NST] tile landed
-  uint64_t* ready = bars + NST;        // [NST] K~ written; the product two tiles before read out
+  uint64_t* ready = bars + NST;        // [NST] K~ written
   uint64_t* empty = bars + 2 * NST;    // [NST] stage read
   uint64_t* dfull = bars + 3 * NST;    // [2] product complete
   uint64_t* lofree = dfull + 2;        // [2] second and third parts read
-  uint64_t* drain = dfull + 4;
+  uint64_t* dfree = dfull + 4;         // [2] product read out
+  uint64_t* drain = dfull + 6;
   uint32_t* holder = reinterpret_cast<uint32_t*>(drain + 1);
   int* sh = reinterpret_cast<int*>(holder + 1);
 
@@ -352,6 +358,8 @@ __global__ void __launch_bounds__(320, 1) decay_tc_total_kernel(const __grid_con
     }
     mbar_init(&dfull[0], 1);
     mbar_init(&dfull[1], 1);
+    mbar_init(&dfree[0], 8);
+    mbar_init(&dfree[1], 8);
     mbar_init(&lofree[0], 1);
     mbar_init(&lofree[1], 1);
     mbar_init(drain, 1);
@@ -398,6 +406,7 @@ __global__ void __launch_bounds__(320, 1) decay_tc_total_kernel(const __grid_con
         const uint64_t parts[3] = {sdesc_sw128(smem_u32(rest) + ((i & 1) * 2 + 1) * TK, C * 128, 1024),
                                    sdesc_sw128(smem_u32(rest) + (i & 1) * 2 * TK, C * 128, 1024), dk};
         decay_wait(dead, &ready[st], (i / NST) & 1, lim);
+        if (i > 1) decay_wait(dead, &dfree[i & 1], ((i >> 1) - 1) & 1, lim);
         tc_fence_after();
 #pragma unroll
         for (int r = 0; r < 3; ++r) {
@@ -414,12 +423,13 @@ __global__ void __launch_bounds__(320, 1) decay_tc_total_kernel(const __grid_con
       tc_commit(drain);
       mbar_wait(drain, 0, lim);
     }
-  } else {
+  } else if (warp < 10) {
+    // K~ in three parts
     bool dead = false;
-    const int t = static_cast<int>(threadIdx.x) - 64, quad = warp & 3, half = (warp - 2) >> 2;
+    const int t = static_cast<int>(threadIdx.x) - 64;
     const float l = decay_log(A.log_decay, h);
     // row weights inside a tile: distance to its end (reverse: to before its start)
-    float wgt[C / 32], acc[NW];
+    float wgt[C / 32];
     auto weights = [&](int n) {
 #pragma unroll
       for (int x = 0; x < C / 32; ++x) {
@@ -428,31 +438,13 @@ __global__ void __launch_bounds__(320, 1) decay_tc_total_kernel(const __grid_con
       }
     };
     weights(C);
-#pragma unroll
-    for (int e = 0; e < NW; ++e) acc[e] = 0.f;
-    // adds the i-th tile's product, weighted by the tile's distance
-    auto add = [&](int i) {
-      const int at = tile_at(i) * C, n = min(C, sp.len - at);
-      const float f = expf(l * static_cast<float>(p.rev ? at : sp.len - at - n));
-      decay_wait(dead, &dfull[i & 1], (i >> 1) & 1, lim);
-      __syncwarp();
-      tc_fence_after();
-      constexpr int PIECE = DV == 128 ? 16 : NW;
-#pragma unroll
-      for (int x = 0; x < NW; x += PIECE) {
-        uint32_t r[PIECE];
-        decay_state_ld<DK, DV>(tmem + (i & 1) * DK, quad, half, x, r);
-        tmem_ld_wait();
-#pragma unroll
-        for (int e = 0; e < PIECE; ++e) acc[x + e] = fmaf(f, __uint_as_float(r[e]), acc[x + e]);
-      }
-    };
     for (int i = 0; i < nt; ++i) {
       const int st = i % NST, n = min(C, sp.len - tile_at(i) * C);
       decay_wait(dead, &full[st], (i / NST) & 1, lim);
       uint8_t* d = smem + st * STAGE;
       if (n < C) weights(n);
       if (i > 1) decay_wait(dead, &lofree[i & 1], ((i >> 1) - 1) & 1, lim);
+      __syncwarp();
       uint8_t* parts = rest + (i & 1) * 2 * TK;
       decay_scale_tile<DK, C, 3>(d, parts, t, wgt);
       if (n < C) {
@@ -465,9 +457,32 @@ __global__ void __launch_bounds__(320, 1) decay_tc_total_kernel(const __grid_con
       }
       fence_async_smem();
       warp_arrive(&ready[st], lane);
-      if (i > 0) add(i - 1);
     }
-    if (nt > 0) add(nt - 1);
+  } else {
+    // the sum of the tiles' products, each weighted by its tile's distance
+    bool dead = false;
+    const int quad = warp & 3, half = (warp - 10) >> 2;
+    const float l = decay_log(A.log_decay, h);
+    float acc[NW];
+#pragma unroll
+    for (int e = 0; e < NW; ++e) acc[e] = 0.f;
+    for (int i = 0; i < nt; ++i) {
+      const int at = tile_at(i) * C, n = min(C, sp.len - at);
+      const float f = expf(l * static_cast<float>(p.rev ? at : sp.len - at - n));
+      decay_wait(dead, &dfull[i & 1], (i >> 1) & 1, lim);
+      __syncwarp();
+      tc_fence_after();
+      constexpr int PIECE = DV == 128 ? 16 : NW;
+#pragma unroll
+      for (int x = 0; x < NW; x += PIECE) {
+        uint32_t r[PIECE];
+        decay_state_ld<DK, DV>(tmem + (i & 1) * DK, quad, half, x, r);
+        tmem_ld_wait();
+        if (x + PIECE == NW) warp_arrive(&dfree[i & 1], lane);
+#pragma unroll
+        for (int e = 0; e < PIECE; ++e) acc[x + e] = fmaf(f, __uint_as_float(r[e]), acc[x + e]);
+      }
+    }
     int row, col;
     decay_state_at<DK, DV>(quad, half, lane, row, col);
     const size_t dd = static_cast<size_t>(p.dk) * p.dv, off = static_cast<size_t>(row) * p.dk;
@@ -701,7 +716,7 @@ __global__ void __launch_bounds__(608, 1) decay_tc_out_kernel(const __grid_const
         if (i + 1 < nt) {
           const uint32_t base = sbase + (i % NST) * STAGE;
           const uint64_t dkm = sdesc_sw128(base + TK, C * 128, 1024), dvm = sdesc_sw128(base + 2 * TK, C * 128, 1024);
-          const uint64_t dlm = sdesc_sw128(base, C * 128, 1024);  // K~'s second part, where Q was
+          const uint64_t dlm = sdesc_sw128(Cfg::LSEP ? sbase + NST * STAGE + Cfg::WBF : base, C * 128, 1024);
           decay_wait(dead, &fullv[i % NST], (i / NST) & 1, lim);
           decay_wait(dead, kready, i & 1, lim);
           tc_fence_after();
@@ -907,9 +922,11 @@ __global__ void __launch_bounds__(608, 1) decay_tc_out_kernel(const __grid_const
         gn = expf(l * static_cast<float>(n));
       }
       if (more) {
-        decay_wait(dead, qdone, i & 1, lim);  // Q, whose place K~'s second part takes, and Wbf have been read
-        __syncwarp();
-        decay_scale_tile<DK, C, 2>(d + TK, d, t, wgt);
+        if (!Cfg::LSEP) {
+          decay_wait(dead, qdone, i & 1, lim);  // Q, whose place K~'s second part takes, has been read
+          __syncwarp();
+        }
+        decay_scale_tile<DK, C, 2>(d + TK, Cfg::LSEP ? smem + NST * STAGE + Cfg::WBF : d, t, wgt);
       }
       if (n < C) weights(C);
       fence_async_smem();
@@ -926,6 +943,10 @@ __global__ void __launch_bounds__(608, 1) decay_tc_out_kernel(const __grid_const
         tmem_ld_wait();
 #pragma unroll
         for (int e = 0; e < PIECE; ++e) w[x + e] = fmaf(gn, w[x + e], __uint_as_float(y[e]));
+      }
+      if (Cfg::LSEP) {
+        decay_wait(dead, qdone, i & 1, lim);  // Wbf has been read
+        __syncwarp();
       }
       put_w();
     }

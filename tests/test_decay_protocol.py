@@ -68,8 +68,9 @@ class Block:
             state[x] = next(self.roles[x], None)
 
 
-def outputs(nt, nst, nsb, ragged, seed, warps=2):
-    """The output kernel: `ragged`: index of the tile that ends early, or -1."""
+def outputs(nt, nst, nsb, ragged, seed, beside=False, warps=2):
+    """The output kernel.  `ragged`: index of the tile that ends early, or -1;
+    `beside`: K~'s second part has a place of its own."""
     k = Block(seed)
     arr = lambda n, c: [Bar(c) for _ in range(n)]  # noqa: E731
     full, fullv, free_qk, empty, sfull, pready = arr(nst, 1), arr(nst, 1), arr(nst, 2), arr(nst, 1), arr(2, 1), arr(2, warps)
@@ -179,7 +180,7 @@ def outputs(nt, nst, nsb, ragged, seed, warps=2):
                 yield "wait", fullv[st], i // nst
                 yield "arrive", cut
             yield "wait", sfull[i & 1], i // 2
-            if i + 1 < nt:
+            if i + 1 < nt and not beside:
                 yield "wait", qdone, i  # K~'s second part goes where Q was
             yield "arrive", kready
             if i + 1 == nt:
@@ -188,6 +189,8 @@ def outputs(nt, nst, nsb, ragged, seed, warps=2):
             read_d[i] = read_d.get(i, 0) + 1
             if read_d[i] == warps:
                 k.drop("D")
+            if beside:
+                yield "wait", qdone, i
             yield "arrive", wready
 
     done_o, meet, read_d = {}, {}, {}
@@ -198,7 +201,7 @@ def outputs(nt, nst, nsb, ragged, seed, warps=2):
 def totals(nt, nst, seed, warps=2):
     k = Block(seed)
     arr = lambda n, c: [Bar(c) for _ in range(n)]  # noqa: E731
-    full, ready, empty, dfull, lofree = arr(nst, 1), arr(nst, warps), arr(nst, 1), arr(2, 1), arr(2, 1)
+    full, ready, empty, dfull, lofree, dfree = arr(nst, 1), arr(nst, warps), arr(nst, 1), arr(2, 1), arr(2, 1), arr(2, warps)
     read = {}
 
     def load():
@@ -211,6 +214,8 @@ def totals(nt, nst, seed, warps=2):
     def mma():
         for i in range(nt):
             yield "wait", ready[i % nst], i // nst
+            if i > 1:
+                yield "wait", dfree[i & 1], i // 2 - 1
             k.hold(("D", i & 1), f"d {i}")
 
             def lo(i=i):
@@ -225,11 +230,6 @@ def totals(nt, nst, seed, warps=2):
             yield "later", "M", done
 
     def scale(w):
-        def add(i):
-            yield "wait", dfull[i & 1], i // 2
-            read[i] = read.get(i, 0) + 1
-            if read[i] == warps:
-                k.drop(("D", i & 1))
         for i in range(nt):
             yield "wait", full[i % nst], i // nst
             if i > 1:
@@ -238,11 +238,16 @@ def totals(nt, nst, seed, warps=2):
                 k.hold(("lo", i & 1), f"scale {i}")
                 read["lo", i] = 1
             yield "arrive", ready[i % nst]
-            if i:
-                yield from add(i - 1)
-        yield from add(nt - 1)
 
-    k.roles = [load(), mma()] + [scale(w) for w in range(warps)]
+    def add(w):
+        for i in range(nt):
+            yield "wait", dfull[i & 1], i // 2
+            read[i] = read.get(i, 0) + 1
+            if read[i] == warps:
+                k.drop(("D", i & 1))
+            yield "arrive", dfree[i & 1]
+
+    k.roles = [load(), mma()] + [scale(w) for w in range(warps)] + [add(w) for w in range(warps)]
     k.run()
 
 
@@ -252,7 +257,7 @@ def test_outputs_protocol(nsb, nst):
     for nt in range(1, 10):
         for ragged in {-1, 0, nt - 1}:
             for seed in range(60):
-                outputs(nt, nst, nsb, ragged, 1000 * nt + seed)
+                outputs(nt, nst, nsb, ragged, 1000 * nt + seed, beside=seed % 2 == 0)
 
 
 @pytest.mark.parametrize("nst", [2, 3, 6])
