@@ -383,15 +383,18 @@ TTT_LA_API ttt_la_status ttt_la_backward_chunked(const ttt_la_grad_args *args, v
  * state_out may be state_in.
  *
  * dtype bf16: d_k and d_v multiples of 8 up to 256; fp32: multiples of 4 up to
- * 256; others TTT_LA_ERR_UNSUPPORTED.  Sums and states are fp32.  A value that
- * is not finite may reach every output of its own tile of 64 tokens, earlier
+ * 256; others TTT_LA_ERR_UNSUPPORTED.  Sums and states are fp32;
+ * bf16 up to 128 wide runs on the tensor cores, where the weighted scores and
+ * the state as it is read for an output are rounded to bf16 once.  A value that
+ * is not finite may reach every output of its own tile of 128 tokens, earlier
  * ones included, and all later ones of its (sequence, head), never another
  * sequence or head.
  *
  * segment_tokens: tokens of a sequence handled by one block, a multiple of 64;
  * 0 = automatic (fills the SMs).  The workspace holds one state per segment
- * where sequences have several (size query; pointers are not read, but whether
- * cu_seqlens is NULL is). */
+ * where sequences have several, or where state_out is state_in (size query; of
+ * the pointers only cu_seqlens' being NULL and state_out's being state_in
+ * count). */
 typedef struct ttt_la_decay_args {
   int32_t N, H, T, d_k, d_v;
   int32_t dtype;            /* of q, k, v, o */
@@ -467,8 +470,8 @@ TTT_LA_API ttt_la_status ttt_la_decode_step_decay(const ttt_la_decay_decode_args
  * activation: 0 none, 1 silu (silu(z) = z / (1 + exp(-z))).  weight, bias [C]
  * of param_dtype, or NULL (1, 0).  mean, rstd: fp32 [N,G], written (the
  * gradient reads them).  Any C and any width of a group; G <= 4096, else
- * TTT_LA_ERR_UNSUPPORTED.  y must not overlap x, gate,
- * weight or bias. */
+ * TTT_LA_ERR_UNSUPPORTED.  x, gate and y start on 16 bytes.  y must not overlap
+ * x, gate, weight or bias. */
 typedef struct ttt_la_group_norm_args {
   int32_t N, L, C, G;
   int32_t dtype;            /* of x, gate, y */

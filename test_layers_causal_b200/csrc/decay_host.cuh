@@ -106,7 +106,9 @@ ttt_la_status decay_simt_runs(const ttt::DecayGeom& g, const ttt::DecayRun* r, i
 }
 
 // ------------------------------------------------- tensor-core kernels ----
-bool decay_on_tc(int dtype, int T, int dk, int dv) { return dtype == TTT_LA_BF16 && T > 0 && dk <= 128 && dv <= 128; }
+// (below half a tile the fp32 kernel is as fast, and rounds nothing but the
+// result: with a token or two the one rounding of a score is a whole row's)
+bool decay_on_tc(int dtype, int T, int dk, int dv) { return dtype == TTT_LA_BF16 && T >= 64 && dk <= 128 && dv <= 128; }
 
 // Tokens per segment of the tensor-core kernels, whose blocks have an SM each.
 // `heads` sequences of `rows` tokens, `runs` outputs of each.  In units of one
@@ -115,7 +117,7 @@ bool decay_on_tc(int dtype, int T, int dk, int dv) { return dtype == TTT_LA_BF16
 // that, and cutting the scan.  Whether the final state is asked for plays no
 // part, so that the outputs' bits do not depend on it.
 constexpr double kDecayBlock = 2.0, kDecayTotal = 0.5, kDecayScan = 2.0;
-int decay_tc_plan_tokens(long long heads, int rows, int runs, int slots) {
+int decay_tc_plan_tokens(long long heads, int rows, int runs, bool packed, int slots) {
   const int tiles = (rows + ttt::kDecayTcC - 1) / ttt::kDecayTcC;
   int best = tiles;
   double cost = 1e30;
@@ -131,6 +133,13 @@ int decay_tc_plan_tokens(long long heads, int rows, int runs, int slots) {
       best = per;
     }
     if (heads * n * runs > 8ll * slots) break;
+  }
+  // Packed sequences end where they end, and what fills the SMs evenly as one long one leaves them waiting for the
+  // longest: at least 1.3 blocks for each SM, but no segment below 512 tokens for that (B200: 3641 tokens in 5
+  // sequences, gradient of 12 heads, 104 us at one block an SM, 83 at 640 tokens; 12385 in 10, prompt, 142 and 135).
+  if (packed) {
+    const long long even = static_cast<long long>(rows) * heads * runs * 10 / (13ll * slots) / ttt::kDecayTcC;
+    best = static_cast<int>(std::min<long long>(best, std::max<long long>(even, 512 / ttt::kDecayTcC)));
   }
   return static_cast<int>(std::min<long long>(static_cast<long long>(best) * ttt::kDecayTcC, 1 << 30));
 }
@@ -243,7 +252,7 @@ int decay_segment_tokens(int asked, const int32_t* cu, int N, int H, int T, int 
   if (asked > 0) return asked;
   const int rows = std::max(1, T);
   const long long seqs = cu ? 1 : N;
-  if (decay_on_tc(dtype, T, dk, dv)) return decay_tc_plan_tokens(seqs * H, rows, runs, sm_count());
+  if (decay_on_tc(dtype, T, dk, dv)) return decay_tc_plan_tokens(seqs * H, rows, runs, cu != nullptr, sm_count());
   const int widest = runs > 1 ? std::max(dk, dv) : dv;
   return decay_plan_tokens(seqs * H * ((widest + ttt::kDecayVT - 1) / ttt::kDecayVT), rows, sm_count() * 2);
 }

@@ -9,11 +9,10 @@ u = 2^-8 is half a bf16 step relative to the value, e = 2^-24 half an fp32 step.
     off by less than 2 (T / 32 + 4) steps (at most T / 32 + 1 products of
     powers, each power within 2 steps and its exponent within one, x exp(-x) < 1):
     |err| <= (T + d + T / 8 + 32) e A for outputs and states.
-  bf16 inputs: the same in fp32, and on the tensor cores the weighted scores,
-    the update's weighted operand and the state read for an output are each
-    rounded to bf16 once, at most two of them in one product chain, and the
-    result once: |err| <= u |x| + 2.1 u A.  States take no rounding below
-    2^-16 (a bf16 pair), and the tensor cores add in at least 22 bits:
+  bf16 inputs: the same in fp32, and on the tensor cores a product chain has
+    one rounding to bf16 (a weighted score, or the state as it is read) beside
+    the result's: |err| <= u |x| + 2.1 u A leaves room for one more.  States
+    take no rounding below 2^-16, and the tensor cores add in at least 22 bits:
     |err| <= (2^-16 + 2^-22 (T / 16 + 16)) A.
 """
 import math
@@ -319,6 +318,49 @@ def test_many_short_sequences():
     c = _make(lens, 1, 64, 64, "bf16", True, "tokens", True, seed=33)
     o, W = ttt.forward_decay(c["q"], c["k"], c["v"], c["ld"], cu_seqlens=c["cu"], state_in=c["W0"])
     _check_forward(c, o, W, "bf16", np.float64(0.125))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_no_rows_at_all(dtype):
+    """Only empty sequences: the states pass through, forwards and backwards."""
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    z = torch.empty(1, 2, 0, 64, dtype=dt, device="cuda")
+    cu = torch.zeros(4, dtype=torch.int32, device="cuda")
+    W0, dW = (torch.randn(3, 2, 64, 64, generator=torch.Generator().manual_seed(i)).cuda() for i in (1, 2))
+    ld = _log_decay(2).cuda()
+    o, W = ttt.forward_decay(z, z, z, ld, cu_seqlens=cu, state_in=W0)
+    assert o.shape == z.shape and torch.equal(W, W0)
+    g = ttt.backward_decay(z, z, z, z, ld, cu_seqlens=cu, state_in=W0, grad_state=dW)
+    assert torch.equal(g["dW0"], dW)
+
+
+def test_two_host_threads_on_two_streams():
+    """Calls of two threads at once, each on its own stream, give the bits of
+    one after the other."""
+    import threading
+    cs = [_make([500, 500], 2, 128, 128, "bf16", False, "tokens", True, seed=70 + i) for i in range(2)]
+
+    def both(c):
+        o, W = ttt.forward_decay(c["q"], c["k"], c["v"], c["ld"], state_in=c["W0"])
+        return [o, W, *ttt.backward_decay(c["q"], c["k"], c["v"], c["dO"], c["ld"], state_in=c["W0"]).values()]
+
+    want = [both(c) for c in cs]
+    torch.cuda.synchronize()
+    got = [None, None]
+
+    def work(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(10):
+                got[i] = both(cs[i])
+            torch.cuda.current_stream().synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for a, b in zip(want, got):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
 
 
 @pytest.mark.parametrize("cu", [[0, 500, 90, 200], [-7, 100, 100, 1 << 30], [200, 200, 0, 0]])
