@@ -317,7 +317,12 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
 // ------------------------------------------------------------- totals ----
 // One block per (segment, head, run).  Tiles are walked from the far end of
 // the walking order to its start, so that the tiles the output kernel reads
-// first are the ones last left in L2.
+// first are the ones last left in L2.  Warps 0 load, 1 issues, 2-9 split K~ into
+// its parts, 10-17 add the products.  Bound by shared memory, through which 192
+// KB pass for 64 tokens of 128 x 128 (three products, K read and three parts
+// written).  Measured: 1 x 8 x 65536 x 128 73 us (268 MB read, 3.7 TB/s; 54 us
+// with two parts, 82 with one set of warps for both), 4 x 16 x 4096 x 64 27 us
+// (33 with tiles of 64 tokens).
 template <int DK, int DV>
 __global__ void __launch_bounds__(576, 1) decay_tc_total_kernel(const __grid_constant__ DecayTcArgs A) {
   using Cfg = DecayTcCfg<DK, DV>;
@@ -531,9 +536,12 @@ __global__ void __launch_bounds__(576, 1) decay_tc_total_kernel(const __grid_con
 // barrier, something that every waiter does after its wait.  Scores and P,
 // which run a tile ahead, have two.
 //
-// Shared memory is the next bound after HBM: an MMA reads both operands of 128
-// bytes a clock, so a tile of 128 x 128 x 128 moves about 600 KB through it;
-// P in tensor memory saves 64 KB of that.
+// Shared memory is the bound before HBM: an MMA reads both operands of 128
+// bytes a clock, so a tile of 128 x 128 x 128 moves about 600 KB through it, of
+// which P in tensor memory saves 64; a tile took 5700 cycles with one part of
+// K~ and takes 7100 with two.  Measured: 1 x 8 x 65536 x 128 125 us (537 MB,
+// 4.3 TB/s), 4 x 16 x 4096 x 64 40 us, the gradient's three runs of 2 x 16 x
+// 8192 x 128 192 us.
 template <int DK, int DV>
 __global__ void __launch_bounds__(608, 1) decay_tc_out_kernel(const __grid_constant__ DecayTcArgs A) {
   using Cfg = DecayTcCfg<DK, DV>;

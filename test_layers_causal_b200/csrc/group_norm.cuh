@@ -254,6 +254,7 @@ struct GnParam {
 // registers, one unit a thread, so the values are read once.  A thread keeps
 // its channels over all its rows, with weight and bias in registers.  Block
 // (x, y): units [x width, (x + 1) width) of rows [y per, (y + 1) per).
+// 16384 x 2048 bf16 gated: 44 us (201 MB, 4.6 TB/s), bound by instruction issue.
 template <typename T, int V, bool GATE, bool ACT>
 __global__ void __launch_bounds__(256, 4) gn_row_kernel(const GnParams p, int lanes) {
   constexpr int P = V / 2, NT = GATE ? 2 : 1;
@@ -305,7 +306,8 @@ __global__ void __launch_bounds__(256, 4) gn_row_kernel(const GnParams p, int la
 }
 
 // Its gradient: dw and db gather in registers over the thread's rows; the
-// block's sums go to part[2][gridDim.y][C].
+// block's sums go to part[2][gridDim.y][C].  The same rows: 69 us (336 MB, 4.9
+// TB/s) and 8 for the parameters' sums.
 template <typename T, int V, bool GATE, bool ACT>
 __global__ void __launch_bounds__(256, 3) gn_row_grad_kernel(const GnParams p, int lanes) {
   constexpr int P = V / 2, NT = GATE ? 3 : 2;
@@ -424,7 +426,8 @@ __device__ __forceinline__ void gn_rows(int L, int rows, int k, int& l0, int& l1
   l1 = static_cast<int>(min(static_cast<long long>(L), static_cast<long long>(l0) + rows));
 }
 
-// Statistics of one split of one sample: part[N][splits][G] of (mean, m2), or,
+// Statistics of one split of one sample (6 x 4225 x 320 fp32: 18 us, of which a
+// step's barrier and its wait are most): part[N][splits][G] of (mean, m2), or,
 // where a sample is one split, mean and rstd.  Dynamic shared memory: G
 // Moments.
 template <typename T, int V>
@@ -596,7 +599,8 @@ __global__ void __launch_bounds__(256) gn_apply_kernel(const GnParams p) {
 }
 
 // Gradient, first pass: part[2][N][splits][C], the sums of dt hat and of dt
-// over a split's positions; also dgate.
+// over a split's positions; also dgate.  8 x 4096 x 512 bf16: 27 us, the third
+// pass as long.
 template <typename T, int V, bool GATE, bool ACT>
 __global__ void __launch_bounds__(256, 3) gn_grad_sums_kernel(const GnParams p) {
   constexpr int P = Unit<T, V>::P, NT = GATE ? 3 : 2;
