@@ -748,7 +748,7 @@ __global__ void __launch_bounds__(608, 1) decay_tc_out_kernel(const __grid_const
     bool dead = false;
     const int quad = warp & 3, half = (warp - 2) >> 2, r = quad * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
-    // 32-column blocks between P's two halves of zeros and of weights: distance of rows and columns in blocks,
+    // for each of its two 32-column blocks: how many blocks the rows are past it (0: the diagonal, below 0: zeros),
     // and the row's power to the block's near edge
     int dist[2];
     float edge[2];
