@@ -119,6 +119,32 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint64
   }
 }
 
+// try_wait that may suspend the thread for up to `hint_ns` instead of polling.
+__device__ __forceinline__ bool mbar_try_wait_hint(uint32_t addr, uint32_t parity, uint32_t hint_ns) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(addr), "r"(parity), "r"(hint_ns)
+      : "memory");
+  return ok != 0;
+}
+// mbar_wait with tries that suspend, so that waiting warps leave the issue slots
+// to the others.
+__device__ __forceinline__ bool mbar_wait_suspended(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
+  const uint32_t a = smem_u32(bar);
+  if (mbar_try_wait_hint(a, parity, 20000)) return true;
+  const uint64_t t0 = globaltimer_ns();
+#pragma unroll 1
+  while (!mbar_try_wait_hint(a, parity, 20000)) {
+    if (globaltimer_ns() - t0 > limit_ns) {
+      record_timeout();
+      return false;
+    }
+  }
+  return true;
+}
+
 // ------------------------------------------- programmatic launches ----
 // A kernel launched programmatically (launch_after on the host) starts when
 // every block of the kernel before it has called launch_next or ended.  Before

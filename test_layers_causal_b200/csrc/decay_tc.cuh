@@ -250,16 +250,6 @@ __device__ __forceinline__ void decay_zero_rows(uint8_t* tile, int n, int t) {
     if (((u >> 3) & (C - 1)) >= n) *reinterpret_cast<uint4*>(tile + u * 16) = z;
 }
 
-// try_wait that may suspend the thread for up to `hint_ns` instead of polling.
-__device__ __forceinline__ bool mbar_try_wait_hint(uint32_t addr, uint32_t parity, uint32_t hint_ns) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(addr), "r"(parity), "r"(hint_ns)
-      : "memory");
-  return ok != 0;
-}
 // The start state into registers through shared memory: 256 threads read whole
 // rows (a thread's own row would be a line of its own in each load: measured
 // 7 us for 128 x 128 where this takes 1), `buf` holds [DV][DK + 4] floats.
@@ -292,20 +282,9 @@ __device__ __forceinline__ void decay_state_in(float* buf, const float* src, boo
   }
 }
 
-// mbar_wait with suspending tries; nothing once `dead`.
+// A suspending wait; nothing once `dead`.
 __device__ __forceinline__ void decay_wait(bool& dead, uint64_t* bar, uint32_t parity, uint64_t lim) {
-  if (dead) return;
-  const uint32_t a = smem_u32(bar);
-  if (mbar_try_wait_hint(a, parity, 20000)) return;
-  const uint64_t t0 = globaltimer_ns();
-#pragma unroll 1
-  while (!mbar_try_wait_hint(a, parity, 20000)) {
-    if (globaltimer_ns() - t0 > lim) {
-      atomicMax(&g_status, kStatusTimeout);
-      dead = true;
-      return;
-    }
-  }
+  if (!dead) dead = !mbar_wait_suspended(bar, parity, lim);
 }
 // This warp's writes (and tensor memory reads) before one arrival for it.
 __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {

@@ -207,7 +207,7 @@ struct GnRing {
         for (; sent < min(S, steps); ++sent) issue(sent);
       for (int k = 0; k < steps; ++k) {
         const int st = (used + k) % S;
-        if (!dead) dead = !mbar_wait(&full[st], ((used + k) / S) & 1, limit_ns);
+        if (!dead) dead = !mbar_wait_suspended(&full[st], ((used + k) / S) & 1, limit_ns);
         uint4 raw[NT];
 #pragma unroll
         for (int i = 0; i < NT; ++i) raw[i] = ld_shared_v4(smem_u32(buf) + (st * NT + i) * kGnStage + tid * 16);
