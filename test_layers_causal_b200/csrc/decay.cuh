@@ -165,7 +165,7 @@ __device__ __forceinline__ const float* decay_start(const DecayRun& p, const Dec
 // --------------------------------------------------------------- scan ----
 // In place over ws: the contribution of each segment of a sequence becomes the
 // state the segment starts from.  One thread per 4 elements of a (sequence,
-// head)'s state, all segments in order (reverse runs: last to first); eight
+// head)'s state, all segments in order (reverse runs: last to first); four
 // loads are in flight at a time, since each is a round trip to L2.  FINAL: the
 // last segment walked has left its contribution too, and the state behind it
 // goes to s_out; `all` takes in sequences of one segment.
@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(256) decay_scan_kernel(const DecayScans ps, co
   const size_t pitch = static_cast<size_t>(g.H) * dd;
   float* w = p.ws + (static_cast<size_t>(first) * g.H + h) * dd + e;
   const int sums = FINAL && p.s_out ? nseg : nseg - 1;  // contributions that are there
-  constexpr int U = 8;
+  constexpr int U = 4;
   for (int i0 = 0; i0 < nseg; i0 += U) {
     float4 t[U];
 #pragma unroll
