@@ -18,6 +18,8 @@
 // formula), so a mean far from zero costs no digits.  Every sum has a fixed
 // order: the same call gives the same bits.
 #pragma once
+#include <type_traits>
+
 #include "common.cuh"
 
 namespace ttt {
@@ -426,65 +428,78 @@ __device__ __forceinline__ void gn_rows(int L, int rows, int k, int& l0, int& l1
   l1 = static_cast<int>(min(static_cast<long long>(L), static_cast<long long>(l0) + rows));
 }
 
-// Statistics of one split of one sample (6 x 4225 x 320 fp32: 18 us, of which a
-// step's barrier and its wait are most): part[N][splits][G] of (mean, m2), or,
-// where a sample is one split, mean and rstd.  Dynamic shared memory: G
-// Moments.
+// Statistics of one split of one sample: part[N][splits][G] of (mean, m2), or,
+// where a sample is one split, mean and rstd.  Plain loads, a batch of eight
+// positions in flight a thread (6 x 4225 x 320 fp32: 15 us cold; through the
+// ring, whose steps cost a barrier, 18).  Dynamic shared memory: G Moments.
 template <typename T, int V>
-__global__ void __launch_bounds__(256, 4) gn_stats_kernel(const GnParams p) {
+__global__ void __launch_bounds__(256, 3) gn_stats_kernel(const GnParams p) {
   constexpr int P = Unit<T, V>::P, U = 8;  // U: positions in a batch
-  extern __shared__ __align__(128) uint8_t smem[];
-  Moments* group = reinterpret_cast<Moments*>(smem + kGnRingBytes);  // [G]
-  __shared__ __align__(8) uint64_t bars[12];
+  extern __shared__ __align__(16) uint8_t smem[];
+  Moments* group = reinterpret_cast<Moments*>(smem);  // [G]
   __shared__ float each[2][256][V + 1];
   __shared__ float counts[256];
   const int tid = threadIdx.x, n = blockIdx.x / p.splits, part = blockIdx.x % p.splits, cv = p.C / V;
   int l0, l1;
   gn_rows(p.L, p.rows, part, l0, l1);
   for (int g = tid; g < p.G; g += 256) group[g] = Moments{0.f, 0.f, 0.f};
-  const T* x = static_cast<const T*>(p.x) + (static_cast<size_t>(n) * p.L + l0) * p.C;
+  const T* x = static_cast<const T*>(p.x) + static_cast<size_t>(n) * p.L * p.C;
   launch_next();
-  GnRing<1> ring;
-  ring.init(smem, bars, p.limit_ns);
   for (int u0 = 0; u0 < cv; u0 += 256) {
-    const int width = min(cv - u0, 256), slots = cv > 256 ? 1 : 256 / width;
-    // a batch's sums relative to its first value, joined to the mean and squares so far
-    float cnt = 0.f, have = 0.f;
-    f2 mean[P], m2[P], at[P], s[P], q[P];
+    const int width = min(cv - u0, 256), slots = cv > 256 ? 1 : 256 / width, slot = tid / width;
+    float cnt = 0.f;
+    f2 mean[P], m2[P];
 #pragma unroll
-    for (int e = 0; e < P; ++e) mean[e] = m2[e] = at[e] = s[e] = q[e] = both(0.f);
-    auto close = [&]() {
-      if (have == 0.f) return;
-      const float f = __fdividef(have, cnt + have), inv = __frcp_rn(have), cf = cnt * f;
+    for (int e = 0; e < P; ++e) mean[e] = m2[e] = both(0.f);
+    // `have` units from l: their sums relative to the first, joined to the mean and squares so far
+    auto batch = [&](int l, int have, bool all) {
+      using Raw = std::conditional_t<V == 1, T, uint4>;
+      const T* at = x + static_cast<size_t>(l) * p.C + (u0 + tid % width) * V;
+      const size_t step = static_cast<size_t>(slots) * p.C;
+      Raw raw[U];
+#pragma unroll
+      for (int i = 0; i < U; ++i)
+        if (all || i < have) raw[i] = __ldg(reinterpret_cast<const Raw*>(at + i * step));
+      auto unit = [&](int i) {
+        if constexpr (V == 1) {
+          Unit<T, V> r;
+          r.v[0] = pair(to_f<T>(raw[i]), 0.f);
+          return r;
+        } else {
+          return unit_of<T, V>(raw[i]);
+        }
+      };
+      const Unit<T, V> first = unit(0);
+      f2 s[P], q[P];
+#pragma unroll
+      for (int e = 0; e < P; ++e) s[e] = q[e] = both(0.f);
+#pragma unroll
+      for (int i = 1; i < U; ++i)
+        if (all || i < have) {
+          const Unit<T, V> y = unit(i);
+#pragma unroll
+          for (int e = 0; e < P; ++e) {
+            const f2 d = fma2(first.v[e], both(-1.f), y.v[e]);
+            s[e] = add2(s[e], d);
+            q[e] = fma2(d, d, q[e]);
+          }
+        }
+      const float h = static_cast<float>(have), inv = __fdividef(1.f, h), f = __fdividef(h, cnt + h), cf = cnt * f;
 #pragma unroll
       for (int e = 0; e < P; ++e) {
-        const f2 d0 = mul2(s[e], both(inv));  // batch mean - at
+        const f2 d0 = mul2(s[e], both(inv));  // the batch's mean - its first value
         const f2 sq = fma2(mul2(s[e], both(-1.f)), d0, q[e]);
-        const f2 d = fma2(mean[e], both(-1.f), add2(at[e], d0));
+        const f2 d = fma2(mean[e], both(-1.f), add2(first.v[e], d0));
         mean[e] = fma2(d, both(f), mean[e]);
         m2[e] = add2(m2[e], fma2(mul2(d, d), both(cf), sq));
-        s[e] = q[e] = both(0.f);
       }
-      cnt += have;
-      have = 0.f;
+      cnt += h;
     };
-    const T* src[1] = {x + u0 * V};
-    ring.template walk<T, V>(src, l1 - l0, p.C, width, slots, [&](int, Unit<T, V>(&in)[1], bool ok) {
-      if (!ok) return;
-      if (have == 0.f) {
-#pragma unroll
-        for (int e = 0; e < P; ++e) at[e] = in[0].v[e];
-      }
-#pragma unroll
-      for (int e = 0; e < P; ++e) {
-        const f2 d = fma2(at[e], both(-1.f), in[0].v[e]);
-        s[e] = add2(s[e], d);
-        q[e] = fma2(d, d, q[e]);
-      }
-      have += 1.f;
-      if (have == static_cast<float>(U)) close();
-    });
-    close();
+    if (slot < slots) {
+      int l = l0 + slot;
+      for (; l + (U - 1) * slots < l1; l += U * slots) batch(l, U, true);
+      if (l < l1) batch(l, (l1 - l - 1) / slots + 1, false);
+    }
     __syncthreads();
     counts[tid] = cnt;
 #pragma unroll

@@ -163,8 +163,8 @@ ttt_la_status ttt_la_group_norm(const ttt_la_group_norm_args* a, void* stream) {
       }
     const long long sums = static_cast<long long>(a->N) * pl.splits, parts = static_cast<long long>(a->N) * pl.parts;
     if (parts >= (1ll << 31) || sums >= (1ll << 31)) return TTT_LA_ERR_UNSUPPORTED;
-    const int sm = kGnRing + a->G * static_cast<int>(sizeof(ttt::Moments));
-    if (!gn_grant(ttt::gn_stats_kernel<T, V>, sm)) return TTT_LA_ERR_CUDA;
+    const int sm = a->G * static_cast<int>(sizeof(ttt::Moments));
+    if (sm > 28 * 1024 && !gn_grant(ttt::gn_stats_kernel<T, V>, sm)) return TTT_LA_ERR_CUDA;
     ttt_la_status r = launch_kernel(ttt::gn_stats_kernel<T, V>, static_cast<int>(sums), 256, sm, st, false, p);
     if (r != TTT_LA_OK) return r;
     if (pl.splits > 1) {
