@@ -132,19 +132,22 @@ def forward_decay_norm(q, k, v, log_decay, gate=None, weight=None, bias=None, ac
                        **kw):
     """The layer and its output norm: forward_decay, then every head's output
     of a token normalised by itself and gated (group_norm with one group a
-    head).  gate [B,T,H*d_v] or None; weight, bias [H*d_v] or None.  Keyword
-    arguments as forward_decay.  Returns (y [B,T,H*d_v], W_T)."""
+    head).  gate [B,T,H*d_v] or None, in any memory order (one that is not
+    contiguous, or starts off 16 bytes, is copied); weight, bias [H*d_v] or
+    None.  Keyword arguments as forward_decay.  Returns (y [B,T,H*d_v], W_T)."""
     B, H, T, dv = v.shape
     if gate is not None and tuple(gate.shape) != (B, T, H * dv):
         raise ValueError("gate: [B,T,H*d_v]")
     if kw.pop("out", None) is not None:
         raise ValueError("forward_decay_norm allocates its output")
-    with on_stream(v.device, stream):
+    rows = (B * T, 1, H * dv)
+    with on_stream(v.device, stream):  # all of the call: a copy made here is read, and its memory used again, there
+        if gate is not None:
+            gate = gate.contiguous()
+            gate = (gate.clone() if gate.data_ptr() % 16 else gate).view(rows)
         o = torch.empty(B, T, H, dv, device=v.device, dtype=v.dtype)
         if kw.get("cu_seqlens") is not None:
             o.zero_()  # rows in no sequence: the norm reads them
-    _, W = forward_decay(q, k, v, log_decay, out=o.transpose(1, 2), stream=stream, **kw)
-    rows = (B * T, 1, H * dv)
-    y, _, _ = group_norm(o.view(rows), H, weight, bias, gate=None if gate is None else gate.reshape(rows),
-                         activation=activation, eps=eps, stream=stream)
+        _, W = forward_decay(q, k, v, log_decay, out=o.transpose(1, 2), stream=stream, **kw)
+        y, _, _ = group_norm(o.view(rows), H, weight, bias, gate=gate, activation=activation, eps=eps, stream=stream)
     return y.view(B, T, H * dv), W

@@ -390,6 +390,32 @@ def test_layer_then_norm(packed):
     assert torch.equal(y.view(x.shape), y2) and torch.equal(W, W2)
 
 
+@pytest.mark.parametrize("layout", ["contiguous", "tokens outermost", "slice", "off 16 bytes"])
+def test_layer_then_norm_on_a_stream(layout):
+    """On a stream of the caller's, with a gate that this stream is still
+    producing when the call is made, in any memory order: the two calls."""
+    c = _make([95, 95], 3, 64, 64, "bf16", False, "tokens", True, seed=41)
+    B, H, T, dv = c["v"].shape
+    C = H * dv
+    values = torch.randn(B, T, C, generator=torch.Generator().manual_seed(2)).to(torch.bfloat16).cuda()
+    gate = {"contiguous": lambda: torch.empty(B, T, C, dtype=torch.bfloat16, device="cuda"),
+            "tokens outermost": lambda: torch.empty(T, B, C, dtype=torch.bfloat16, device="cuda").transpose(0, 1),
+            "slice": lambda: torch.empty(B, T, 3 * C, dtype=torch.bfloat16, device="cuda")[..., C:2 * C],
+            "off 16 bytes": lambda: torch.empty(B * T * C + 1, dtype=torch.bfloat16, device="cuda")[1:].view(B, T, C)}[layout]()
+    gate.fill_(float("nan"))
+    o, W = ttt.forward_decay(c["q"], c["k"], c["v"], c["ld"], state_in=c["W0"])
+    want, _, _ = ttt.group_norm(o.transpose(1, 2).reshape(B * T, 1, C), H, gate=values.view(B * T, 1, C))
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(50_000_000)  # some 25 ms
+        gate.copy_(values)
+    y, W2 = ttt.forward_decay_norm(c["q"], c["k"], c["v"], c["ld"], gate=gate, state_in=c["W0"], stream=s)
+    after = [torch.full((B, T, C), float("nan"), dtype=torch.bfloat16, device="cuda") for _ in range(4)]  # memory let go of
+    torch.cuda.synchronize()
+    assert torch.equal(y.view(want.shape), want) and torch.equal(W2, W) and len(after) == 4
+
+
 def test_past_2_31_elements():
     """q, k, v of 257 heads x 65536 tokens x 128 (2^31 elements and more):
     the last head against the oracle."""
