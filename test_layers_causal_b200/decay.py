@@ -19,7 +19,7 @@ import torch
 
 from . import _abi
 from ._call import FORMATS, check, check_distinct_rows, check_rows, launch_on, on_stream, run, run_with_workspace
-from .norm import group_norm
+from .norm import check_group_norm, group_norm
 
 _FORWARD = FORMATS["ttt_la_decay_args"].pack
 _BACKWARD = FORMATS["ttt_la_decay_grad_args"].pack
@@ -134,7 +134,9 @@ def forward_decay_norm(q, k, v, log_decay, gate=None, weight=None, bias=None, ac
     of a token normalised by itself and gated (group_norm with one group a
     head).  gate [B,T,H*d_v] or None, in any memory order (one that is not
     contiguous, or starts off 16 bytes, is copied); weight, bias [H*d_v] or
-    None.  Keyword arguments as forward_decay.  Returns (y [B,T,H*d_v], W_T)."""
+    None.  Keyword arguments as forward_decay.  Returns (y [B,T,H*d_v], W_T),
+    y empty where there are no rows.  What either operator refuses is refused
+    before the layer runs."""
     B, H, T, dv = v.shape
     if gate is not None and tuple(gate.shape) != (B, T, H * dv):
         raise ValueError("gate: [B,T,H*d_v]")
@@ -146,8 +148,12 @@ def forward_decay_norm(q, k, v, log_decay, gate=None, weight=None, bias=None, ac
             gate = gate.contiguous()
             gate = (gate.clone() if gate.data_ptr() % 16 else gate).view(rows)
         o = torch.empty(B, T, H, dv, device=v.device, dtype=v.dtype)
+        x, y = o.view(rows), torch.empty(rows, device=v.device, dtype=v.dtype)
+        # before the layer, which may update its state in place
+        check_group_norm(x, H, weight, bias, gate, activation, eps)
         if kw.get("cu_seqlens") is not None:
             o.zero_()  # rows in no sequence: the norm reads them
         _, W = forward_decay(q, k, v, log_decay, out=o.transpose(1, 2), stream=stream, **kw)
-        y, _, _ = group_norm(o.view(rows), H, weight, bias, gate=gate, activation=activation, eps=eps, stream=stream)
+        if B * T > 0:
+            group_norm(x, H, weight, bias, gate=gate, activation=activation, eps=eps, out=y, stream=stream)
     return y.view(B, T, H * dv), W

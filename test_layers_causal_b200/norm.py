@@ -12,13 +12,13 @@ _BACKWARD = FORMATS["ttt_la_group_norm_grad_args"].pack
 _ACTIVATIONS = {None: 0, "none": 0, "silu": 1}
 
 
-def _describe(x, num_groups, weight, bias, gate, activation):
+def _describe(x, num_groups, weight, bias, gate, activation, empty=False):
     if x.dim() < 2:
         raise ValueError("x: [N, ..., C], channels last")
     if activation not in _ACTIVATIONS:
         raise ValueError(f"activation: one of {sorted(map(str, _ACTIVATIONS))}")
     N, C = x.shape[0], x.shape[-1]
-    if N < 1 or C < 1 or x.numel() == 0:
+    if C < 1 or (x.numel() == 0 and not empty):
         raise ValueError("x is empty")
     G = int(num_groups)
     if G < 1 or C % G:
@@ -30,8 +30,18 @@ def _describe(x, num_groups, weight, bias, gate, activation):
         raise TypeError("weight and bias: fp32 or the dtype of x")
     pointers = (check(x, "x", dt, dev), check(gate, "gate", dt, dev, x.shape),
                 check(weight, "weight", pdt, dev, (C,)), check(bias, "bias", pdt, dev, (C,)))
-    return N, x.numel() // (N * C), C, G, _abi._dtype_code(x), _abi.BF16 if pdt == torch.bfloat16 else _abi.F32, \
+    return N, x.numel() // max(N * C, 1), C, G, _abi._dtype_code(x), _abi.BF16 if pdt == torch.bfloat16 else _abi.F32, \
         _ACTIVATIONS[activation], pointers, pdt
+
+
+def check_group_norm(x, num_groups, weight, bias, gate, activation, eps):
+    """Refuses what group_norm refuses, without a launch, for callers whose own
+    work comes before the norm; x may hold no rows."""
+    G = _describe(x, num_groups, weight, bias, gate, activation, empty=True)[3]
+    if not eps >= 0:
+        raise _abi.TttError("ttt_la_group_norm", _abi.ERR_INVALID_ARG)
+    if G > 4096:
+        raise _abi.TttError("ttt_la_group_norm", _abi.ERR_UNSUPPORTED)
 
 
 def group_norm(x, num_groups, weight=None, bias=None, gate=None, activation="silu", eps=1e-5, out=None,

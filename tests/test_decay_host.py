@@ -238,3 +238,19 @@ def test_workspace_grows_with_the_segments(abi, packed):
     assert a // state >= (1000 // 64 + 7 if packed else 2 * 16)
     back = abi.lib().ttt_la_backward_decay_workspace_size(ctypes.byref(_bwd(abi, segment_tokens=64, **base)))
     assert back >= 2 * a
+
+
+def test_norm_checks_come_before_the_layer():
+    """forward_decay_norm refuses what its norm would refuse while nothing has
+    been launched; no rows are no reason."""
+    from test_layers_causal_b200 import _abi
+    from test_layers_causal_b200.norm import _describe, check_group_norm
+    x = torch.zeros(5, 1, 64)
+    for G, act, eps, error in ((3, "silu", 1e-5, ValueError), (4, "relu", 1e-5, ValueError)):
+        with pytest.raises(error):
+            check_group_norm(x, G, None, None, None, act, eps)
+    with pytest.raises(ValueError, match="empty"):
+        _describe(x[:0], 4, None, None, None, None)
+    with pytest.raises(ValueError, match="CUDA"):  # the rows' number passes, their device does not
+        check_group_norm(x[:0], 4, None, None, None, None, 1e-5)
+    assert issubclass(_abi.TttError, RuntimeError)

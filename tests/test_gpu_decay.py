@@ -416,6 +416,33 @@ def test_layer_then_norm_on_a_stream(layout):
     assert torch.equal(y.view(want.shape), want) and torch.equal(W2, W) and len(after) == 4
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_layer_then_norm_of_no_rows(dtype):
+    """Only empty sequences: an empty output, the state as it was."""
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    z = torch.empty(1, 2, 0, 64, dtype=dt, device="cuda")
+    cu = torch.zeros(4, dtype=torch.int32, device="cuda")
+    S = torch.randn(3, 2, 64, 64, generator=torch.Generator().manual_seed(1)).cuda()
+    W0 = S.clone()
+    y, W = ttt.forward_decay_norm(z, z, z, _log_decay(2).cuda(), gate=torch.empty(1, 0, 128, dtype=dt, device="cuda"),
+                                  cu_seqlens=cu, state_in=S, state_out=S)
+    assert y.shape == (1, 0, 128) and y.dtype == dt and W is S and torch.equal(S, W0)
+
+
+@pytest.mark.parametrize("bad", ["activation", "eps", "eps nan", "weight", "weight dtype", "gate dtype", "gate device"])
+def test_layer_then_norm_refuses_before_the_state_moves(bad):
+    c = _make([70], 2, 64, 64, "bf16", False, "tokens", True, seed=42)
+    gate = torch.zeros(1, 70, 128, dtype=torch.bfloat16, device="cuda")
+    kw = {"activation": dict(activation="relu"), "eps": dict(eps=-1e-5), "eps nan": dict(eps=float("nan")),
+          "weight": dict(weight=torch.ones(64, device="cuda")), "weight dtype": dict(weight=torch.ones(128, device="cuda").half()),
+          "gate dtype": dict(gate=gate.float()), "gate device": dict(gate=gate.cpu())}[bad]
+    S = c["W0"].clone()
+    with pytest.raises((ValueError, TypeError, ttt.TttError)):
+        ttt.forward_decay_norm(c["q"], c["k"], c["v"], c["ld"], state_in=S, state_out=S, **kw)
+    torch.cuda.synchronize()
+    assert torch.equal(S, c["W0"])
+
+
 def test_past_2_31_elements():
     """q, k, v of 257 heads x 65536 tokens x 128 (2^31 elements and more):
     the last head against the oracle."""
