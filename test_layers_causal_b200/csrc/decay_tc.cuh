@@ -515,6 +515,13 @@ __global__ void __launch_bounds__(576, 1) decay_tc_total_kernel(const __grid_con
 // barrier, something that every waiter does after its wait.  Scores and P,
 // which run a tile ahead, have two.
 //
+// The kernel starts before the launch before it has ended, and only the state
+// warps need that launch's results. The limit of a wait is to measure this
+// block's own pipeline, so each role calls wait_before (which has no limit)
+// ahead of its first wait that the state warps have a part in; what comes
+// earlier, the first loads and the scores and P of a whole first tile, overlaps
+// that launch.
+//
 // Shared memory is the bound before HBM: an MMA reads both operands of 128
 // bytes a clock, so a tile of 128 x 128 x 128 moves about 600 KB through it, of
 // which P in tensor memory saves 64; a tile took 5700 cycles with one part of
@@ -615,7 +622,10 @@ __global__ void __launch_bounds__(608, 1) decay_tc_out_kernel(const __grid_const
         const int st = i % NST, y = sp.row0 + tile_at(i);
         uint8_t* d = smem + st * STAGE;
         if (i >= NST) decay_wait(dead, &free_qk[st], (i / NST - 1) & 1, lim);
-        if (i == NST - 1) decay_wait(dead, sread, 0, lim);
+        if (i == NST - 1) {
+          wait_before();
+          decay_wait(dead, sread, 0, lim);
+        }
         if (dead) break;
         mbar_arrive_expect_tx(&full[st], 2 * TK);
 #pragma unroll
@@ -656,7 +666,9 @@ __global__ void __launch_bounds__(608, 1) decay_tc_out_kernel(const __grid_const
         tc_commit(&sfull[i & 1]);
       };
       decay_wait(dead, &full[0], 0, lim);
+      if (ragged(0)) wait_before();
       scores(0);
+      wait_before();
       for (int i = 0; i < nt; ++i) {
         const uint32_t base = sbase + (i % NST) * STAGE, par = i & 1;
         const uint64_t dq = sdesc_sw128(base, 16, 1024), dvm = sdesc_sw128(base + 2 * TK, C * 128, 1024);
@@ -699,6 +711,7 @@ __global__ void __launch_bounds__(608, 1) decay_tc_out_kernel(const __grid_const
     if (lane == 0) {
       bool dead = false;
       constexpr uint32_t ID_D = idesc_bf16_f32(DV, DK, true, true);
+      wait_before();
       for (int i = 0; i < nt; ++i) {
         if (i + 1 < nt) {
           const uint32_t base = sbase + (i % NST) * STAGE;
@@ -829,8 +842,10 @@ __global__ void __launch_bounds__(608, 1) decay_tc_out_kernel(const __grid_const
         mbar_arrive(&empty[i % NST]);
       }
     };
+    if (sp.len - tile_at(0) < C) wait_before();
     if (NSB == 2) {
       scores_to_p(0);
+      wait_before();
       for (int i = 0; i < nt; ++i) {
         if (i + 1 < nt) scores_to_p(i + 1);
         output(i);
@@ -838,6 +853,7 @@ __global__ void __launch_bounds__(608, 1) decay_tc_out_kernel(const __grid_const
     } else {
       for (int i = 0; i < nt; ++i) {
         scores_to_p(i);
+        if (i == 0) wait_before();
         output(i);
       }
     }

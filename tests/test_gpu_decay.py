@@ -443,6 +443,26 @@ def test_layer_then_norm_refuses_before_the_state_moves(bad):
     assert torch.equal(S, c["W0"])
 
 
+def test_a_wait_limit_covers_one_block_not_the_launches_before():
+    """One block's 1024 tiles, some 4 ms, under a limit of 1 ms for each wait:
+    launches that start early do not count that run against their waits."""
+    T = 131072
+    c = _make([T], 1, 64, 128, "bf16", False, "heads", True, seed=44)
+    kw = dict(state_in=c["W0"], segment_tokens=T)
+    both = lambda: [*ttt.forward_decay(c["q"], c["k"], c["v"], c["ld"], **kw),  # noqa: E731
+                    *ttt.backward_decay(c["q"], c["k"], c["v"], c["dO"], c["ld"], grad_state=c["dW"], **kw).values()]
+    want = both()
+    torch.cuda.synchronize()
+    ttt.set_wait_limit_ns(1_000_000)
+    try:
+        got = both()
+        torch.cuda.synchronize()
+    finally:
+        ttt.set_wait_limit_ns(1_000_000_000)
+    assert ttt.device_status() == 0
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
 def test_past_2_31_elements():
     """q, k, v of 257 heads x 65536 tokens x 128 (2^31 elements and more):
     the last head against the oracle."""
