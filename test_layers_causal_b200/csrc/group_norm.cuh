@@ -423,6 +423,7 @@ __global__ void __launch_bounds__(256) gn_param_grad_kernel(const float* __restr
 // ------------------------------------------------------ any L and width ----
 // A thread keeps one unit of channels (whose channels may lie in two groups)
 // and walks positions: rows [k rows, (k + 1) rows) of a sample are part k.
+// (L may be 2^31 - 1: a position with a step past the last one is unsigned.)
 __device__ __forceinline__ void gn_rows(int L, int rows, int k, int& l0, int& l1) {
   l0 = static_cast<int>(min(static_cast<long long>(L), static_cast<long long>(k) * rows));
   l1 = static_cast<int>(min(static_cast<long long>(L), static_cast<long long>(l0) + rows));
@@ -452,7 +453,7 @@ __global__ void __launch_bounds__(256, 3) gn_stats_kernel(const GnParams p) {
 #pragma unroll
     for (int e = 0; e < P; ++e) mean[e] = m2[e] = both(0.f);
     // `have` units from l: their sums relative to the first, joined to the mean and squares so far
-    auto batch = [&](int l, int have, bool all) {
+    auto batch = [&](unsigned l, int have, bool all) {
       using Raw = std::conditional_t<V == 1, T, uint4>;
       const T* at = x + static_cast<size_t>(l) * p.C + (u0 + tid % width) * V;
       const size_t step = static_cast<size_t>(slots) * p.C;
@@ -496,9 +497,10 @@ __global__ void __launch_bounds__(256, 3) gn_stats_kernel(const GnParams p) {
       cnt += h;
     };
     if (slot < slots) {
-      int l = l0 + slot;
-      for (; l + (U - 1) * slots < l1; l += U * slots) batch(l, U, true);
-      if (l < l1) batch(l, (l1 - l - 1) / slots + 1, false);
+      unsigned l = static_cast<unsigned>(l0) + slot;
+      const unsigned end = l1;
+      for (; l + (U - 1) * slots < end; l += U * slots) batch(l, U, true);
+      if (l < end) batch(l, (end - l - 1) / slots + 1, false);
     }
     __syncthreads();
     counts[tid] = cnt;
@@ -601,7 +603,7 @@ __global__ void __launch_bounds__(256) gn_apply_kernel(const GnParams p) {
       par.w[e] = mul2(par.w[e], rstd.v[e]);
     }
 #pragma unroll 4
-    for (int l = l0 + slot; l < l1; l += slots) {
+    for (unsigned l = static_cast<unsigned>(l0) + slot; l < static_cast<unsigned>(l1); l += slots) {
       const size_t at = base + static_cast<size_t>(l) * p.C + c;
       const Unit<T, V> x = ld_unit<T, V>(static_cast<const T*>(p.x) + at);
       Unit<T, V> z = x, y;

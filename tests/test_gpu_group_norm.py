@@ -239,3 +239,37 @@ def test_past_2_31_elements():
     ry, rm, _ = oracle.group_norm_f64(f64(last), 16)
     assert (np.abs(f64(y[-1:]) - ry) <= U * np.abs(ry) + 1e-5).all()
     assert np.abs(f64(mean[-1:]) - rm).max() <= 1e-5 and not y[:-1].any()
+
+
+def test_the_most_positions():
+    """2^31 - 1 positions of one channel, all zero but the last: positions plus
+    a step pass 31 bits.  The sums over the zeros are known."""
+    L, n = (1 << 31) - 1, 3000
+    g = torch.Generator().manual_seed(6)
+    tail, dtail = (torch.randn(n, generator=g).to(torch.bfloat16) for _ in range(2))
+    x = torch.zeros(1, L, 1, dtype=torch.bfloat16, device="cuda")
+    x[0, L - n:, 0] = tail.cuda()
+    y, mean, rstd = ttt.group_norm(x, 1, activation=None)
+    X, D = f64(tail), f64(dtail)
+    m = X.sum() / L
+    r = ((X * X).sum() / L - m * m + 1e-5) ** -0.5
+    top = np.abs(X).max()
+    assert abs(f64(mean)[0, 0] - m) <= 64 * E * top
+    assert abs(f64(rstd)[0, 0] - r) <= 128 * E * r * (1 + top * r)
+    M, R = f64(mean)[0, 0], f64(rstd)[0, 0]
+    hat = (X - M) * R
+    tol = 64 * E * (3 * np.abs(hat) + abs(M) * R + 1) + U * np.abs(hat)
+    assert (np.abs(f64(y[0, L - n:, 0]) - hat) <= tol).all()
+    zero = y[0, 0, 0]  # what a zero becomes
+    assert abs(float(zero) + M * R) <= 64 * E + U * abs(M) * R
+    assert (y[0, :L - n, 0] == zero).all()
+    del y
+    dy = torch.zeros_like(x)
+    dy[0, L - n:, 0] = dtail.cuda()
+    dx = ttt.group_norm_backward(dy, x, 1, mean, rstd, activation=None)["dx"]
+    s1, s2 = D.sum() / L, (D * hat).sum() / L
+    a1, a2 = np.abs(D).sum() / L, (np.abs(D) * (np.abs(hat) + 1)).sum() / L
+    want = R * (D - s1 - hat * s2)
+    tol = R * (64 * E * (np.abs(D) + a1 + (np.abs(hat) + 1) * a2 * 3)) + U * np.abs(want)
+    assert (np.abs(f64(dx[0, L - n:, 0]) - want) <= tol).all()
+    assert (dx[0, :L - n, 0] == dx[0, 0, 0]).all()
