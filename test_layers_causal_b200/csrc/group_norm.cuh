@@ -134,19 +134,22 @@ __device__ __forceinline__ f2 gn_grad(f2 g, f2 t, f2 z, f2& dz) {
   return mul2(g, fma2(mul2(t, s), fma2(s, both(-1.f), both(1.f)), s));
 }
 
-// Count, mean and sum of squares around it; joined exactly.
+// Count, mean and variance; joined exactly.  The variance instead of the sum of
+// squares, and the means' distance weighted before it is squared: neither
+// passes the largest number before the variance itself does.  (With nothing on
+// one side that distance is the other's mean.)
 struct Moments {
-  float n, mean, m2;
+  float n, mean, var;
 };
 __device__ __forceinline__ Moments join(const Moments& a, const Moments& b) {
   const float n = a.n + b.n;
   if (n == 0.f) return a;
   const float f = __fdividef(b.n, n), d = b.mean - a.mean;  // (counts: far from the division's limits)
-  return Moments{n, fmaf(d, f, a.mean), a.m2 + b.m2 + d * d * a.n * f};
+  return Moments{n, fmaf(d, f, a.mean), fmaf(f, b.var - a.var, a.var) + d * (f * __fdividef(a.n, n)) * d};
 }
 __device__ __forceinline__ Moments shfl_xor(const Moments& a, int off) {
   return Moments{__shfl_xor_sync(0xffffffffu, a.n, off), __shfl_xor_sync(0xffffffffu, a.mean, off),
-                 __shfl_xor_sync(0xffffffffu, a.m2, off)};
+                 __shfl_xor_sync(0xffffffffu, a.var, off)};
 }
 
 // Walks rows of C values in memory, `slots` rows at a time, a thread one unit of
@@ -429,7 +432,7 @@ __device__ __forceinline__ void gn_rows(int L, int rows, int k, int& l0, int& l1
   l1 = static_cast<int>(min(static_cast<long long>(L), static_cast<long long>(l0) + rows));
 }
 
-// Statistics of one split of one sample: part[N][splits][G] of (mean, m2), or,
+// Statistics of one split of one sample: part[N][splits][G] of (mean, variance), or,
 // where a sample is one split, mean and rstd.  Plain loads, a batch of eight
 // positions in flight a thread (6 x 4225 x 320 fp32: 15 us cold; through the
 // ring, whose steps cost a barrier, 18).  Dynamic shared memory: G Moments.
@@ -449,10 +452,10 @@ __global__ void __launch_bounds__(256, 3) gn_stats_kernel(const GnParams p) {
   for (int u0 = 0; u0 < cv; u0 += 256) {
     const int width = min(cv - u0, 256), slots = cv > 256 ? 1 : 256 / width, slot = tid / width;
     float cnt = 0.f;
-    f2 mean[P], m2[P];
+    f2 mean[P], var[P];
 #pragma unroll
-    for (int e = 0; e < P; ++e) mean[e] = m2[e] = both(0.f);
-    // `have` units from l: their sums relative to the first, joined to the mean and squares so far
+    for (int e = 0; e < P; ++e) mean[e] = var[e] = both(0.f);
+    // `have` units from l: their sums relative to the first, joined to the mean and variance so far
     auto batch = [&](unsigned l, int have, bool all) {
       using Raw = std::conditional_t<V == 1, T, uint4>;
       const T* at = x + static_cast<size_t>(l) * p.C + (u0 + tid % width) * V;
@@ -485,14 +488,15 @@ __global__ void __launch_bounds__(256, 3) gn_stats_kernel(const GnParams p) {
             q[e] = fma2(d, d, q[e]);
           }
         }
-      const float h = static_cast<float>(have), inv = __fdividef(1.f, h), f = __fdividef(h, cnt + h), cf = cnt * f;
+      const float h = static_cast<float>(have), inv = __fdividef(1.f, h), f = __fdividef(h, cnt + h);
+      const float cf = f * __fdividef(cnt, cnt + h);
 #pragma unroll
       for (int e = 0; e < P; ++e) {
         const f2 d0 = mul2(s[e], both(inv));  // the batch's mean - its first value
-        const f2 sq = fma2(mul2(s[e], both(-1.f)), d0, q[e]);
+        const f2 more = fma2(fma2(mul2(s[e], both(-1.f)), d0, q[e]), both(inv), mul2(var[e], both(-1.f)));
         const f2 d = fma2(mean[e], both(-1.f), add2(first.v[e], d0));
         mean[e] = fma2(d, both(f), mean[e]);
-        m2[e] = add2(m2[e], fma2(mul2(d, d), both(cf), sq));
+        var[e] = add2(fma2(more, both(f), var[e]), mul2(mul2(d, both(cf)), d));
       }
       cnt += h;
     };
@@ -507,7 +511,7 @@ __global__ void __launch_bounds__(256, 3) gn_stats_kernel(const GnParams p) {
 #pragma unroll
     for (int e = 0; e < V; ++e) {
       each[0][tid][e] = e & 1 ? hi_of(mean[e / 2]) : lo_of(mean[e / 2]);
-      each[1][tid][e] = e & 1 ? hi_of(m2[e / 2]) : lo_of(m2[e / 2]);
+      each[1][tid][e] = e & 1 ? hi_of(var[e / 2]) : lo_of(var[e / 2]);
     }
     __syncthreads();
     // a warp for each group that these channels touch
@@ -529,10 +533,10 @@ __global__ void __launch_bounds__(256, 3) gn_stats_kernel(const GnParams p) {
     if (p.splits == 1) {
       const size_t at = static_cast<size_t>(n) * p.G + g;
       p.mean[at] = group[g].mean;
-      p.rstd[at] = rsqrtf(group[g].m2 / group[g].n + p.eps);
+      p.rstd[at] = rsqrtf(group[g].var + p.eps);
     } else {
       float2* d = reinterpret_cast<float2*>(p.part) + (static_cast<size_t>(n) * p.splits + part) * p.G + g;
-      *d = make_float2(group[g].mean, group[g].m2);
+      *d = make_float2(group[g].mean, group[g].var);
     }
   }
 }
@@ -563,7 +567,7 @@ __global__ void __launch_bounds__(256) gn_join_kernel(const GnParams p) {
   for (int off = 16; off > 0; off >>= 1) m = join(m, shfl_xor(m, off));
   if ((threadIdx.x & 31) == 0) {
     p.mean[i] = m.mean;
-    p.rstd[i] = rsqrtf(m.m2 / m.n + p.eps);
+    p.rstd[i] = rsqrtf(m.var + p.eps);
   }
 }
 

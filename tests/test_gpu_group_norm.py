@@ -273,3 +273,22 @@ def test_the_most_positions():
     tol = R * (64 * E * (np.abs(D) + a1 + (np.abs(hat) + 1) * a2 * 3)) + U * np.abs(want)
     assert (np.abs(f64(dx[0, L - n:, 0]) - want) <= tol).all()
     assert (dx[0, :L - n, 0] == dx[0, 0, 0]).all()
+
+
+@pytest.mark.parametrize("shape,G,dtype", [((2, 300, 64), 4, "f32"), ((3, 70, 48), 16, "bf16"), ((2, 9, 10), 2, "f32"),
+                                           ((5, 1, 96), 2, "bf16"), ((5, 1, 256), 2, "f32"), ((2, 3000, 320), 32, "f32")])
+def test_values_whose_square_is_too_large(shape, G, dtype):
+    """Values around 2^66 with a spread of 2^60: the square of the mean passes
+    the largest fp32 number, the variance does not.  Against the oracle, with
+    the bounds of test_forward_matches_oracle."""
+    g = torch.Generator().manual_seed(8)
+    x = (torch.randn(shape, generator=g).double() * 2.0 ** 60 + 2.0 ** 66).to(torch.bfloat16 if dtype == "bf16" else torch.float32).cuda()
+    y, mean, rstd = ttt.group_norm(x, G, activation=None)
+    X = f64(x)
+    ry, rm, rr = oracle.group_norm_f64(X, G, silu=False)
+    top = np.abs(X).reshape(shape[0], -1, G, shape[-1] // G).max(axis=(1, 3))
+    assert (np.abs(f64(mean) - rm) <= 64 * E * top).all()
+    assert (np.abs(f64(rstd) - rr) <= 128 * E * rr * (1 + top * rr)).all()
+    hat = (X - _spread(rm, G, shape)) * _spread(rr, G, shape)
+    tol = 64 * E * (np.abs(hat) * 4 + _spread(np.abs(rm) * rr, G, shape) + 1) + (U * np.abs(ry) if dtype == "bf16" else 0)
+    assert (np.abs(f64(y) - ry) <= tol).all()
