@@ -444,9 +444,11 @@ TTT_LA_API ttt_la_status ttt_la_backward_decay(const ttt_la_decay_grad_args *arg
 
 /* The same layer for one new token of each of N sequences, the state updated
  * IN PLACE: q, k [N,H,d_k], v, o [N,H,d_v] with contiguous features and
- * x_stride[2] elements between sequences and heads (multiples of 16 bytes);
- * state [N,H,d_v,d_k] fp32.  d_k in {32, 64, 128}, any d_v with
- * N H d_v < 2^31 - 2^20; memory-bound. */
+ * x_stride[2] elements between sequences and heads (positive; of q and k
+ * multiples of 16 bytes; not read for a dimension of size 1); q, k, v, o and
+ * state start on 16 bytes; state [N,H,d_v,d_k] fp32.  o must not overlap q, k,
+ * v or itself.  d_k in {32, 64, 128} (a prompt takes more widths than the
+ * step), any d_v with N H d_v < 2^31 - 2^20; memory-bound. */
 typedef struct ttt_la_decay_decode_args {
   int32_t N, H, d_k, d_v;
   int32_t dtype;            /* of q, k, v, o */

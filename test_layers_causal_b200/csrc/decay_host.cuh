@@ -468,8 +468,9 @@ extern "C" ttt_la_status ttt_la_decode_step_decay(const ttt_la_decay_decode_args
   for (int i = 0; i < 4; ++i) {
     if (!t[i] || !aligned16(t[i])) return TTT_LA_ERR_INVALID_ARG;
     const long long size[2] = {a->N, a->H};
+    const int step = i < 2 ? unit : 1;  // q and k are read in 16-byte pieces, v and o one value at a time
     for (int j = 0; j < 2; ++j)
-      if (size[j] > 1 && (stride[i][j] < unit || stride[i][j] % unit || stride[i][j] > (1ll << 36)))
+      if (size[j] > 1 && (stride[i][j] < step || stride[i][j] % step || stride[i][j] > (1ll << 36)))
         return TTT_LA_ERR_INVALID_ARG;
     x[i] = ttt::DecayTensor{t[i], stride[i][0], stride[i][1], 0};
   }

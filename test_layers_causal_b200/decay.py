@@ -103,7 +103,8 @@ def backward_decay(q, k, v, grad_o, log_decay, eta_const=None, ascent=False, cu_
 
 def decode_step_decay(q, k, v, log_decay, state, eta_const=None, ascent=False, out=None, stream=None):
     """One new token of each of N sequences (ttt_la_decode_step_decay): q, k
-    [N,H,d_k], v [N,H,d_v]; state [N,H,d_v,d_k] fp32, updated in place.
+    [N,H,d_k], v [N,H,d_v]; state [N,H,d_v,d_k] fp32, updated in place.  d_k
+    is 32, 64 or 128 (a prompt takes more widths than the step), d_v any.
     Returns o [N,H,d_v]."""
     if q.dim() != 3 or k.shape != q.shape or v.dim() != 3 or v.shape[:2] != q.shape[:2]:
         raise ValueError("q, k: [N,H,d_k]; v: [N,H,d_v]")

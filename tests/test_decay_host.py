@@ -254,3 +254,17 @@ def test_norm_checks_come_before_the_layer():
     with pytest.raises(ValueError, match="CUDA"):  # the rows' number passes, their device does not
         check_group_norm(x[:0], 4, None, None, None, None, 1e-5)
     assert issubclass(_abi.TttError, RuntimeError)
+
+
+@pytest.mark.parametrize("bad", [dict(q_stride=I2(256, 60)), dict(k_stride=I2(252, 128)), dict(v_stride=I2(256, 0)),
+                                 dict(o_stride=I2(-20, 20)), dict(v_stride=I2(1 << 40, 20))], ids=str)
+def test_step_strides_that_are_refused(abi, bad):
+    assert abi.lib().ttt_la_decode_step_decay(ctypes.byref(_step(abi, **bad)), None) == abi.ERR_INVALID_ARG
+
+
+def test_step_takes_values_of_any_width(abi):
+    """Rows of v and o start anywhere. (A width of the keys that is not there
+    is found behind the checks of the strides: nothing is launched.)"""
+    for d_v in (1, 20, 33):
+        block = _step(abi, d_k=96, d_v=d_v, v_stride=I2(2 * d_v, d_v), o_stride=I2(2 * d_v + 3, d_v + 1))
+        assert abi.lib().ttt_la_decode_step_decay(ctypes.byref(block), None) == abi.ERR_UNSUPPORTED

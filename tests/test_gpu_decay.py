@@ -276,6 +276,34 @@ def test_step_matches_oracle(dtype, N, H, dk, dv):
     assert (np.abs(f64(o) - ro[..., 0, :]) <= tol * 1.001).all()
 
 
+@pytest.mark.parametrize("padded", [False, True])
+@pytest.mark.parametrize("dtype,N,H,dk,dv", [("bf16", 300, 7, 64, 72), ("bf16", 1000, 5, 32, 40), ("f32", 300, 7, 64, 20),
+                                             ("bf16", 5, 3, 64, 33), ("bf16", 700, 3, 128, 15), ("f32", 3, 2, 32, 1),
+                                             ("bf16", 1500, 3, 32, 17)])
+def test_step_of_any_value_width(dtype, N, H, dk, dv, padded):
+    """Widths of v that a warp's rows do not divide: its accesses lie in two
+    (sequence, head)s, or behind the last row; v and o with rows that do not
+    start on 16 bytes; the memory around o stays as it is."""
+    g = torch.Generator().manual_seed(N + dv)
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    q, k = (torch.randn(N, H, dk, generator=g).to(dt).cuda() for _ in range(2))
+    pad = 3 if padded else 0
+    v = torch.randn(N, H, dv + pad, generator=g).to(dt).cuda()[..., :dv]
+    room = torch.full((N, H, dv + pad), 7.0, dtype=dt, device="cuda")
+    S = torch.randn(N, H, dv, dk, generator=g).cuda()
+    ld = _log_decay(H).cuda()
+    W0 = f64(S)
+    ro, rW = oracle.decay_forward_f64(*(f64(x)[..., None, :] for x in (q, k, v)), f64(ld), 0.25, W0)
+    Ao, AW = oracle.decay_forward_f64(*(np.abs(f64(x))[..., None, :] for x in (q, k, v)), f64(ld), 0.25, np.abs(W0))
+    S2 = S.clone()
+    o = ttt.decode_step_decay(q, k, v, ld, S, eta_const=0.25)
+    o2 = ttt.decode_step_decay(q, k, v, ld, S2, eta_const=0.25, out=room[..., :dv])
+    assert torch.equal(o, o2) and torch.equal(S, S2) and (room[..., dv:] == 7).all()
+    _check(S, rW, AW, "state", "f32", 1, 1)
+    tol = (dk + 8) * E * Ao[..., 0, :] + (U * np.abs(ro[..., 0, :]) if dtype == "bf16" else 0)
+    assert (np.abs(f64(o) - ro[..., 0, :]) <= tol * 1.001).all()
+
+
 def test_streams_graphs_and_repeats_give_the_same_bits():
     c = _make([700, 700], 3, 128, 128, "bf16", False, "tokens", True, seed=30)
     kw = dict(state_in=c["W0"], segment_tokens=128)
