@@ -376,8 +376,9 @@ TTT_LA_API ttt_la_status ttt_la_backward_chunked(const ttt_la_grad_args *args, v
  * must not overlap.  With cu_seqlens (device int32 [N+1], not decreasing) the
  * sequences are packed: q, k, v, o have T rows in all, sequence n's are rows
  * [cu_seqlens[n], cu_seqlens[n+1]), x_stride[0] is not read, and rows in no
- * sequence are neither read into a result nor written.  Sequences may be
- * empty: their state passes through.  Values of cu_seqlens outside [0, T] are
+ * sequence, those before the first one and behind the last, are not read into
+ * a result, and of o left as they are, or set to zero where clear_rest is 1.
+ * Sequences may be empty: their state passes through.  Values of cu_seqlens outside [0, T] are
  * clamped to it.  log_decay: device fp32 [H], <= 0 (-inf: gamma = 0); it is a
  * constant, without a gradient.  state_in / state_out: fp32 [N,H,d_v,d_k],
  * state_out may be state_in.
@@ -408,6 +409,7 @@ typedef struct ttt_la_decay_args {
   const float *state_in;    /* or NULL -> zeros */
   float *state_out;         /* or NULL -> not returned */
   int32_t segment_tokens;
+  int32_t clear_rest;       /* 0 or 1; of packed sequences */
   void *workspace;
   size_t workspace_bytes;
 } ttt_la_decay_args;

@@ -86,7 +86,7 @@ class TttDecayArgs(ctypes.Structure):
         ("q", _c_vp), ("k", _c_vp), ("v", _c_vp), ("o", _c_vp),
         ("q_stride", _c_i64 * 3), ("k_stride", _c_i64 * 3), ("v_stride", _c_i64 * 3), ("o_stride", _c_i64 * 3),
         ("log_decay", _c_vp), ("cu_seqlens", _c_vp), ("eta_const", _c_f32), ("ascent", _c_i32),
-        ("state_in", _c_vp), ("state_out", _c_vp), ("segment_tokens", _c_i32),
+        ("state_in", _c_vp), ("state_out", _c_vp), ("segment_tokens", _c_i32), ("clear_rest", _c_i32),
         ("workspace", _c_vp), ("workspace_bytes", _c_sz),
     ]
 

@@ -18,7 +18,7 @@ from . import _abi
 
 # Formats of the C structs, without the trailing workspace and workspace_bytes where there are such.
 FORMATS = {
-    "ttt_la_decay_args": struct.Struct("<6i4Q12q2Qfi2Qi4x"),
+    "ttt_la_decay_args": struct.Struct("<6i4Q12q2Qfi2Q2i"),
     "ttt_la_decay_grad_args": struct.Struct("<6i7Q21q2Qfi3Qi4x"),
     "ttt_la_decay_decode_args": struct.Struct("<5i4x4Q8qQfiQ"),
     "ttt_la_group_norm_args": struct.Struct("<7if7Q"),

@@ -62,6 +62,23 @@ __device__ __forceinline__ void decay_rows(const DecayGeom& g, int n, int& a, in
   b = min(max(__ldg(g.cu + n + 1), a), g.T);
 }
 
+// Zeros for the rows of o in no sequence, those before the first one and behind
+// the last; the grid's blocks share them.  Inside the output kernels, so that
+// rows which are there to be written once cost no launch, and none are cleared
+// that the layer writes.
+template <typename T>
+__device__ __forceinline__ void decay_clear_rest(const DecayGeom& g, T* o, long long oh, long long ot, int dv) {
+  constexpr int unit = 16 / sizeof(T);
+  const int a = min(max(__ldg(g.cu), 0), g.T), b = min(max(__ldg(g.cu + g.N), a), g.T);
+  const long long units = dv / unit, per = g.H * units, n = (a + static_cast<long long>(g.T - b)) * per;
+  for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < n;
+       i += static_cast<long long>(gridDim.x) * blockDim.x) {
+    const long long row = i / per, at = i - row * per, h = at / units;
+    *reinterpret_cast<uint4*>(o + h * oh + (row < a ? row : row - a + b) * ot + (at - h * units) * unit) =
+        make_uint4(0u, 0u, 0u, 0u);
+  }
+}
+
 // Segment s counted over all sequences; called by whole warps.
 __device__ __forceinline__ DecaySpan decay_span(const DecayGeom& g, int s) {
   DecaySpan r;
@@ -148,6 +165,7 @@ struct DecayRun {
   int s_in_t;
   float* s_out;            // [N][H][dv][dk] or nullptr
   float* ws;               // [nseg][H][dv][dk]: segments' contributions, then start states; nullptr: one segment each
+  int clear;               // zeros for o's rows in no (packed) sequence
 };
 
 // The state that a segment's block starts from: the caller's where the
@@ -280,6 +298,7 @@ __global__ void __launch_bounds__(256) decay_simt_kernel(const DecayGeom g, cons
 
   const int nvt = (dv + VT - 1) / VT;
   const int vt = blockIdx.x % nvt, h = (blockIdx.x / nvt) % g.H, s = blockIdx.x / nvt / g.H;
+  if (!TOT && p.clear) decay_clear_rest(g, static_cast<T*>(const_cast<void*>(p.o.p)), p.o.sh, p.o.st, dv);
   const DecaySpan sp = decay_span(g, s);
   if (sp.seq < 0) return;
   if (TOT && (sp.nseg <= 1 || sp.j == (p.rev ? 0 : sp.nseg - 1))) return;

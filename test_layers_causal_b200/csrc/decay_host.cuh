@@ -242,6 +242,7 @@ ttt::DecayRun decay_forward_run(const ttt_la_decay_args* a) {
   r.sR = 1.f;
   r.s_in = a->state_in;
   r.s_out = a->state_out;
+  r.clear = a->cu_seqlens && a->clear_rest;
   return r;
 }
 
@@ -292,6 +293,7 @@ ttt_la_status ttt_la_forward_decay(const ttt_la_decay_args* a, void* stream) {
   const ttt_la_status s = check_decay_shape(a->N, a->H, a->T, a->d_k, a->d_v, a->dtype, a->cu_seqlens, a->log_decay,
                                             a->segment_tokens);
   if (s != TTT_LA_OK) return s;
+  if (a->clear_rest != 0 && a->clear_rest != 1) return TTT_LA_ERR_INVALID_ARG;
   const bool packed = a->cu_seqlens != nullptr;
   const void* t[4] = {a->q, a->k, a->v, a->o};
   const int64_t* stride[4] = {a->q_stride, a->k_stride, a->v_stride, a->o_stride};
@@ -316,7 +318,7 @@ ttt_la_status ttt_la_forward_decay(const ttt_la_decay_args* a, void* stream) {
       !decay_map(&m.map[4], r.k, batch, a->H, a->T, a->d_k, ttt::decay_total_tile(a->d_k)) ||
       !decay_map(&m.map[5], r.v, batch, a->H, a->T, a->d_v, ttt::decay_total_tile(a->d_k)))
     return TTT_LA_ERR_CUDA;
-  m.g = l.g, m.log_decay = a->log_decay, m.limit_ns = g_limit_ns;
+  m.g = l.g, m.log_decay = a->log_decay, m.limit_ns = g_limit_ns, m.clear = r.clear;
   ttt::DecayTcRun run = decay_tc_run(0, 1, 2, 3, 4, 5, r);
   run.ws_all = decay_in_place(a);
   if (r.ws || r.s_out) {

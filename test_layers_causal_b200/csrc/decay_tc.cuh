@@ -102,6 +102,7 @@ struct alignas(64) DecayTcArgs {
   DecayGeom g;
   DecayTcRun run[kDecayTcRuns];
   int nrun;
+  int clear;                // zeros for the first run's rows of o in no (packed) sequence
   const float* log_decay;
   uint64_t limit_ns;
 };
@@ -564,6 +565,7 @@ __global__ void __launch_bounds__(608, 1) decay_tc_out_kernel(const __grid_const
   const DecayTcRun& p = A.run[ri];
   const DecaySpan sp = decay_span_block(g, s, sh);
   launch_next();
+  if (A.clear) decay_clear_rest(g, A.run[0].op, A.run[0].oh, A.run[0].ot, A.run[0].dv);
   if (sp.seq < 0 || sp.len <= 0) {
     wait_before();
     return;

@@ -45,12 +45,14 @@ def _default_eta(eta_const, dk):
 
 
 def forward_decay(q, k, v, log_decay, eta_const=None, ascent=False, cu_seqlens=None, state_in=None,
-                  return_state=True, out=None, state_out=None, workspace=None, segment_tokens=0, stream=None):
+                  return_state=True, out=None, state_out=None, workspace=None, segment_tokens=0, clear_rest=False,
+                  stream=None):
     """Whole sequences (ttt_la_forward_decay).  Returns (o, W_T), W_T None
     when not requested.  ``eta_const`` defaults to 1/sqrt(d_k).  ``out``,
     ``state_out`` (which may be ``state_in``) and ``workspace`` may be
     preallocated; ``segment_tokens`` (a multiple of 64) overrides the
-    automatic split of long sequences."""
+    automatic split of long sequences; with ``clear_rest`` the rows of o in no
+    packed sequence are zeros instead of what was there."""
     N, H, T, dk, dv, dev = _shapes(q, k, v, log_decay, cu_seqlens)
     dt, code, state_shape = q.dtype, _abi._dtype_code(q), (N, H, dv, dk)
 
@@ -68,7 +70,8 @@ def forward_decay(q, k, v, log_decay, eta_const=None, ascent=False, cu_seqlens=N
             N, H, T, dk, dv, code, pq, pk, pv, po, *sq[:3], *sk[:3], *sv[:3], *so[:3], log_decay.data_ptr(),
             0 if cu_seqlens is None else cu_seqlens.data_ptr(), _default_eta(eta_const, dk), 1 if ascent else 0,
             check(state_in, "state_in", torch.float32, dev, state_shape),
-            check(state_out, "state_out", torch.float32, dev, state_shape) if return_state else 0, int(segment_tokens))
+            check(state_out, "state_out", torch.float32, dev, state_shape) if return_state else 0, int(segment_tokens),
+            1 if clear_rest else 0)
         run_with_workspace("ttt_la_forward_decay", "ttt_la_decay_workspace_size", block, workspace, dev, handle)
 
     launch_on(dev, stream, call)
@@ -152,9 +155,8 @@ def forward_decay_norm(q, k, v, log_decay, gate=None, weight=None, bias=None, ac
         x, y = o.view(rows), torch.empty(rows, device=v.device, dtype=v.dtype)
         # before the layer, which may update its state in place
         check_group_norm(x, H, weight, bias, gate, activation, eps)
-        if kw.get("cu_seqlens") is not None:
-            o.zero_()  # rows in no sequence: the norm reads them
-        _, W = forward_decay(q, k, v, log_decay, out=o.transpose(1, 2), stream=stream, **kw)
+        # (the norm reads all rows)
+        _, W = forward_decay(q, k, v, log_decay, out=o.transpose(1, 2), stream=stream, **{**kw, "clear_rest": True})
         if B * T > 0:
             group_norm(x, H, weight, bias, gate=gate, activation=activation, eps=eps, out=y, stream=stream)
     return y.view(B, T, H * dv), W

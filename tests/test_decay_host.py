@@ -268,3 +268,8 @@ def test_step_takes_values_of_any_width(abi):
     for d_v in (1, 20, 33):
         block = _step(abi, d_k=96, d_v=d_v, v_stride=I2(2 * d_v, d_v), o_stride=I2(2 * d_v + 3, d_v + 1))
         assert abi.lib().ttt_la_decode_step_decay(ctypes.byref(block), None) == abi.ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("clear_rest", [2, -1])
+def test_forward_refuses_a_clear_rest_that_is_no_truth_value(abi, clear_rest):
+    assert abi.lib().ttt_la_forward_decay(ctypes.byref(_fwd(abi, clear_rest=clear_rest)), None) == abi.ERR_INVALID_ARG

@@ -491,6 +491,49 @@ def test_a_wait_limit_covers_one_block_not_the_launches_before():
     assert all(torch.equal(x, y) for x, y in zip(got, want))
 
 
+@pytest.mark.parametrize("extra", [(0, 0), (5, 37), (0, 300), (90, 0)])
+@pytest.mark.parametrize("dtype,dk,dv,order", [("bf16", 64, 64, "tokens"), ("bf16", 128, 80, "heads"), ("bf16", 16, 136, "tokens"),
+                                               ("f32", 32, 12, "heads"), ("f32", 32, 64, "tokens")])
+def test_rest_is_cleared_where_it_is_asked_for(dtype, dk, dv, order, extra):
+    """Rows in no sequence become zeros, the others' bits stay, in a tensor
+    whose neighbours keep theirs."""
+    c = _make([70, 0, 200], 3, dk, dv, dtype, True, order, True, seed=45, extra=extra)
+    want, W = ttt.forward_decay(c["q"], c["k"], c["v"], c["ld"], cu_seqlens=c["cu"], state_in=c["W0"])
+    T = want.shape[2]
+    shape = (1, T, 3, 2 * dv) if order == "tokens" else (1, 3, T, 2 * dv)
+    room = torch.full(shape, 7.0, dtype=c["v"].dtype, device="cuda")
+    out = room[..., :dv]
+    out = out.transpose(1, 2) if order == "tokens" else out
+    o, W2 = ttt.forward_decay(c["q"], c["k"], c["v"], c["ld"], cu_seqlens=c["cu"], state_in=c["W0"], out=out, clear_rest=True)
+    a, b = extra[0], T - extra[1]
+    assert torch.equal(o[:, :, a:b], want[:, :, a:b]) and torch.equal(W, W2)
+    assert not o[:, :, :a].any() and not o[:, :, b:].any() and (room[..., dv:] == 7).all()
+
+
+def test_rest_of_only_empty_sequences_and_of_equal_lengths():
+    c = _make([0, 0], 2, 64, 64, "bf16", True, "tokens", True, seed=46, extra=(60, 80))
+    o, W = ttt.forward_decay(c["q"], c["k"], c["v"], c["ld"], cu_seqlens=c["cu"], state_in=c["W0"], clear_rest=True)
+    assert not o.any() and torch.equal(W, c["W0"])
+    c = _make([150, 150], 2, 64, 64, "bf16", False, "tokens", True, seed=47)  # nothing to clear
+    a = ttt.forward_decay(c["q"], c["k"], c["v"], c["ld"], state_in=c["W0"], clear_rest=True)
+    b = ttt.forward_decay(c["q"], c["k"], c["v"], c["ld"], state_in=c["W0"])
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_layer_then_norm_of_rows_in_no_sequence():
+    """Zeros as the norm sees them, whatever memory the output comes to lie in."""
+    c = _make([70, 0, 200], 2, 64, 64, "bf16", True, "tokens", True, seed=48, extra=(5, 37))
+    T, C = c["v"].shape[2], 128
+    b = torch.randn(C, generator=torch.Generator().manual_seed(3)).cuda()
+    for fill in (float("nan"), 3.0):
+        old = [torch.full((1, T, 2, 64), fill, dtype=torch.bfloat16, device="cuda") for _ in range(4)]
+        torch.cuda.synchronize()
+        del old  # the allocator hands it out again
+        y, _ = ttt.forward_decay_norm(c["q"], c["k"], c["v"], c["ld"], bias=b, cu_seqlens=c["cu"], state_in=c["W0"])
+        rest, _, _ = ttt.group_norm(torch.zeros(42, 1, C, dtype=torch.bfloat16, device="cuda"), 2, bias=b)
+        assert torch.equal(torch.cat([y[0, :5], y[0, T - 37:]]), rest[:, 0])
+
+
 def test_past_2_31_elements():
     """q, k, v of 257 heads x 65536 tokens x 128 (2^31 elements and more):
     the last head against the oracle."""
