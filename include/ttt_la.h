@@ -392,10 +392,10 @@ TTT_LA_API ttt_la_status ttt_la_backward_chunked(const ttt_la_grad_args *args, v
  * sequence or head.
  *
  * segment_tokens: tokens of a sequence handled by one block, a multiple of 64;
- * 0 = automatic (fills the SMs).  The workspace holds one state per segment
- * where sequences have several, or where state_out is state_in (size query; of
- * the pointers only cu_seqlens' being NULL and state_out's being state_in
- * count). */
+ * 0 = automatic (fills the SMs).  The workspace holds one state for each segment
+ * of the sequences that have several, packed at most 2 T / segment_tokens + 1
+ * of them, and where state_out is state_in of all (size query; of the pointers
+ * only cu_seqlens' being NULL and state_out's being state_in count). */
 typedef struct ttt_la_decay_args {
   int32_t N, H, T, d_k, d_v;
   int32_t dtype;            /* of q, k, v, o */

@@ -35,9 +35,16 @@ namespace ttt {
 // [cu[n], cu[n+1]) (values outside [0, T] are clamped to it, so no access
 // leaves the tensors whatever cu holds).  Every sequence has at least one
 // segment, an empty one too, whose block hands its state on.
+//
+// The workspace has a slot for each segment of the sequences that have several
+// (`all`: of every sequence), numbered like the segments.  Many short sequences
+// so need no more of it than the tokens do.  (Offsets that overlap make more
+// segments than there are slots: those without one are not worked on.)
 struct DecayGeom {
   int N, H, T, S;
   int nseg;         // upper bound of the segments over all sequences
+  int slots;        // of the workspace
+  int all;
   const int* cu;
 };
 
@@ -47,6 +54,7 @@ struct DecaySpan {
   int row0;    // first token row
   int len;     // tokens in the segment
   int j, nseg; // segment j of the sequence's nseg
+  int slot;    // its place in the workspace, where it has one
 };
 
 __device__ __forceinline__ int decay_segments(int len, int S) { return len > 0 ? (len - 1) / S + 1 : 1; }
@@ -84,6 +92,7 @@ __device__ __forceinline__ DecaySpan decay_span(const DecayGeom& g, int s) {
   DecaySpan r;
   r.seq = -1;
   r.batch = r.row0 = r.len = r.j = r.nseg = 0;
+  r.slot = s;
   if (!g.cu) {
     const int per = decay_segments(g.T, g.S);
     if (s >= g.N * per) return r;
@@ -96,6 +105,7 @@ __device__ __forceinline__ DecaySpan decay_span(const DecayGeom& g, int s) {
   }
   const int lane = threadIdx.x & 31;
   int before = 0;  // segments of the sequences before n0
+  int single = 0;  // sequences among them that are one segment, which has no slot
   for (int n0 = 0; n0 < g.N; n0 += 32) {
     const int n = n0 + lane;
     int a = 0, b = 0, c = 0;
@@ -109,9 +119,10 @@ __device__ __forceinline__ DecaySpan decay_span(const DecayGeom& g, int s) {
       const int y = __shfl_up_sync(0xffffffffu, incl, off);
       if (lane >= off) incl += y;
     }
-    const unsigned hit = __ballot_sync(0xffffffffu, before + incl > s);
+    const unsigned hit = __ballot_sync(0xffffffffu, before + incl > s), one = __ballot_sync(0xffffffffu, c == 1 && !g.all);
     if (hit) {
       const int f = __ffs(hit) - 1;
+      r.slot = s - single - __popc(one & ((1u << f) - 1u));
       a = __shfl_sync(0xffffffffu, a, f);
       b = __shfl_sync(0xffffffffu, b, f);
       c = __shfl_sync(0xffffffffu, c, f);
@@ -121,24 +132,27 @@ __device__ __forceinline__ DecaySpan decay_span(const DecayGeom& g, int s) {
       r.nseg = c;
       r.row0 = a + r.j * g.S;
       r.len = min(g.S, b - r.row0);
+      if ((c > 1 || g.all) && r.slot >= g.slots) r.seq = -1;
       return r;
     }
     before += __shfl_sync(0xffffffffu, incl, 31);
+    single += __popc(one);
   }
   return r;
 }
 
-// The first segment of sequence n, counted over all sequences; whole warps.
-__device__ __forceinline__ int decay_first_segment(const DecayGeom& g, int n) {
+// The first slot of sequence n, at most `slots`; whole warps.
+__device__ __forceinline__ int decay_first_slot(const DecayGeom& g, int n) {
   if (!g.cu) return n * decay_segments(g.T, g.S);
   int c = 0;
   for (int m = threadIdx.x & 31; m < n; m += 32) {
     int a, b;
     decay_rows(g, m, a, b);
-    c += decay_segments(b - a, g.S);
+    const int x = decay_segments(b - a, g.S);
+    if (x > 1 || g.all) c = min(c + x, g.slots);  // (at most 2^25 each: no overflow whatever the offsets)
   }
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) c += __shfl_xor_sync(0xffffffffu, c, off);
+  for (int off = 16; off > 0; off >>= 1) c = min(c + __shfl_xor_sync(0xffffffffu, c, off), g.slots);
   return c;
 }
 
@@ -164,17 +178,17 @@ struct DecayRun {
   const float* s_in;       // [N][H][dv][dk], or [N][H][dk][dv] where s_in_t; nullptr: zeros
   int s_in_t;
   float* s_out;            // [N][H][dv][dk] or nullptr
-  float* ws;               // [nseg][H][dv][dk]: segments' contributions, then start states; nullptr: one segment each
+  float* ws;               // [slots][H][dv][dk]: segments' contributions, then start states; nullptr: one segment each
   int clear;               // zeros for o's rows in no (packed) sequence
 };
 
 // The state that a segment's block starts from: the caller's where the
 // sequence is a single segment, else the scan's.
-__device__ __forceinline__ const float* decay_start(const DecayRun& p, const DecaySpan& sp, int s, int H, int h,
+__device__ __forceinline__ const float* decay_start(const DecayRun& p, const DecaySpan& sp, int H, int h,
                                                     bool* transposed) {
   const size_t dd = static_cast<size_t>(p.dv) * p.dk;
   *transposed = false;
-  if (sp.nseg > 1) return p.ws + (static_cast<size_t>(s) * H + h) * dd;
+  if (sp.nseg > 1) return p.ws + (static_cast<size_t>(sp.slot) * H + h) * dd;
   if (!p.s_in) return nullptr;
   *transposed = p.s_in_t != 0;
   return p.s_in + (static_cast<size_t>(sp.seq) * H + h) * dd;
@@ -213,7 +227,7 @@ __global__ void __launch_bounds__(256) decay_scan_kernel(const DecayScans ps, co
   decay_rows(g, n, a, b);
   const int len = b - a, nseg = decay_segments(len, g.S);
   if (nseg <= 1 && !p.all) return;
-  const int first = decay_first_segment(g, n);
+  const int first = decay_first_slot(g, n);
   const size_t e = (static_cast<size_t>(blockIdx.x % slices) * blockDim.x + threadIdx.x) * 4;
   if (e >= dd) return;
   const float l = decay_log(log_decay, h);
@@ -238,13 +252,12 @@ __global__ void __launch_bounds__(256) decay_scan_kernel(const DecayScans ps, co
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int i = i0 + u, j = p.rev ? nseg - 1 - i : i;
-      // (segments past the bound, of offsets that overlap, have no slot)
-      if (i < sums && first + j < g.nseg) t[u] = ld_after(reinterpret_cast<const float4*>(w + j * pitch));
+      if (i < sums && first + j < g.slots) t[u] = ld_after(reinterpret_cast<const float4*>(w + j * pitch));
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int i = i0 + u, j = p.rev ? nseg - 1 - i : i;
-      if (i < nseg && first + j < g.nseg) {
+      if (i < nseg && first + j < g.slots) {
         __stcg(reinterpret_cast<float4*>(w + j * pitch), run);
         if (i < sums) {
           const float f = (j == nseg - 1) ? gL : gS;
@@ -309,7 +322,7 @@ __global__ void __launch_bounds__(256) decay_simt_kernel(const DecayGeom g, cons
 
   if (tid <= C) gp[tid] = expf(l * static_cast<float>(tid));
   bool tr = false;
-  const float* s0 = TOT ? nullptr : decay_start(p, sp, s, g.H, h, &tr);
+  const float* s0 = TOT ? nullptr : decay_start(p, sp, g.H, h, &tr);
   for (int i = tid; i < VT * dk; i += 256) {
     const int r = i / dk, c = i % dk;
     float x = 0.f;
@@ -467,7 +480,7 @@ __global__ void __launch_bounds__(256) decay_simt_kernel(const DecayGeom g, cons
   __syncthreads();
   float* dst = nullptr;
   if (TOT)
-    dst = p.ws + (static_cast<size_t>(s) * g.H + h) * dd;
+    dst = p.ws + (static_cast<size_t>(sp.slot) * g.H + h) * dd;
   else if (p.s_out && sp.j == (p.rev ? 0 : sp.nseg - 1))
     dst = p.s_out + (static_cast<size_t>(sp.seq) * g.H + h) * dd;
   if (dst)

@@ -53,7 +53,15 @@ DecayLayout decay_layout(const int32_t* cu, int N, int H, int T, int dk, int dv,
   const long long nseg = cu ? (multi ? T / tokens : 0) + static_cast<long long>(N)
                             : static_cast<long long>(N) * (T > 0 ? (T - 1) / tokens + 1 : 1);
   l.g.nseg = nseg < (1ll << 31) ? static_cast<int>(nseg) : -1;
-  l.run_floats = multi || every ? static_cast<size_t>(nseg) * H * dk * dv : 0;
+  // packed: each sequence of several segments is longer than one and has at most one that is not whole
+  long long slots = 0;
+  if (every || (multi && !cu))
+    slots = nseg;
+  else if (multi)
+    slots = T / tokens + std::min<long long>(N, T / (static_cast<long long>(tokens) + 1));
+  l.g.slots = slots < (1ll << 31) ? static_cast<int>(slots) : 0;  // (nseg, which is no less, is refused then)
+  l.g.all = every;
+  l.run_floats = static_cast<size_t>(slots) * H * dk * dv;
   return l;
 }
 

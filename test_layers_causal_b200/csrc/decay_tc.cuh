@@ -107,12 +107,12 @@ struct alignas(64) DecayTcArgs {
   uint64_t limit_ns;
 };
 
-// decay_span by all threads of the block; sh: 40 ints of shared memory.
+// decay_span by all threads of the block; sh: 64 ints of shared memory.
 __device__ __forceinline__ DecaySpan decay_span_block(const DecayGeom& g, int s, int* sh) {
   if (!g.cu) return decay_span(g, s);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
   if (tid == 0) sh[32] = -1;
-  int before = 0;
+  int before = 0, single = 0;
   for (int n0 = 0; n0 < g.N; n0 += static_cast<int>(blockDim.x)) {
     const int n = n0 + tid;
     int a = 0, b = 0, c = 0;
@@ -126,12 +126,20 @@ __device__ __forceinline__ DecaySpan decay_span_block(const DecayGeom& g, int s,
       const int y = __shfl_up_sync(0xffffffffu, incl, off);
       if (lane >= off) incl += y;
     }
-    if (lane == 31) sh[warp] = incl;
+    const unsigned one = __ballot_sync(0xffffffffu, c == 1 && !g.all);
+    if (lane == 31) {
+      sh[warp] = incl;
+      sh[40 + warp] = __popc(one);
+    }
     __syncthreads();
-    int below = before, all = before;
+    int below = before, all = before, none = single + __popc(one & ((1u << lane) - 1u));
     for (int w = 0; w < nw; ++w) {
-      if (w < warp) below += sh[w];
+      if (w < warp) {
+        below += sh[w];
+        none += sh[40 + w];
+      }
       all += sh[w];
+      single += sh[40 + w];
     }
     incl += below;
     if (incl > s && incl - c <= s && c > 0) {  // exactly one thread, if any
@@ -140,6 +148,7 @@ __device__ __forceinline__ DecaySpan decay_span_block(const DecayGeom& g, int s,
       sh[34] = b;
       sh[35] = s - (incl - c);
       sh[36] = c;
+      sh[37] = s - none;
     }
     before = all;
     __syncthreads();
@@ -148,12 +157,14 @@ __device__ __forceinline__ DecaySpan decay_span_block(const DecayGeom& g, int s,
   DecaySpan r;
   r.seq = sh[32];
   r.batch = 0;
-  r.row0 = r.len = r.j = r.nseg = 0;
+  r.row0 = r.len = r.j = r.nseg = r.slot = 0;
   if (r.seq >= 0) {
     r.j = sh[35];
     r.nseg = sh[36];
     r.row0 = sh[33] + r.j * g.S;
     r.len = min(g.S, sh[34] - r.row0);
+    r.slot = sh[37];
+    if ((r.nseg > 1 || g.all) && r.slot >= g.slots) r.seq = -1;
   }
   return r;
 }
@@ -170,6 +181,7 @@ struct DecayTcCfg {
   static constexpr int NST = ROOM > 4 ? 4 : ROOM;
   static constexpr int BIG = NST * STAGE + WBF + LO;
   static constexpr int SMEM = BIG + 1024 + 1024;           // + barriers and tables, + alignment
+  static_assert((4 * NST + 18) * 8 + 97 * 4 + 64 * 4 <= 1024, "barriers, tables and decay_span_block's");
   static constexpr int THREADS = 608;                      // TMA, MMA, 8 warps P and outputs, 8 warps state, MMA
   static constexpr int NW = DK * DV / 256;                 // elements of X per state thread
   // tensor memory: Sc (P over it; twice where it fits), O1, O2, D
@@ -474,7 +486,7 @@ __global__ void __launch_bounds__(576, 1) decay_tc_total_kernel(const __grid_con
     // a sequence of one segment: its final state is made here
     const bool direct = sp.nseg == 1 && !p.ws_all;
     float* dst = (direct ? p.s_out + (static_cast<size_t>(sp.seq) * g.H + h) * dd
-                         : p.ws + (static_cast<size_t>(s) * g.H + h) * dd) + off;
+                         : p.ws + (static_cast<size_t>(sp.slot) * g.H + h) * dd) + off;
     const float* src = direct && p.s_in ? p.s_in + (static_cast<size_t>(sp.seq) * g.H + h) * dd + off : nullptr;
     const float gl = expf(l * static_cast<float>(sp.len));
 #pragma unroll
@@ -557,7 +569,7 @@ __global__ void __launch_bounds__(608, 1) decay_tc_out_kernel(const __grid_const
   float* colp = reinterpret_cast<float*>(bars + 4 * NST + 18);  // [32] gamma^(31-t), reverse gamma^t
   float* diag = colp + 32;                                      // [64] sP gamma^(x-31) at x >= 31
   uint32_t* holder = reinterpret_cast<uint32_t*>(diag + 64);
-  int* sh = reinterpret_cast<int*>(holder + 1);                 // [40]
+  int* sh = reinterpret_cast<int*>(holder + 1);                 // [64]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const DecayGeom& g = A.g;
@@ -871,7 +883,7 @@ __global__ void __launch_bounds__(608, 1) decay_tc_out_kernel(const __grid_const
       const size_t dd = static_cast<size_t>(p.dk) * p.dv;
       wait_before();  // the scan's states
       const bool via = p.ws && (sp.nseg > 1 || p.ws_all);
-      const float* src = via ? p.ws + (static_cast<size_t>(s) * g.H + h) * dd
+      const float* src = via ? p.ws + (static_cast<size_t>(sp.slot) * g.H + h) * dd
                              : p.s_in ? p.s_in + (static_cast<size_t>(sp.seq) * g.H + h) * dd : nullptr;
       const bool tr = via ? p.ws_t != 0 : p.s_in_t != 0;
       if (src) {

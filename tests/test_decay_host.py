@@ -273,3 +273,27 @@ def test_step_takes_values_of_any_width(abi):
 @pytest.mark.parametrize("clear_rest", [2, -1])
 def test_forward_refuses_a_clear_rest_that_is_no_truth_value(abi, clear_rest):
     assert abi.lib().ttt_la_forward_decay(ctypes.byref(_fwd(abi, clear_rest=clear_rest)), None) == abi.ERR_INVALID_ARG
+
+
+def test_workspace_does_not_grow_with_short_sequences(abi):
+    """Thousands of packed sequences of a few tokens: the workspace follows the
+    tokens, as segments of sequences that are one need none; in place, where
+    all start states go through it, each has a state."""
+    L = abi.lib()
+    kw = dict(N=4096, H=16, T=8192, d_k=128, d_v=128, cu_seqlens=0x60000, segment_tokens=64)
+    state = 16 * 128 * 128 * 4
+    assert 0 < L.ttt_la_decay_workspace_size(ctypes.byref(_fwd(abi, **kw))) <= (2 * 8192 // 64 + 1) * state
+    assert 0 < L.ttt_la_backward_decay_workspace_size(ctypes.byref(_bwd(abi, **kw))) <= 2 * (2 * 8192 // 64 + 1) * state
+    inplace = L.ttt_la_decay_workspace_size(ctypes.byref(_fwd(abi, state_in=0x70000, state_out=0x70000, **kw)))
+    assert inplace >= 4096 * state
+    # with the segments left to the library too
+    kw.pop("segment_tokens")
+    assert L.ttt_la_decay_workspace_size(ctypes.byref(_fwd(abi, **kw))) <= 4096 * state // 8
+    # and however the tokens lie: one sequence of all of them, and N - 1 empty ones
+    for N, T, S in ((1, 1000, 64), (2, 129, 64), (7, 1000, 64), (300, 12800, 128), (5, 64 * 50, 64)):
+        kw = dict(N=N, H=1, T=T, d_k=64, d_v=64, cu_seqlens=0x60000, segment_tokens=S)
+        slots = L.ttt_la_decay_workspace_size(ctypes.byref(_fwd(abi, **kw))) // (64 * 64 * 4)
+        one = (T + S - 1) // S
+        many = min(N, T // (S + 1))  # as many of two segments as there can be, the rest behind the first
+        worst = max(one, 2 * (many - 1) + -(-(T - (many - 1) * (S + 1)) // S)) if many else one
+        assert worst <= slots <= worst + 1, (N, T, S, worst, slots)

@@ -534,6 +534,76 @@ def test_layer_then_norm_of_rows_in_no_sequence():
         assert torch.equal(torch.cat([y[0, :5], y[0, T - 37:]]), rest[:, 0])
 
 
+def _exact_workspace(need):
+    """A workspace of just the bytes, between others that are to stay."""
+    room = torch.full((need + 8192,), 85, dtype=torch.uint8, device="cuda")
+    return room, room[4096:4096 + need], lambda: bool((room[:4096] == 85).all() and (room[4096 + need:] == 85).all())
+
+
+def _workspace_need(c, seg, in_place=False):
+    """(forward's, gradient's) bytes, as the library asks for them."""
+    import ctypes
+    from test_layers_causal_b200 import _abi
+    N, (_, H, T, dk), dv = len(c["lens"]), c["q"].shape, c["v"].shape[-1]
+    out = []
+    for cls, name in ((_abi.TttDecayArgs, "ttt_la_decay_workspace_size"), (_abi.TttDecayGradArgs, "ttt_la_backward_decay_workspace_size")):
+        a = cls()
+        a.N, a.H, a.T, a.d_k, a.d_v, a.dtype, a.segment_tokens = N, H, T, dk, dv, _abi._dtype_code(c["q"]), seg
+        a.log_decay, a.cu_seqlens = c["ld"].data_ptr(), c["cu"].data_ptr()
+        if in_place and cls is _abi.TttDecayArgs:
+            a.state_in = a.state_out = c["W0"].data_ptr()
+        out.append(getattr(_abi.lib(), name)(ctypes.byref(a)))
+    return out
+
+
+@pytest.mark.parametrize("dtype,dk,dv", [("bf16", 64, 64), ("bf16", 64, 128), ("bf16", 16, 136), ("f32", 32, 36)])
+def test_workspace_of_few_long_among_many_short(dtype, dk, dv):
+    """Sequences of several segments here and there among hundreds of one, more
+    than a block counts at once: each finds its slots, in just the bytes that
+    the library asks for."""
+    lens = [(7 * i) % 5 for i in range(900)]
+    for i, n in ((0, 65), (31, 64), (32, 200), (33, 129), (607, 300), (608, 65), (899, 190)):
+        lens[i] = n
+    c = _make(lens, 1, dk, dv, dtype, True, "tokens", True, seed=51)
+    need, back = _workspace_need(c, 64)
+    T, state = sum(lens), dk * dv * 4
+    assert 0 < need <= (2 * T // 64 + 1) * state < len(lens) * state
+    room, w, whole = _exact_workspace(need)
+    S = c["W0"].clone()
+    o, W = ttt.forward_decay(c["q"], c["k"], c["v"], c["ld"], cu_seqlens=c["cu"], state_in=c["W0"], segment_tokens=64, workspace=w)
+    assert whole()
+    _check_forward(c, o, W, dtype, np.float64(np.float32(1 / math.sqrt(dk))))
+    if dtype == "bf16" and dv <= 128:
+        room, w, whole = _exact_workspace(_workspace_need(c, 64, True)[0])
+        o2, _ = ttt.forward_decay(c["q"], c["k"], c["v"], c["ld"], cu_seqlens=c["cu"], state_in=S, state_out=S, segment_tokens=64,
+                                  workspace=w)
+        assert whole() and torch.equal(o, o2) and torch.equal(S, W)
+    room, w, whole = _exact_workspace(back)
+    g = ttt.backward_decay(c["q"], c["k"], c["v"], c["dO"], c["ld"], cu_seqlens=c["cu"], state_in=c["W0"], grad_state=c["dW"],
+                           segment_tokens=64, workspace=w)
+    assert whole()
+    _check_backward(c, g, dtype, np.float64(np.float32(1 / math.sqrt(dk))))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_offsets_of_more_segments_than_slots_stay_in_the_workspace(dtype):
+    """Offsets that go back and forth over the rows: the call returns, the
+    memory around its workspace and output as it was."""
+    c = _make([640], 1, 32, 64, dtype, True, "tokens", False, seed=52)
+    n = 3000
+    c["cu"] = torch.randint(-50, 700, (n + 1,), dtype=torch.int32, generator=torch.Generator().manual_seed(1)).cuda()
+    c["lens"] = [0] * n
+    need, back = _workspace_need(c, 64)
+    room, w, whole = _exact_workspace(need)
+    rows = torch.full((3, 640, 1, 64), 5.0, dtype=c["v"].dtype, device="cuda")
+    ttt.forward_decay(c["q"], c["k"], c["v"], c["ld"], cu_seqlens=c["cu"], out=rows[1:2].transpose(1, 2), segment_tokens=64,
+                      workspace=w)
+    assert whole() and (rows[0] == 5).all() and (rows[2] == 5).all()
+    room, w, whole = _exact_workspace(back)
+    ttt.backward_decay(c["q"], c["k"], c["v"], c["dO"], c["ld"], cu_seqlens=c["cu"], segment_tokens=64, workspace=w)
+    assert whole()
+
+
 def test_past_2_31_elements():
     """q, k, v of 257 heads x 65536 tokens x 128 (2^31 elements and more):
     the last head against the oracle."""
