@@ -372,21 +372,24 @@ TTT_LA_API ttt_la_status ttt_la_backward_chunked(const ttt_la_grad_args *args, v
  * Layout.  N sequences.  q, k: [N,H,T,d_k], v, o: [N,H,T,d_v] in any memory
  * order whose features are contiguous: x_stride[3] are the elements between
  * sequences, heads and tokens, multiples of 16 bytes (not read for a
- * dimension of size 1); rows of different (sequence, head, token) of an output
- * must not overlap.  With cu_seqlens (device int32 [N+1], not decreasing) the
- * sequences are packed: q, k, v, o have T rows in all, sequence n's are rows
- * [cu_seqlens[n], cu_seqlens[n+1]), x_stride[0] is not read, and rows in no
- * sequence, those before the first one and behind the last, are not read into
- * a result, and of o left as they are, or set to zero where clear_rest is 1.
- * Sequences may be empty: their state passes through.  Values of cu_seqlens outside [0, T] are
- * clamped to it.  log_decay: device fp32 [H], <= 0 (-inf: gamma = 0); it is a
- * constant, without a gradient.  state_in / state_out: fp32 [N,H,d_v,d_k],
- * state_out may be state_in.
+ * dimension of size 1; a stride of 0 is refused); rows of different (sequence,
+ * head, token) of an output must not overlap, nor o the inputs, nor state_out
+ * anything but state_in, which it may equal.  With cu_seqlens (device int32
+ * [N+1], not decreasing) the sequences are packed: q, k, v, o have T rows in
+ * all, sequence n's are rows [cu_seqlens[n], cu_seqlens[n+1]), x_stride[0] is
+ * not read, and rows in no sequence, those before the first one and behind the
+ * last, are not read into a result, and of o left as they are, or set to zero
+ * where clear_rest is 1.  Sequences may be empty: their state passes through.
+ * Values of cu_seqlens outside [0, T] are clamped to it.  log_decay: device fp32
+ * [H], <= 0 (-inf: gamma = 0); it is a constant, without a gradient.  state_in
+ * / state_out: fp32 [N,H,d_v,d_k].
  *
  * dtype bf16: d_k and d_v multiples of 8 up to 256; fp32: multiples of 4 up to
  * 256; others TTT_LA_ERR_UNSUPPORTED.  Sums and states are fp32;
  * bf16 up to 128 wide runs on the tensor cores, where the weighted scores and
- * the state as it is read for an output are rounded to bf16 once.  A value that
+ * the state as it is read for an output are rounded to bf16 once, from T = 64 on
+ * (T: the rows of the call, so the bits of a packed sequence's outputs may
+ * depend on what it is packed with, by the kernel and by the split).  A value that
  * is not finite may reach every output of its own tile of 128 tokens, earlier
  * ones included, and all later ones of its (sequence, head), never another
  * sequence or head.
@@ -494,7 +497,10 @@ TTT_LA_API ttt_la_status ttt_la_group_norm(const ttt_la_group_norm_args *args, v
 
 /* Its gradient for dL/dy, with the forward's x, gate, weight, bias, mean and
  * rstd: grad_x (required), grad_gate (required with a gate), grad_weight and
- * grad_bias of param_dtype (each optional).  Sums in fp32 in a fixed order.
+ * grad_bias of param_dtype (each optional).  Sums in fp32 in a fixed order.  The
+ * workspace holds two fp32 sums of each channel for each part of a sample, a
+ * sample being one part or more: 8 N C bytes where samples are single positions
+ * whose groups are not 1, 2, 4 .. 32 times 16 bytes wide.
  * Outputs must not overlap inputs or one another. */
 typedef struct ttt_la_group_norm_grad_args {
   int32_t N, L, C, G;

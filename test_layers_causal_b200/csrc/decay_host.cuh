@@ -119,6 +119,12 @@ ttt_la_status decay_simt_runs(const ttt::DecayGeom& g, const ttt::DecayRun* r, i
 // whole row's): relative error 1.7e-3 against 2.4e-3 here. The price, two
 // sequences x 24 heads x 128: forward 23 us either way, at 31 tokens there and 32
 // here; gradient 67 us there, 30 us here; with one head 45 and 30 us.
+// T counts all rows of the call, those of packed sequences together, so that many
+// short ones come here, where a block costs less than the fp32 kernel's four even
+// for one token (64 sequences x 16 heads x 128 of 1, 15, 46 tokens: forward 114,
+// 143, 151 us here and 184, 250, 417 there, gradient 211, 280, 293 and 493, 682,
+// 1181; the exception is 64 wide up to eight tokens: 89 and 64 us at one). Their
+// outputs are rounded as long ones' are.
 bool decay_on_tc(int dtype, int T, int dk, int dv) { return dtype == TTT_LA_BF16 && T >= 64 && dk <= 128 && dv <= 128; }
 
 // Tokens per segment of the tensor-core kernels, whose blocks have an SM each.
@@ -146,8 +152,12 @@ int decay_tc_plan_tokens(long long heads, int rows, int runs, bool packed, int s
     if (heads * n * runs > 8ll * slots) break;
   }
   // Packed sequences end where they end, and what fills the SMs evenly as one long one leaves them waiting for the
-  // longest: at least 1.3 blocks for each SM, but no segment below 512 tokens for that (B200: 3641 tokens in 5
-  // sequences, gradient of 12 heads, 104 us at one block an SM, 83 at 640 tokens; 12385 in 10, prompt, 142 and 135).
+  // longest: at least 1.3 blocks for each SM, but no segment below 512 tokens for that.  The host does not see the
+  // lengths, and the rule pays where they differ: us with the even split, then with the rule, of 10 sequences of 1 to
+  // 3999 tokens, gradient of 4 heads x 128 93 and 86, of 12 x 64 151 and 133; 30 of 1 to 2000, prompt of 4 x 128 111
+  // and 99; no difference for 16 heads x 128 of either, 200 of 1 to 120, 64 of 256.  It costs where a few are equally
+  // long or one is nearly all: 2 of 6000, prompt of 16 x 128 93 and 116, gradient of 4 x 128 72 and 86; 12000 tokens
+  // and 20 of 20, gradient of 4 x 128 86 and 94.
   if (packed) {
     const long long even = static_cast<long long>(rows) * heads * runs * 10 / (13ll * slots) / ttt::kDecayTcC;
     best = static_cast<int>(std::min<long long>(best, std::max<long long>(even, 512 / ttt::kDecayTcC)));

@@ -95,7 +95,9 @@ __device__ __forceinline__ float gn_param(const void* p, int pbf, int c, float n
   return pbf ? __bfloat162float(__ldg(static_cast<const __nv_bfloat16*>(p) + c)) : __ldg(static_cast<const float*>(p) + c);
 }
 // 1 / (1 + exp(-x)): the approximate exponential and reciprocal are off by a
-// few steps; an exp(-x) that overflows gives 0.
+// few steps and the rounded exponent by |x| of them relative to the result, which
+// falls off faster where x is negative: silu is off by a few 2^-24 at most, its
+// slope too.  Below x = -87, where the result passes 2^-126, it is 0.
 __device__ __forceinline__ float gn_sigmoid1(float e) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(e));

@@ -604,6 +604,43 @@ def test_offsets_of_more_segments_than_slots_stay_in_the_workspace(dtype):
     assert whole()
 
 
+def test_captured_packed_calls_follow_the_offsets():
+    """A captured call of the layer, its gradient and its norm on packed
+    sequences, replayed after the offsets, the inputs and the state changed,
+    gives what a fresh call gives: nothing of the offsets is kept."""
+    c = _make([300, 1, 0, 200], 2, 64, 128, "bf16", True, "tokens", True, seed=53, extra=(0, 20))
+    C = 256
+    gate = torch.randn(1, C, 521, generator=torch.Generator().manual_seed(4)).to(torch.bfloat16).cuda().transpose(1, 2)
+
+    def call():
+        y, W = ttt.forward_decay_norm(c["q"], c["k"], c["v"], c["ld"], gate=gate, cu_seqlens=c["cu"], state_in=c["W0"],
+                                      segment_tokens=64)
+        g = ttt.backward_decay(c["q"], c["k"], c["v"], c["dO"], c["ld"], cu_seqlens=c["cu"], state_in=c["W0"],
+                               grad_state=c["dW"], segment_tokens=64)
+        return [y, W, *g.values()]
+
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = call()
+    for cu in ([0, 300, 301, 301, 501], [0, 64, 130, 130, 521], [3, 3, 503, 503, 504]):
+        for n in ("q", "k", "v", "dO"):
+            c[n].copy_(torch.randn(c[n].shape, generator=torch.Generator().manual_seed(cu[1])).to(torch.bfloat16) * 0.1)
+        c["W0"].mul_(0.5)
+        c["cu"].copy_(torch.tensor(cu, dtype=torch.int32))
+        for t in got[2:5]:
+            t.zero_()  # rows in no sequence are nobody's
+        graph.replay()
+        want = call()
+        torch.cuda.synchronize()
+        a, b = cu[0], cu[-1]
+        for i, (x, y) in enumerate(zip(got, want)):
+            if 2 <= i < 5:
+                x, y = x[:, :, a:b], y[:, :, a:b]
+            assert torch.equal(x, y), i
+
+
 def test_past_2_31_elements():
     """q, k, v of 257 heads x 65536 tokens x 128 (2^31 elements and more):
     the last head against the oracle."""
