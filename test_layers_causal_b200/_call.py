@@ -31,6 +31,19 @@ _current_handle = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
+def packer(name):
+    """Packs the struct's fields; a size that its field cannot hold (2^31
+    positions and more) is refused as an argument."""
+    pack = FORMATS[name].pack
+
+    def packed(*fields):
+        try:
+            return pack(*fields)
+        except struct.error as e:
+            raise ValueError(f"{name}: {e}") from None
+    return packed
+
+
 def _function(name, restype):
     f = _functions.get(name)
     if f is None:

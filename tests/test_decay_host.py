@@ -297,3 +297,13 @@ def test_workspace_does_not_grow_with_short_sequences(abi):
         many = min(N, T // (S + 1))  # as many of two segments as there can be, the rest behind the first
         worst = max(one, 2 * (many - 1) + -(-(T - (many - 1) * (S + 1)) // S)) if many else one
         assert worst <= slots <= worst + 1, (N, T, S, worst, slots)
+
+
+def test_sizes_past_their_field_are_refused_as_arguments():
+    from test_layers_causal_b200._call import FORMATS, packer
+    for name, fmt in FORMATS.items():
+        n = len(fmt.unpack(bytes(fmt.size)))
+        assert packer(name)(*[0] * n) == bytes(fmt.size)
+        for bad in (1 << 31, -(1 << 31) - 1):
+            with pytest.raises(ValueError, match=name):
+                packer(name)(bad, *[0] * (n - 1))
