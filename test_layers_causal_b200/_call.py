@@ -31,19 +31,6 @@ _current_handle = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def packer(name):
-    """Packs the struct's fields; a size that its field cannot hold (2^31
-    positions and more) is refused as an argument."""
-    pack = FORMATS[name].pack
-
-    def packed(*fields):
-        try:
-            return pack(*fields)
-        except struct.error as e:
-            raise ValueError(f"{name}: {e}") from None
-    return packed
-
-
 def _function(name, restype):
     f = _functions.get(name)
     if f is None:
@@ -91,13 +78,18 @@ def on_stream(device, stream):
 
 def launch_on(device, stream, call):
     """call(handle) with the tensors' device and the call's stream current
-    (on_stream without its cost where they already are)."""
+    (on_stream without its cost where they already are).  A size that its
+    field of the block cannot hold (2^31 positions and more) is refused as an
+    argument."""
     if device.type != "cuda":
         raise ValueError("all tensors must be on one CUDA device")
-    if stream is None and torch.cuda.current_device() == device.index:
-        return call(_current_handle(device.index))
-    with on_stream(device, stream) as handle:
-        return call(handle)
+    try:
+        if stream is None and torch.cuda.current_device() == device.index:
+            return call(_current_handle(device.index))
+        with on_stream(device, stream) as handle:
+            return call(handle)
+    except struct.error as e:
+        raise ValueError(f"an argument is too large: {e}") from None
 
 
 def check(t, name, dtype, device, shape=None, contiguous=True):

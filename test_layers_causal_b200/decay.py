@@ -18,12 +18,12 @@ import math
 import torch
 
 from . import _abi
-from ._call import check, check_distinct_rows, check_rows, launch_on, on_stream, packer, run, run_with_workspace
+from ._call import FORMATS, check, check_distinct_rows, check_rows, launch_on, on_stream, run, run_with_workspace
 from .norm import check_group_norm, group_norm
 
-_FORWARD = packer("ttt_la_decay_args")
-_BACKWARD = packer("ttt_la_decay_grad_args")
-_STEP = packer("ttt_la_decay_decode_args")
+_FORWARD = FORMATS["ttt_la_decay_args"].pack
+_BACKWARD = FORMATS["ttt_la_decay_grad_args"].pack
+_STEP = FORMATS["ttt_la_decay_decode_args"].pack
 
 
 def _shapes(q, k, v, log_decay, cu_seqlens):

@@ -5,10 +5,10 @@ from __future__ import annotations
 import torch
 
 from . import _abi
-from ._call import check, launch_on, packer, run_with_workspace
+from ._call import FORMATS, check, launch_on, run_with_workspace
 
-_FORWARD = packer("ttt_la_group_norm_args")
-_BACKWARD = packer("ttt_la_group_norm_grad_args")
+_FORWARD = FORMATS["ttt_la_group_norm_args"].pack
+_BACKWARD = FORMATS["ttt_la_group_norm_grad_args"].pack
 _ACTIVATIONS = {None: 0, "none": 0, "silu": 1}
 
 

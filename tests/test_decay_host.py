@@ -299,11 +299,12 @@ def test_workspace_does_not_grow_with_short_sequences(abi):
         assert worst <= slots <= worst + 1, (N, T, S, worst, slots)
 
 
-def test_sizes_past_their_field_are_refused_as_arguments():
-    from test_layers_causal_b200._call import FORMATS, packer
-    for name, fmt in FORMATS.items():
+def test_sizes_past_their_field_are_refused_as_arguments(monkeypatch):
+    from test_layers_causal_b200 import _call
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(_call, "_current_handle", lambda index: 0)
+    for fmt in _call.FORMATS.values():
         n = len(fmt.unpack(bytes(fmt.size)))
-        assert packer(name)(*[0] * n) == bytes(fmt.size)
         for bad in (1 << 31, -(1 << 31) - 1):
-            with pytest.raises(ValueError, match=name):
-                packer(name)(bad, *[0] * (n - 1))
+            with pytest.raises(ValueError, match="too large"):
+                _call.launch_on(torch.device("cuda", 0), None, lambda handle: fmt.pack(bad, *[0] * (n - 1)))
