@@ -107,11 +107,12 @@ struct alignas(64) DecayTcArgs {
   uint64_t limit_ns;
 };
 
-// decay_span by all threads of the block; sh: 64 ints of shared memory.
+// decay_span by all threads of the block (at most 768), where there are more
+// sequences than a warp sees at once; sh: 64 ints of shared memory on 8 bytes.
 __device__ __forceinline__ DecaySpan decay_span_block(const DecayGeom& g, int s, int* sh) {
-  if (!g.cu) return decay_span(g, s);
+  if (!g.cu || g.N <= 32) return decay_span(g, s);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
-  if (tid == 0) sh[32] = -1;
+  if (tid == 0) sh[48] = -1;
   int before = 0, single = 0;
   for (int n0 = 0; n0 < g.N; n0 += static_cast<int>(blockDim.x)) {
     const int n = n0 + tid;
@@ -127,43 +128,42 @@ __device__ __forceinline__ DecaySpan decay_span_block(const DecayGeom& g, int s,
       if (lane >= off) incl += y;
     }
     const unsigned one = __ballot_sync(0xffffffffu, c == 1 && !g.all);
-    if (lane == 31) {
-      sh[warp] = incl;
-      sh[40 + warp] = __popc(one);
-    }
+    int2* sums = reinterpret_cast<int2*>(sh);
+    if (lane == 31) sums[warp] = make_int2(incl, __popc(one));
     __syncthreads();
     int below = before, all = before, none = single + __popc(one & ((1u << lane) - 1u));
     for (int w = 0; w < nw; ++w) {
+      const int2 x = sums[w];
       if (w < warp) {
-        below += sh[w];
-        none += sh[40 + w];
+        below += x.x;
+        none += x.y;
       }
-      all += sh[w];
-      single += sh[40 + w];
+      all += x.x;
+      single += x.y;
     }
     incl += below;
     if (incl > s && incl - c <= s && c > 0) {  // exactly one thread, if any
-      sh[32] = n;
-      sh[33] = a;
-      sh[34] = b;
-      sh[35] = s - (incl - c);
-      sh[36] = c;
-      sh[37] = s - none;
+      sh[48] = n;
+      sh[49] = a;
+      sh[50] = b;
+      sh[51] = s - (incl - c);
+      sh[52] = c;
+      sh[53] = s - none;
     }
     before = all;
     __syncthreads();
-    if (sh[32] >= 0) break;
+    if (sh[48] >= 0) break;
   }
   DecaySpan r;
-  r.seq = sh[32];
+  r.seq = sh[48];
   r.batch = 0;
   r.row0 = r.len = r.j = r.nseg = r.slot = 0;
   if (r.seq >= 0) {
-    r.j = sh[35];
-    r.nseg = sh[36];
-    r.row0 = sh[33] + r.j * g.S;
-    r.len = min(g.S, sh[34] - r.row0);
-    r.slot = sh[37];
+    r.j = sh[51];
+    r.nseg = sh[52];
+    r.row0 = sh[49] + r.j * g.S;
+    r.len = min(g.S, sh[50] - r.row0);
+    r.slot = sh[53];
     if ((r.nseg > 1 || g.all) && r.slot >= g.slots) r.seq = -1;
   }
   return r;
@@ -181,7 +181,7 @@ struct DecayTcCfg {
   static constexpr int NST = ROOM > 4 ? 4 : ROOM;
   static constexpr int BIG = NST * STAGE + WBF + LO;
   static constexpr int SMEM = BIG + 1024 + 1024;           // + barriers and tables, + alignment
-  static_assert((4 * NST + 18) * 8 + 97 * 4 + 64 * 4 <= 1024, "barriers, tables and decay_span_block's");
+  static_assert((4 * NST + 18) * 8 + 98 * 4 + 64 * 4 <= 1024, "barriers, tables and decay_span_block's");
   static constexpr int THREADS = 608;                      // TMA, MMA, 8 warps P and outputs, 8 warps state, MMA
   static constexpr int NW = DK * DV / 256;                 // elements of X per state thread
   // tensor memory: Sc (P over it; twice where it fits), O1, O2, D
@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(576, 1) decay_tc_total_kernel(const __grid_con
   uint64_t* dfree = dfull + 4;         // [2] product read out
   uint64_t* drain = dfull + 6;
   uint32_t* holder = reinterpret_cast<uint32_t*>(drain + 1);
-  int* sh = reinterpret_cast<int*>(holder + 1);
+  int* sh = reinterpret_cast<int*>(holder + 2);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const DecayGeom& g = A.g;
@@ -569,7 +569,7 @@ __global__ void __launch_bounds__(608, 1) decay_tc_out_kernel(const __grid_const
   float* colp = reinterpret_cast<float*>(bars + 4 * NST + 18);  // [32] gamma^(31-t), reverse gamma^t
   float* diag = colp + 32;                                      // [64] sP gamma^(x-31) at x >= 31
   uint32_t* holder = reinterpret_cast<uint32_t*>(diag + 64);
-  int* sh = reinterpret_cast<int*>(holder + 1);                 // [64]
+  int* sh = reinterpret_cast<int*>(holder + 2);                 // [64]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const DecayGeom& g = A.g;

@@ -146,8 +146,8 @@ struct Moments {
 __device__ __forceinline__ Moments join(const Moments& a, const Moments& b) {
   const float n = a.n + b.n;
   if (n == 0.f) return a;
-  const float f = __fdividef(b.n, n), d = b.mean - a.mean;  // (counts: far from the division's limits)
-  return Moments{n, fmaf(d, f, a.mean), fmaf(f, b.var - a.var, a.var) + d * (f * __fdividef(a.n, n)) * d};
+  const float r = __fdividef(1.f, n), f = b.n * r, d = b.mean - a.mean;  // (counts: far from the division's limits)
+  return Moments{n, fmaf(d, f, a.mean), fmaf(d * (f * (a.n * r)), d, fmaf(f, b.var - a.var, a.var))};
 }
 __device__ __forceinline__ Moments shfl_xor(const Moments& a, int off) {
   return Moments{__shfl_xor_sync(0xffffffffu, a.n, off), __shfl_xor_sync(0xffffffffu, a.mean, off),
@@ -490,8 +490,8 @@ __global__ void __launch_bounds__(256, 3) gn_stats_kernel(const GnParams p) {
             q[e] = fma2(d, d, q[e]);
           }
         }
-      const float h = static_cast<float>(have), inv = __fdividef(1.f, h), f = __fdividef(h, cnt + h);
-      const float cf = f * __fdividef(cnt, cnt + h);
+      const float h = static_cast<float>(have), inv = all ? 1.f / U : __fdividef(1.f, h), r = __fdividef(1.f, cnt + h);
+      const float f = h * r, cf = f * (cnt * r);
 #pragma unroll
       for (int e = 0; e < P; ++e) {
         const f2 d0 = mul2(s[e], both(inv));  // the batch's mean - its first value
