@@ -154,6 +154,12 @@ __device__ __forceinline__ Moments shfl_xor(const Moments& a, int off) {
                  __shfl_xor_sync(0xffffffffu, a.var, off)};
 }
 
+// A variance past the largest number is infinite or, joined on, NaN, and stays
+// so: beside a mean that is a number rstd is 0 then, as of an infinite variance.
+__device__ __forceinline__ float gn_rstd(float mean, float var, float eps) {
+  return isnan(var) && isfinite(mean) ? 0.f : rsqrtf(var + eps);
+}
+
 // Walks rows of C values in memory, `slots` rows at a time, a thread one unit of
 // each: thread slot * units + u has unit u of row `slot`.  What a step reads of
 // the block's units is contiguous (narrow rows are held whole, a wide one
@@ -535,7 +541,7 @@ __global__ void __launch_bounds__(256, 3) gn_stats_kernel(const GnParams p) {
     if (p.splits == 1) {
       const size_t at = static_cast<size_t>(n) * p.G + g;
       p.mean[at] = group[g].mean;
-      p.rstd[at] = rsqrtf(group[g].var + p.eps);
+      p.rstd[at] = gn_rstd(group[g].mean, group[g].var, p.eps);
     } else {
       float2* d = reinterpret_cast<float2*>(p.part) + (static_cast<size_t>(n) * p.splits + part) * p.G + g;
       *d = make_float2(group[g].mean, group[g].var);
@@ -569,7 +575,7 @@ __global__ void __launch_bounds__(256) gn_join_kernel(const GnParams p) {
   for (int off = 16; off > 0; off >>= 1) m = join(m, shfl_xor(m, off));
   if ((threadIdx.x & 31) == 0) {
     p.mean[i] = m.mean;
-    p.rstd[i] = rsqrtf(m.var + p.eps);
+    p.rstd[i] = gn_rstd(m.mean, m.var, p.eps);
   }
 }
 

@@ -292,3 +292,23 @@ def test_values_whose_square_is_too_large(shape, G, dtype):
     hat = (X - _spread(rm, G, shape)) * _spread(rr, G, shape)
     tol = 64 * E * (np.abs(hat) * 4 + _spread(np.abs(rm) * rr, G, shape) + 1) + (U * np.abs(ry) if dtype == "bf16" else 0)
     assert (np.abs(f64(y) - ry) <= tol).all()
+
+
+@pytest.mark.parametrize("shape,G", [((2, 300, 64), 4), ((2, 9, 10), 2), ((5, 1, 96), 2), ((5, 1, 256), 2), ((2, 3000, 320), 32),
+                                     ((1, 70, 8), 1)])
+def test_variance_past_the_largest_number(shape, G):
+    """Values of 2^70 here and there: the variance is past fp32, rstd 0, the
+    group's outputs zeros and not NaN; NaN and infinities stay what they are."""
+    g = torch.Generator().manual_seed(9)
+    x = torch.randn(shape, generator=g)
+    cg = shape[-1] // G
+    x[0, ..., 1] = 2.0 ** 70 * torch.where(torch.arange(x[0, ..., 1].numel()) % 3 == 0, 1.0, -0.25).view(x[0, ..., 1].shape)
+    y, mean, rstd = ttt.group_norm(x.cuda(), G, activation=None)
+    assert rstd[0, 0] == 0 and torch.isfinite(mean).all() and torch.isfinite(rstd).all() and torch.isfinite(y).all()
+    assert (y[0, ..., :cg] == 0).all()
+    for bad in (float("nan"), float("inf")):
+        x[0, ..., 0] = bad
+        y, mean, rstd = ttt.group_norm(x.cuda(), G, activation=None)
+        assert not torch.isfinite(mean[0, 0]) and torch.isnan(y[0, ..., :cg]).all()
+        if G > 1:
+            assert torch.isfinite(y[0, ..., cg:]).all()
