@@ -78,9 +78,9 @@ def on_stream(device, stream):
 
 def launch_on(device, stream, call):
     """call(handle) with the tensors' device and the call's stream current
-    (on_stream without its cost where they already are).  A size that its
-    field of the block cannot hold (2^31 positions and more) is refused as an
-    argument."""
+    (on_stream without its cost where they already are).  A value that
+    its field of the block cannot hold (2^31 positions and more) is refused as
+    an argument."""
     if device.type != "cuda":
         raise ValueError("all tensors must be on one CUDA device")
     try:
@@ -88,8 +88,8 @@ def launch_on(device, stream, call):
             return call(_current_handle(device.index))
         with on_stream(device, stream) as handle:
             return call(handle)
-    except struct.error as e:
-        raise ValueError(f"an argument is too large: {e}") from None
+    except (struct.error, OverflowError) as e:
+        raise ValueError(f"an argument does not fit its field: {e}") from None
 
 
 def check(t, name, dtype, device, shape=None, contiguous=True):

@@ -38,7 +38,7 @@ def check_group_norm(x, num_groups, weight, bias, gate, activation, eps):
     """Refuses what group_norm refuses, without a launch, for callers whose own
     work comes before the norm; x may hold no rows."""
     G = _describe(x, num_groups, weight, bias, gate, activation, empty=True)[3]
-    if not eps >= 0:
+    if not 0 <= eps < 2.0 ** 128:
         raise _abi.TttError("ttt_la_group_norm", _abi.ERR_INVALID_ARG)
     if G > 4096:
         raise _abi.TttError("ttt_la_group_norm", _abi.ERR_UNSUPPORTED)

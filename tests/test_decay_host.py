@@ -306,5 +306,8 @@ def test_sizes_past_their_field_are_refused_as_arguments(monkeypatch):
     for fmt in _call.FORMATS.values():
         n = len(fmt.unpack(bytes(fmt.size)))
         for bad in (1 << 31, -(1 << 31) - 1):
-            with pytest.raises(ValueError, match="too large"):
+            with pytest.raises(ValueError, match="does not fit"):
                 _call.launch_on(torch.device("cuda", 0), None, lambda handle: fmt.pack(bad, *[0] * (n - 1)))
+    with pytest.raises(ValueError, match="does not fit"):
+        _call.launch_on(torch.device("cuda", 0), None,
+                        lambda handle: _call.FORMATS["ttt_la_group_norm_args"].pack(*[1] * 7, 1e40, *[0] * 7))

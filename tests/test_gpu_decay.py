@@ -457,11 +457,11 @@ def test_layer_then_norm_of_no_rows(dtype):
     assert y.shape == (1, 0, 128) and y.dtype == dt and W is S and torch.equal(S, W0)
 
 
-@pytest.mark.parametrize("bad", ["activation", "eps", "eps nan", "weight", "weight dtype", "gate dtype", "gate device"])
+@pytest.mark.parametrize("bad", ["activation", "eps", "eps nan", "eps large", "weight", "weight dtype", "gate dtype", "gate device"])
 def test_layer_then_norm_refuses_before_the_state_moves(bad):
     c = _make([70], 2, 64, 64, "bf16", False, "tokens", True, seed=42)
     gate = torch.zeros(1, 70, 128, dtype=torch.bfloat16, device="cuda")
-    kw = {"activation": dict(activation="relu"), "eps": dict(eps=-1e-5), "eps nan": dict(eps=float("nan")),
+    kw = {"activation": dict(activation="relu"), "eps": dict(eps=-1e-5), "eps nan": dict(eps=float("nan")), "eps large": dict(eps=1e40),
           "weight": dict(weight=torch.ones(64, device="cuda")), "weight dtype": dict(weight=torch.ones(128, device="cuda").half()),
           "gate dtype": dict(gate=gate.float()), "gate device": dict(gate=gate.cpu())}[bad]
     S = c["W0"].clone()
