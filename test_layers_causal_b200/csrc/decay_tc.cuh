@@ -538,9 +538,9 @@ __global__ void __launch_bounds__(576, 1) decay_tc_total_kernel(const __grid_con
 // Shared memory is the bound before HBM: an MMA reads both operands of 128
 // bytes a clock, so a tile of 128 x 128 x 128 moves about 600 KB through it, of
 // which P in tensor memory saves 64; a tile took 5700 cycles with one part of
-// K~ and takes 7100 with two.  Measured: 1 x 8 x 65536 x 128 125 us (537 MB,
-// 4.3 TB/s), 4 x 16 x 4096 x 64 40 us, the gradient's three runs of 2 x 16 x
-// 8192 x 128 192 us.
+// K~ and takes 7100 with two.  Measured, of calls of 192 to 226 us by the card's
+// clock: 1 x 8 x 65536 x 128 125 to 138 us (537 MB, 4.3 TB/s), 4 x 16 x 4096 x 64
+// 40 us, the gradient's three runs of 2 x 16 x 8192 x 128 192 us.
 template <int DK, int DV>
 __global__ void __launch_bounds__(608, 1) decay_tc_out_kernel(const __grid_constant__ DecayTcArgs A) {
   using Cfg = DecayTcCfg<DK, DV>;

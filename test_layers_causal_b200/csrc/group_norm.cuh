@@ -442,8 +442,8 @@ __device__ __forceinline__ void gn_rows(int L, int rows, int k, int& l0, int& l1
 
 // Statistics of one split of one sample: part[N][splits][G] of (mean, variance), or,
 // where a sample is one split, mean and rstd.  Plain loads, a batch of eight
-// positions in flight a thread (6 x 4225 x 320 fp32: 15 us cold; through the
-// ring, whose steps cost a barrier, 18).  Dynamic shared memory: G Moments.
+// positions in flight a thread (6 x 4225 x 320 fp32: 15 us cold, of a call of 30
+// to 34; through the ring, whose steps cost a barrier, 18).  Dynamic shared memory: G Moments.
 template <typename T, int V>
 __global__ void __launch_bounds__(256, 3) gn_stats_kernel(const GnParams p) {
   constexpr int P = Unit<T, V>::P, U = 8;  // U: positions in a batch
