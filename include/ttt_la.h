@@ -385,11 +385,12 @@ TTT_LA_API ttt_la_status ttt_la_backward_chunked(const ttt_la_grad_args *args, v
  * / state_out: fp32 [N,H,d_v,d_k].
  *
  * dtype bf16: d_k and d_v multiples of 8 up to 256; fp32: multiples of 4 up to
- * 256; others TTT_LA_ERR_UNSUPPORTED.  Sums and states are fp32;
- * bf16 up to 128 wide runs on the tensor cores, where the weighted scores and
- * the state as it is read for an output are rounded to bf16 once, from T = 64 on
- * (T: the rows of the call, so the bits of a packed sequence's outputs may
- * depend on what it is packed with, by the kernel and by the split).  A value that
+ * 256; others TTT_LA_ERR_UNSUPPORTED.  Sums and states are fp32, the bf16
+ * result's rounding the only one above 2^-14: bf16 up to 128 wide runs on the
+ * tensor cores (prompts from T = 64 on), where the weighted scores and the state
+ * as it is read for an output are two bf16 parts each.  The kernel and the split
+ * follow the whole call, so the bits of a packed sequence's outputs may depend on
+ * what it is packed with.  A value that
  * is not finite may reach every output of its own tile of 128 tokens, earlier
  * ones included, and all later ones of its (sequence, head), never another
  * sequence or head.

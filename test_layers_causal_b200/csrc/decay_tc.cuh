@@ -5,9 +5,9 @@
 // Per tile of C = 128 tokens, rows r and columns c in memory order, with P and
 // the powers of decay.cuh:
 //   Sc = Q K^T                       M = C,  N = C,  K = DK
-//   O2 = Q Wbf^T                     M = C,  N = DV, K = DK   Wbf = bf16(X)
-//   D  = V^T K~ , K~_c = w_c k_c     M = DV, N = DK, K = C    K~ = bf16 pair hi + lo
-//   O1 = P V , P = bf16(weights * Sc) M = C,  N = DV, K = C
+//   O2 = Q X^T                       M = C,  N = DV, K = DK
+//   D  = V^T K~ , K~_c = w_c k_c     M = DV, N = DK, K = C
+//   O1 = P V , P = weights * Sc      M = C,  N = DV, K = C
 //   o_r = O1 + (read power of r) O2 ,  X <- gamma^n X + D
 // The state X stays in registers in fp32: D is a fresh product every tile, so
 // the decay between tiles is one FMA and the tensor memory is only read.  The
@@ -17,14 +17,15 @@
 // wanted:
 //   decay_tc_total_kernel   every segment's own contribution to the state, by
 //       tiles of 64 or 128 tokens whose products are added in fp32 registers, K~ as
-//       three bf16 parts that carry it to 2^-24: the states that the caller
-//       sees are fp32 sums of unrounded products.
+//       three bf16 parts whose sum it is: the states that the caller sees are
+//       fp32 sums of unrounded products.
 //   decay_scan_kernel       contributions -> start states and final states.
-//   decay_tc_out_kernel     the outputs.  Rounded to bf16 on the way, once
-//       each: P (the weighted scores) and the state where it is read for O2;
-//       with the output's own rounding an output is off by 2.3e-3 of its norm,
-//       where one rounding alone costs 1.7e-3.  K~ takes two parts, since its
-//       error would come on top of the state's (2.7e-3 with one).
+//   decay_tc_out_kernel     the outputs.  P, the state where it is read for O2
+//       and K~ are two bf16 parts each, which carry them to 2^-14, so that an
+//       output is off by its own rounding, 1.66e-3 of its norm.  With one part
+//       of P and of the state it was 2.35e-3, at 196 us for 1 x 8 x 65536 x 128
+//       where two take 210, and 281 us for the gradient of 2 x 16 x 8192 x 128
+//       where two take 303.
 //
 // Weights gamma^(r-c) <= 1 come as products of a row's and a column's power,
 // each with a distance >= 0 to the edge of a 32-column block, so no power
@@ -62,6 +63,16 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+// After tmem_ld_wait: what is made of r stays behind it.
+__device__ __forceinline__ void tmem_ld_done(uint32_t (&r)[16]) {
+  asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                    "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
 }
 // tmem_ld_half32 with 16 columns a thread.
 __device__ __forceinline__ void tmem_ld_half16(uint32_t taddr, uint32_t (&r)[16]) {
@@ -175,13 +186,15 @@ struct DecayTcCfg {
   static constexpr int TK = C * DK * 2, TV = C * DV * 2;   // bytes of a tile
   static constexpr int STAGE = 2 * TK + TV;                // Q, K, V
   static constexpr int WBF = DK * DV * 2;
-  // K~'s second part beside the stages where two stages still fit; else over Q once that has been read
-  static constexpr bool LSEP = 2 * STAGE + WBF + TK <= 232448 - 2048;
-  static constexpr int LO = LSEP ? TK : 0, ROOM = (232448 - 2048 - WBF - LO) / STAGE;
+  // the second parts of K~ and of the state have places of their own where two stages still fit beside them (LSEP);
+  // else K~'s goes over the state's first part, which has been read by then, and the state's over the Q of the tile
+  // before, which then is loaded anew one tile later than K and V
+  static constexpr bool LSEP = 2 * STAGE + 2 * WBF + TK <= 232448 - 2048;
+  static constexpr int LO = LSEP ? TK + WBF : 0, ROOM = (232448 - 2048 - WBF - LO) / STAGE;
   static constexpr int NST = ROOM > 4 ? 4 : ROOM;
   static constexpr int BIG = NST * STAGE + WBF + LO;
   static constexpr int SMEM = BIG + 1024 + 1024;           // + barriers and tables, + alignment
-  static_assert((4 * NST + 18) * 8 + 98 * 4 + 64 * 4 <= 1024, "barriers, tables and decay_span_block's");
+  static_assert((5 * NST + 18) * 8 + 98 * 4 + 64 * 4 <= 1024, "barriers, tables and decay_span_block's");
   static constexpr int THREADS = 608;                      // TMA, MMA, 8 warps P and outputs, 8 warps state, MMA
   static constexpr int NW = DK * DV / 256;                 // elements of X per state thread
   // tensor memory: Sc (P over it; twice where it fits), O1, O2, D
@@ -224,34 +237,70 @@ __device__ __forceinline__ void decay_state_ld(uint32_t t_d, int quad, int half,
     tmem_ld_half16(at, r);
 }
 
+// Takes the leading bf16 of each of two values off x and returns the pair of
+// them.  The upper halves of the words, not the nearest values: a part then is a
+// byte permutation, and what is left is exact with 8 of 24 bits less, so three
+// parts are the value itself.
+__device__ __forceinline__ uint32_t take_bf16x2(f2& x) {
+  const uint32_t a = __float_as_uint(lo_of(x)), b = __float_as_uint(hi_of(x));
+  x = add2(x, pair((a & 0xffff0000u) ^ 0x80000000u, (b & 0xffff0000u) ^ 0x80000000u));
+  return __byte_perm(a, b, 0x7632);
+}
+// x as the sum of two bf16 values, to 2^-14 of it.
+__device__ __forceinline__ void split_bf16x2(f2 x, uint32_t& hi, uint32_t& lo) {
+  hi = take_bf16x2(x);
+  lo = take_bf16x2(x);
+}
 // Splits a K tile (64-column blocks of C rows of 128 bytes) scaled by w[i], the
-// weight of row (t >> 3) + 32 i, for thread t of 256, into PARTS bf16 tiles of
+// weight of row (t >> 3) + 32 i, for thread t of 256, into three bf16 tiles of
 // decreasing size whose sum it is: the first over the tile itself, the others
 // at `rest`, `rest` + one tile.  (A unit's place in its row does not matter
 // here, so the swizzle is left alone.)
-template <int DK, int C, int PARTS>
+template <int DK, int C>
 __device__ __forceinline__ void decay_scale_tile(uint8_t* kt, uint8_t* rest, int t, const float (&w)[C / 32]) {
+#pragma unroll 1
+  for (int b = 0; b < DK / 64; ++b)
 #pragma unroll
-  for (int i = 0; i < C * DK / 2048; ++i) {
-    const int u = i * 256 + t;
+  for (int i = 0; i < C / 32; ++i) {
+    const int u = (b * (C / 32) + i) * 256 + t;
     const uint4 x = *reinterpret_cast<const uint4*>(kt + u * 16);
     const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
-    uint32_t out[PARTS][4];
-    const f2 wt = pair(w[i % (C / 32)], w[i % (C / 32)]);
+    uint32_t out[3][4];
+    const f2 wt = pair(w[i], w[i]);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       f2 y = mul2(pair(xs[e] << 16, xs[e] & 0xffff0000u), wt);
 #pragma unroll
-      for (int r = 0; r < PARTS; ++r) {
-        out[r][e] = pack_bf16x2(y);
-        if (r + 1 < PARTS) y = add2(y, pair((out[r][e] << 16) ^ 0x80000000u, (out[r][e] & 0xffff0000u) ^ 0x80000000u));
-      }
+      for (int r = 0; r < 3; ++r) out[r][e] = take_bf16x2(y);
     }
     *reinterpret_cast<uint4*>(kt + u * 16) = make_uint4(out[0][0], out[0][1], out[0][2], out[0][3]);
 #pragma unroll
-    for (int r = 1; r < PARTS; ++r)
+    for (int r = 1; r < 3; ++r)
       *reinterpret_cast<uint4*>(rest + (r - 1) * (C * DK * 2) + u * 16) = make_uint4(out[r][0], out[r][1], out[r][2], out[r][3]);
   }
+}
+// The same in two parts for the rows [64 y, 64 y + 64) of a tile: the first over
+// the tile, the second into registers, and from there to `rest`.
+template <int DK, int C>
+__device__ __forceinline__ void decay_scale_half(uint8_t* kt, int t, int y, float w0, float w1, uint4 (&lo)[DK / 32]) {
+#pragma unroll
+  for (int i = 0; i < DK / 32; ++i) {
+    uint4* at = reinterpret_cast<uint4*>(kt + (((i >> 1) * (C / 32) + 2 * y + (i & 1)) * 256 + t) * 16);
+    const uint4 x = *at;
+    const f2 wt = i & 1 ? pair(w1, w1) : pair(w0, w0);
+    uint4 hi;
+    split_bf16x2(mul2(pair(x.x << 16, x.x & 0xffff0000u), wt), hi.x, lo[i].x);
+    split_bf16x2(mul2(pair(x.y << 16, x.y & 0xffff0000u), wt), hi.y, lo[i].y);
+    split_bf16x2(mul2(pair(x.z << 16, x.z & 0xffff0000u), wt), hi.z, lo[i].z);
+    split_bf16x2(mul2(pair(x.w << 16, x.w & 0xffff0000u), wt), hi.w, lo[i].w);
+    *at = hi;
+  }
+}
+template <int DK, int C>
+__device__ __forceinline__ void decay_store_half(uint8_t* rest, int t, int y, const uint4 (&lo)[DK / 32]) {
+#pragma unroll
+  for (int i = 0; i < DK / 32; ++i)
+    *reinterpret_cast<uint4*>(rest + (((i >> 1) * (C / 32) + 2 * y + (i & 1)) * 256 + t) * 16) = lo[i];
 }
 // Zeroes the rows >= n of a tile of D features: what is in memory behind a
 // segment's end, whatever it holds, then enters no sum.
@@ -443,7 +492,7 @@ __global__ void __launch_bounds__(576, 1) decay_tc_total_kernel(const __grid_con
       if (i > 1) decay_wait(dead, &lofree[i & 1], ((i >> 1) - 1) & 1, lim);
       __syncwarp();
       uint8_t* parts = rest + (i & 1) * 2 * TK;
-      decay_scale_tile<DK, C, 3>(d, parts, t, wgt);
+      decay_scale_tile<DK, C>(d, parts, t, wgt);
       if (n < C) {
         // (a thread zeroes the units that it scaled itself)
         decay_zero_rows<DK, C>(d, n, t);
@@ -535,12 +584,15 @@ __global__ void __launch_bounds__(576, 1) decay_tc_total_kernel(const __grid_con
 // earlier, the first loads and the scores and P of a whole first tile, overlaps
 // that launch.
 //
-// Shared memory is the bound before HBM: an MMA reads both operands of 128
-// bytes a clock, so a tile of 128 x 128 x 128 moves about 600 KB through it, of
-// which P in tensor memory saves 64; a tile took 5700 cycles with one part of
-// K~ and takes 7100 with two.  Measured, of calls of 192 to 226 us by the card's
-// clock: 1 x 8 x 65536 x 128 125 to 138 us (537 MB, 4.3 TB/s), 4 x 16 x 4096 x 64
-// 40 us, the gradient's three runs of 2 x 16 x 8192 x 128 192 us.
+// A tile's time is the state's chain before HBM: its parts written, O2, the
+// second part of K~ (which takes the place of the state's first), D, the state
+// read and updated: 7400 cycles for 128 x 128 x 128, with about 750 KB through
+// shared memory meanwhile, of which an MMA reads 128 bytes a clock for both
+// operands.  K~ is written and multiplied in two halves of the tokens, and its
+// first half's second part is made before O2 is done (8000 cycles without).
+// 64 wide it is the chain of P and outputs, 4250 cycles.  Measured, of calls of
+// 210 and 72 us: 1 x 8 x 65536 x 128 130 us (537 MB, 4.1 TB/s), 4 x 16 x 4096 x
+// 64 42 us, the gradient's three runs of 2 x 16 x 8192 x 128 200 us.
 template <int DK, int DV>
 __global__ void __launch_bounds__(608, 1) decay_tc_out_kernel(const __grid_constant__ DecayTcArgs A) {
   using Cfg = DecayTcCfg<DK, DV>;
@@ -550,23 +602,24 @@ __global__ void __launch_bounds__(608, 1) decay_tc_out_kernel(const __grid_const
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t sbase = smem_u32(smem);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Cfg::BIG);
-  uint64_t* full = bars;                // [NST] Q and K landed
+  uint64_t* full = bars;                // [NST] K and Q landed
   uint64_t* fullv = bars + NST;         // [NST] V landed
   uint64_t* free_qk = bars + 2 * NST;   // [NST] O2 and D complete: Q and K read for the last time, V by D
   uint64_t* empty = bars + 3 * NST;     // [NST] V's slot free: the output has left
   uint64_t* sfull = bars + 4 * NST;     // [2] scores complete
-  uint64_t* kready = sfull + 2;         // K~ written; D of the tile before read out
-  uint64_t* qdone = sfull + 3;          // O2 complete: Q and Wbf have been read
+  uint64_t* kready = sfull + 15;        // [2] K~ of the tile's first, of its last 64 tokens written; D before read out
+  uint64_t* qdone = sfull + 3;          // O2 complete: Q and the state's parts have been read
   uint64_t* pready = sfull + 13;        // [2] P written over the scores
   uint64_t* dfull = sfull + 5;          // D complete
-  uint64_t* wready = sfull + 6;         // Wbf written
+  uint64_t* wready = sfull + 6;         // the state's parts written
   uint64_t* ofull = sfull + 7;          // O1 complete
   uint64_t* ofree = sfull + 8;          // O1 and O2 read out
   uint64_t* drain = sfull + 9;
   uint64_t* drain2 = sfull + 11;
   uint64_t* cut = sfull + 12;           // rows past the segment's end zeroed in K and V (its last tile, if it has such)
   uint64_t* sread = sfull + 10;         // start state read: the last stage, its buffer, is free
-  float* colp = reinterpret_cast<float*>(bars + 4 * NST + 18);  // [32] gamma^(31-t), reverse gamma^t
+  uint64_t* wfree = sfull + 17;         // [NST] not LSEP: O2 complete that read the state's second part in Q's place there
+  float* colp = reinterpret_cast<float*>(bars + 5 * NST + 18);  // [32] gamma^(31-t), reverse gamma^t
   float* diag = colp + 32;                                      // [64] sP gamma^(x-31) at x >= 31
   uint32_t* holder = reinterpret_cast<uint32_t*>(diag + 64);
   int* sh = reinterpret_cast<int*>(holder + 2);                 // [64]
@@ -590,14 +643,16 @@ __global__ void __launch_bounds__(608, 1) decay_tc_out_kernel(const __grid_const
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < NST; ++i) {
-      mbar_init(&full[i], 1);
+      mbar_init(&full[i], 2);
+      mbar_init(&wfree[i], 1);
       mbar_init(&fullv[i], 1);
       mbar_init(&free_qk[i], 2);
       mbar_init(&empty[i], 1);
     }
     mbar_init(&sfull[0], 1);
     mbar_init(&sfull[1], 1);
-    mbar_init(kready, 8);
+    mbar_init(&kready[0], 8);
+    mbar_init(&kready[1], 8);
     mbar_init(qdone, 1);
     mbar_init(&pready[0], 8);
     mbar_init(&pready[1], 8);
@@ -624,6 +679,8 @@ __global__ void __launch_bounds__(608, 1) decay_tc_out_kernel(const __grid_const
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *holder;
+  // offset of the state's second part for tile i
+  auto second_of = [&](int i) { return Cfg::LSEP ? NST * STAGE + Cfg::WBF : (i + NST - 1) % NST * STAGE; };
   const uint32_t t_o1 = tmem + Cfg::T_O1, t_o2 = tmem + Cfg::T_O2, t_d = tmem + Cfg::T_D;
 
   if (warp == 0) {
@@ -641,13 +698,21 @@ __global__ void __launch_bounds__(608, 1) decay_tc_out_kernel(const __grid_const
           decay_wait(dead, sread, 0, lim);
         }
         if (dead) break;
-        mbar_arrive_expect_tx(&full[st], 2 * TK);
+        mbar_arrive_expect_tx(&full[st], TK);
 #pragma unroll
-        for (int x = 0; x < DK / 64; ++x) {
-          tma_load_4d(&A.map[p.q], &full[st], d + x * C * 128, x * 64, y, h, sp.batch, pol);
+        for (int x = 0; x < DK / 64; ++x)
           tma_load_4d(&A.map[p.k], &full[st], d + TK + x * C * 128, x * 64, y, h, sp.batch, pol);
-        }
         sent = i + 1;
+        // (the state's second part for tile j lies in stage (j - 1) % NST: j = i - NST + 1, the last one's uses first)
+        if (!Cfg::LSEP && i >= NST - 1) decay_wait(dead, &wfree[st], (st == NST - 1 ? i / NST : i / NST - 1) & 1, lim);
+        if (dead) {
+          mbar_arrive(&full[st]);  // complete when K has landed
+          break;
+        }
+        mbar_arrive_expect_tx(&full[st], TK);
+#pragma unroll
+        for (int x = 0; x < DK / 64; ++x)
+          tma_load_4d(&A.map[p.q], &full[st], d + x * C * 128, x * 64, y, h, sp.batch, pol);
         if (i >= NST) decay_wait(dead, &empty[st], (i / NST - 1) & 1, lim);
         if (dead) break;
         mbar_arrive_expect_tx(&fullv[st], TV);
@@ -687,7 +752,7 @@ __global__ void __launch_bounds__(608, 1) decay_tc_out_kernel(const __grid_const
         const uint32_t base = sbase + (i % NST) * STAGE, par = i & 1;
         const uint64_t dq = sdesc_sw128(base, 16, 1024), dvm = sdesc_sw128(base + 2 * TK, C * 128, 1024);
         const int j = i + 1;
-        // Wbf of tile i: the state warps are done with tile i - 1, its scores' barrier among that
+        // the state at tile i: its warps are done with tile i - 1, its scores' barrier among that
         decay_wait(dead, wready, par, lim);
         bool ahead = false;
         if (NSB == 2) {  // (the other score columns were last P of tile i - 1, read by the O1 before)
@@ -701,7 +766,14 @@ __global__ void __launch_bounds__(608, 1) decay_tc_out_kernel(const __grid_const
           for (int kk = 0; kk < DK / 16; ++kk)
             mma_bf16_ss(t_o2, dq + k_step(C, kk), d_w + k_step(DV, kk), ID_Q, kk > 0);
         }
+        if (!dead) {
+          const uint64_t d_wl = sdesc_sw128(sbase + second_of(i), 16, 1024);
+#pragma unroll
+          for (int kk = 0; kk < DK / 16; ++kk)
+            mma_bf16_ss(t_o2, dq + k_step(C, kk), d_wl + k_step(DV, kk), ID_Q, 1);
+        }
         tc_commit(qdone);
+        if (!Cfg::LSEP) tc_commit(&wfree[(i + NST - 1) % NST]);
         tc_commit(&free_qk[i % NST]);
         decay_wait(dead, &fullv[i % NST], (i / NST) & 1, lim);
         decay_wait(dead, &pready[par], (i >> 1) & 1, lim);
@@ -710,7 +782,10 @@ __global__ void __launch_bounds__(608, 1) decay_tc_out_kernel(const __grid_const
         if (!dead) {
 #pragma unroll
           for (int kk = 0; kk < C / 16; ++kk)
-            mma_bf16_ts(t_o1, t_p + (kk >> 2) * 64 + (kk & 3) * 8, dvm + mn_step(kk), ID_P, kk > 0);
+            mma_bf16_ts(t_o1, t_p + 16 * kk + 8, dvm + mn_step(kk), ID_P, kk > 0);
+#pragma unroll
+          for (int kk = 0; kk < C / 16; ++kk)
+            mma_bf16_ts(t_o1, t_p + 16 * kk, dvm + mn_step(kk), ID_P, 1);
         }
         tc_commit(ofull);
         if (j < nt && !ahead) {
@@ -730,15 +805,20 @@ __global__ void __launch_bounds__(608, 1) decay_tc_out_kernel(const __grid_const
         if (i + 1 < nt) {
           const uint32_t base = sbase + (i % NST) * STAGE;
           const uint64_t dkm = sdesc_sw128(base + TK, C * 128, 1024), dvm = sdesc_sw128(base + 2 * TK, C * 128, 1024);
-          const uint64_t dlm = sdesc_sw128(Cfg::LSEP ? sbase + NST * STAGE + Cfg::WBF : base, C * 128, 1024);
+          const uint64_t dlm = sdesc_sw128(sbase + NST * STAGE + (Cfg::LSEP ? 2 * Cfg::WBF : 0), C * 128, 1024);
           decay_wait(dead, &fullv[i % NST], (i / NST) & 1, lim);
-          decay_wait(dead, kready, i & 1, lim);
-          tc_fence_after();
-          if (!dead) {
 #pragma unroll
-            for (int kk = 0; kk < C / 16; ++kk) mma_bf16_ss(t_d, dvm + mn_step(kk), dlm + mn_step(kk), ID_D, kk > 0);
+          for (int y = 0; y < 2; ++y) {
+            decay_wait(dead, &kready[y], i & 1, lim);
+            tc_fence_after();
+            if (!dead) {
 #pragma unroll
-            for (int kk = 0; kk < C / 16; ++kk) mma_bf16_ss(t_d, dvm + mn_step(kk), dkm + mn_step(kk), ID_D, 1);
+              for (int kk = y * C / 32; kk < (y + 1) * C / 32; ++kk)
+                mma_bf16_ss(t_d, dvm + mn_step(kk), dlm + mn_step(kk), ID_D, kk > 0);
+#pragma unroll
+              for (int kk = y * C / 32; kk < (y + 1) * C / 32; ++kk)
+                mma_bf16_ss(t_d, dvm + mn_step(kk), dkm + mn_step(kk), ID_D, 1);
+            }
           }
           tc_commit(dfull);
         }
@@ -769,37 +849,39 @@ __global__ void __launch_bounds__(608, 1) decay_tc_out_kernel(const __grid_const
       __syncwarp();
       tc_fence_after();
       const uint32_t ts = tmem + lanes + (i % NSB) * C + 64 * half;
-#pragma unroll
-      for (int b2 = 0; b2 < 2; ++b2) {
-        uint32_t x[32];
+      // P's two parts of 16 scores, 8 columns each, go over those scores; the next 16 are read meanwhile.  One loop
+      // body for all four: what these warps do for a tile is bound by fetching it, not by its arithmetic (4 x 16 x
+      // 4096 x 64: 75 us a call, 78 with two bodies, 91 with four).
+      uint32_t x[16], next[16];
+      if (dist[0] >= 0) tmem_ld16(ts, next);
+#pragma unroll 1
+      for (int c = 0; c < 64; c += 16) {
+        const int d = c < 32 ? dist[0] : dist[1], t0 = c & 31;
         uint32_t pk[16];
-        if (dist[b2] >= 0) tmem_ld32(ts + 32 * b2, x);
-        if (dist[b2] < 0) {
+        tmem_ld_wait();
+        tmem_ld_done(next);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) pk[e] = 0u;
-        } else if (dist[b2] == 0) {
-          tmem_ld_wait();
-          if (rev) {
-            const float* w = diag + 31 - lane;
+        for (int y = 0; y < 16; ++y) x[y] = next[y];
+        if (c < 48 && (c < 16 ? dist[0] : dist[1]) >= 0) tmem_ld16(ts + c + 16, next);
+        if (d > 0) {
+          const f2 rp = c < 32 ? pair(edge[0], edge[0]) : pair(edge[1], edge[1]);
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) pk[e / 2] = pack_bf16x2(mul2(pair(w[e], w[e + 1]), pair(x[e], x[e + 1])));
-          } else {
-            const float* w = diag + 31 + lane;
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) pk[e / 2] = pack_bf16x2(mul2(pair(w[-e], w[-e - 1]), pair(x[e], x[e + 1])));
+          for (int y = 0; y < 16; y += 4) {
+            const float4 cp = *reinterpret_cast<const float4*>(colp + t0 + y);
+            split_bf16x2(mul2(mul2(rp, pair(cp.x, cp.y)), pair(x[y], x[y + 1])), pk[y / 2], pk[8 + y / 2]);
+            split_bf16x2(mul2(mul2(rp, pair(cp.z, cp.w)), pair(x[y + 2], x[y + 3])), pk[y / 2 + 1], pk[8 + y / 2 + 1]);
           }
+        } else if (d == 0) {
+          const float* at = rev ? diag + 31 - lane + t0 : diag + 31 + lane - t0;
+          const int step = rev ? 1 : -1;
+#pragma unroll
+          for (int y = 0; y < 16; y += 2)
+            split_bf16x2(mul2(pair(at[y * step], at[(y + 1) * step]), pair(x[y], x[y + 1])), pk[y / 2], pk[8 + y / 2]);
         } else {
-          const f2 rp = pair(edge[b2], edge[b2]);
-          tmem_ld_wait();
 #pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            const float4 cp = *reinterpret_cast<const float4*>(colp + e);
-            pk[e / 2] = pack_bf16x2(mul2(mul2(rp, pair(cp.x, cp.y)), pair(x[e], x[e + 1])));
-            pk[e / 2 + 1] = pack_bf16x2(mul2(mul2(rp, pair(cp.z, cp.w)), pair(x[e + 2], x[e + 3])));
-          }
+          for (int y = 0; y < 16; ++y) pk[y] = 0u;
         }
-        // over this warp's own score columns: those of the block before have been read
-        tmem_st16(ts + 16 * b2, pk);
+        tmem_st16(ts + c, pk);
       }
       tmem_st_wait();
       warp_arrive(&pready[i & 1], lane);
@@ -816,7 +898,7 @@ __global__ void __launch_bounds__(608, 1) decay_tc_out_kernel(const __grid_const
       decay_wait(dead, &free_qk[i % NST], (i / NST) & 1, lim);
       __syncwarp();
       tc_fence_after();
-#pragma unroll
+#pragma unroll(DV == 64 ? 2 : 1)
       for (int x = 0; x < DV / 2; x += 16) {
         const int c0 = half * (DV / 2) + x;
         uint32_t a[16], q[16], pk[8];
@@ -857,19 +939,11 @@ __global__ void __launch_bounds__(608, 1) decay_tc_out_kernel(const __grid_const
       }
     };
     if (sp.len - tile_at(0) < C) wait_before();
-    if (NSB == 2) {
-      scores_to_p(0);
-      wait_before();
-      for (int i = 0; i < nt; ++i) {
-        if (i + 1 < nt) scores_to_p(i + 1);
-        output(i);
-      }
-    } else {
-      for (int i = 0; i < nt; ++i) {
-        scores_to_p(i);
-        if (i == 0) wait_before();
-        output(i);
-      }
+#pragma unroll 1
+    for (int i = 0; i < nt + NSB - 1; ++i) {
+      if (i < nt) scores_to_p(i);
+      if (i == 0) wait_before();
+      if (i >= NSB - 1) output(i - (NSB - 1));
     }
     if (threadIdx.x == 2 * 32) bulk_wait0();
   } else {
@@ -894,18 +968,24 @@ __global__ void __launch_bounds__(608, 1) decay_tc_out_kernel(const __grid_const
       }
       fence_async_smem();
       warp_arrive(sread, lane);
+      // the state's second part goes over the buffer
+      if (!Cfg::LSEP && src) asm volatile("bar.sync 2, 256;" ::: "memory");
     }
     const uint32_t wtile = sbase + NST * STAGE;
-    auto put_w = [&]() {
+    // the state's two bf16 parts as O2 reads them
+    auto put_w = [&](uint32_t second) {
 #pragma unroll
-      for (int e = 0; e < NW; e += 8)
-        st_shared_v4(wtile + ((col + e) >> 6) * (DV * 128) + sw128_off(row, ((col + e) & 63) >> 3),
-                     pack_bf16x2(w[e], w[e + 1]), pack_bf16x2(w[e + 2], w[e + 3]), pack_bf16x2(w[e + 4], w[e + 5]),
-                     pack_bf16x2(w[e + 6], w[e + 7]));
+      for (int e = 0; e < NW; e += 8) {
+        const uint32_t at = ((col + e) >> 6) * (DV * 128) + sw128_off(row, ((col + e) & 63) >> 3);
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) split_bf16x2(pair(w[e + 2 * y], w[e + 2 * y + 1]), hi[y], lo[y]);
+        st_shared_v4(wtile + at, hi[0], hi[1], hi[2], hi[3]);
+        st_shared_v4(second + at, lo[0], lo[1], lo[2], lo[3]);
+      }
       fence_async_smem();
       warp_arrive(wready, lane);
     };
-    put_w();
     float wgt[4];
     auto weights = [&](int n) {
 #pragma unroll
@@ -919,6 +999,7 @@ __global__ void __launch_bounds__(608, 1) decay_tc_out_kernel(const __grid_const
     for (int i = 0; i < nt; ++i) {
       const int st = i % NST, n = min(C, sp.len - tile_at(i));
       const bool more = i + 1 < nt;
+      put_w(sbase + second_of(i));
       decay_wait(dead, &full[st], (i / NST) & 1, lim);
       uint8_t* d = smem + st * STAGE;
       if (n < C) {
@@ -938,17 +1019,22 @@ __global__ void __launch_bounds__(608, 1) decay_tc_out_kernel(const __grid_const
         weights(n);
         gn = expf(l * static_cast<float>(n));
       }
-      if (more) {
-        if (!Cfg::LSEP) {
-          decay_wait(dead, qdone, i & 1, lim);  // Q, whose place K~'s second part takes, has been read
+      if (!more) break;
+      // 64 tokens at a time, so that D starts on the first of them; without a place of its own K~'s second part of
+      // those waits in registers for the state's first part to have been read
+#pragma unroll(Cfg::LSEP ? 1 : 2)
+      for (int y = 0; y < 2; ++y) {
+        uint4 lo[DK / 32];
+        decay_scale_half<DK, C>(d + TK, t, y, y ? wgt[2] : wgt[0], y ? wgt[3] : wgt[1], lo);
+        if (!Cfg::LSEP && y == 0) {
+          decay_wait(dead, qdone, i & 1, lim);
           __syncwarp();
         }
-        decay_scale_tile<DK, C, 2>(d + TK, Cfg::LSEP ? smem + NST * STAGE + Cfg::WBF : d, t, wgt);
+        decay_store_half<DK, C>(smem + NST * STAGE + (Cfg::LSEP ? 2 * Cfg::WBF : 0), t, y, lo);
+        fence_async_smem();
+        warp_arrive(&kready[y], lane);
       }
       if (n < C) weights(C);
-      fence_async_smem();
-      warp_arrive(kready, lane);
-      if (!more) break;
       decay_wait(dead, dfull, i & 1, lim);
       __syncwarp();
       tc_fence_after();
@@ -962,10 +1048,9 @@ __global__ void __launch_bounds__(608, 1) decay_tc_out_kernel(const __grid_const
         for (int e = 0; e < PIECE; ++e) w[x + e] = fmaf(gn, w[x + e], __uint_as_float(y[e]));
       }
       if (Cfg::LSEP) {
-        decay_wait(dead, qdone, i & 1, lim);  // Wbf has been read
+        decay_wait(dead, qdone, i & 1, lim);  // the state's parts have been read
         __syncwarp();
       }
-      put_w();
     }
     tc_fence_before();
   }

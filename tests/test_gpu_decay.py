@@ -186,6 +186,34 @@ def test_backward_matches_oracle(case):
     _check_backward(c, g, dtype, np.float64(np.float32(0.2)))
 
 
+@pytest.mark.parametrize("lens,H,dk,dv,packed,seg", [
+    ([300, 300], 3, 128, 128, False, 128), ([700], 2, 128, 128, False, 0), ([513], 2, 64, 64, False, 128),
+    ([390], 2, 128, 64, False, 192), ([450], 2, 64, 128, False, 0), ([200], 2, 96, 80, False, 64),
+    ([130, 0, 1, 65, 511, 127], 3, 128, 128, True, 128), ([3, 400, 0, 77], 2, 64, 64, True, 0)])
+def test_outputs_take_one_rounding(lens, H, dk, dv, packed, seg):
+    """bf16 on the tensor cores: an output's own rounding, u |x|, and beside it
+    what two bf16 parts leave out.  A part is the upper half of a word, with 8
+    bits, so two leave less than 2^-14: of a weighted score, or of the keys in
+    the state and of the state as it is read, 2^-13 in all; sums are added in 22
+    bits at least, (T / 16 + 16) terms deep, weights off by fewer steps than
+    that.  |err| <= u |x| + (2^-13 + 2^-21 (T / 16 + 16)) A."""
+    c = _make(lens, H, dk, dv, "bf16", packed, "tokens", True, seed=61 + dk)
+    kw = dict(cu_seqlens=c["cu"], state_in=c["W0"], segment_tokens=seg, eta_const=0.25)
+    o, _ = ttt.forward_decay(c["q"], c["k"], c["v"], c["ld"], **kw)
+    g = ttt.backward_decay(c["q"], c["k"], c["v"], c["dO"], c["ld"], grad_state=c["dW"], **kw)
+    ld = f64(c["ld"])
+    for n, T in enumerate(lens):
+        q, k, v, dO = (f64(_of_seq(c[x], c, n)) for x in ("q", "k", "v", "dO"))
+        W0, dW = f64(c["W0"][n]), f64(c["dW"][n])
+        ref = dict(oracle.decay_backward_f64(q, k, v, dO, ld, 0.25, W0, dW), o=oracle.decay_forward_f64(q, k, v, ld, 0.25, W0)[0])
+        A = dict(oracle.decay_backward_f64(*_abs(q, k, v, dO), ld, 0.25, *_abs(W0, dW)),
+                 o=oracle.decay_forward_f64(*_abs(q, k, v), ld, 0.25, np.abs(W0))[0])
+        for name, x in (("o", o), ("dq", g["dq"]), ("dk", g["dk"]), ("dv", g["dv"])):
+            x = f64(_of_seq(x, c, n))
+            tol = U * np.abs(ref[name]) + (2.0 ** -13 + 2.0 ** -21 * (T / 16 + 16)) * A[name]
+            assert (np.abs(x - ref[name]) <= tol + 1e-30).all(), (name, n)
+
+
 def test_gradient_agrees_with_differences():
     """<gradient, direction> against the fp32 layer's own central difference;
     the loss is a sum over o and W_T, linear in each input alone, so the
