@@ -114,18 +114,18 @@ ttt_la_status decay_simt_runs(const ttt::DecayGeom& g, const ttt::DecayRun* r, i
 }
 
 // ------------------------------------------------- tensor-core kernels ----
-// From 64 tokens on, the length of half a tile. Below it the fp32 kernel rounds
-// nothing but the result (with a token or two the one rounding of a score is a
-// whole row's): relative error 1.7e-3 against 2.4e-3 here. The price, two
-// sequences x 24 heads x 128: forward 23 us either way, at 31 tokens there and 32
-// here; gradient 67 us there, 30 us here; with one head 45 and 30 us.
-// T counts all rows of the call, those of packed sequences together, so that many
-// short ones come here, where a block costs less than the fp32 kernel's four even
-// for one token (64 sequences x 16 heads x 128 of 1, 15, 46 tokens: forward 114,
-// 143, 151 us here and 184, 250, 417 there, gradient 211, 280, 293 and 493, 682,
-// 1181; the exception is 64 wide up to eight tokens: 89 and 64 us at one). Their
-// outputs are rounded as long ones' are.
-bool decay_on_tc(int dtype, int T, int dk, int dv) { return dtype == TTT_LA_BF16 && T >= 64 && dk <= 128 && dv <= 128; }
+// Prompts from 64 rows on, and every gradient.  T counts all rows of the call,
+// those of packed sequences together.  Measured, us here and in fp32 FMA, whose
+// outputs are as exact: gradients of 1 to 63 tokens 28 to 29 and 30 to 93 for up
+// to 48 (sequence, head)s, 124 to 134 and 269 to 606 for 32 x 16 x 128, 167 to 175
+// and 177 to 388 for 64 x 16 x 64.  Prompts of one token 22 and 19 for few, 96 and
+// 70 for 64 x 16 x 64, 86 and 111 for 32 x 16 x 128; of 63 tokens 23 and 19 to 35,
+// 97 and 138, 91 and 258.  Of many short packed ones, which come here, 64 x 16
+// heads x 128 of 1, 15, 46 tokens: prompts 114, 143, 151 and 184, 250, 417,
+// gradients 211, 280, 293 and 493, 682, 1181.
+bool decay_on_tc(int dtype, int T, int dk, int dv, bool gradient) {
+  return dtype == TTT_LA_BF16 && T >= (gradient ? 1 : 64) && dk <= 128 && dv <= 128;
+}
 
 // Tokens per segment of the tensor-core kernels, whose blocks have an SM each.
 // `heads` sequences of `rows` tokens, `runs` outputs of each.  In units of one
@@ -267,14 +267,14 @@ ttt::DecayRun decay_forward_run(const ttt_la_decay_args* a) {
 // The final states overwrite the start states, which the outputs are read
 // from: those go through the workspace.
 bool decay_in_place(const ttt_la_decay_args* a) {
-  return a->state_in && a->state_in == a->state_out && decay_on_tc(a->dtype, a->T, a->d_k, a->d_v);
+  return a->state_in && a->state_in == a->state_out && decay_on_tc(a->dtype, a->T, a->d_k, a->d_v, false);
 }
 
 int decay_segment_tokens(int asked, const int32_t* cu, int N, int H, int T, int dk, int dv, int dtype, int runs) {
   if (asked > 0) return asked;
   const int rows = std::max(1, T);
   const long long seqs = cu ? 1 : N;
-  if (decay_on_tc(dtype, T, dk, dv)) return decay_tc_plan_tokens(seqs * H, rows, runs, cu != nullptr, sm_count());
+  if (decay_on_tc(dtype, T, dk, dv, runs > 1)) return decay_tc_plan_tokens(seqs * H, rows, runs, cu != nullptr, sm_count());
   const int widest = runs > 1 ? std::max(dk, dv) : dv;
   return decay_plan_tokens(seqs * H * ((widest + ttt::kDecayVT - 1) / ttt::kDecayVT), rows, sm_count() * 2);
 }
@@ -290,7 +290,7 @@ DecayLayout decay_backward_layout(const ttt_la_decay_grad_args* a, size_t* float
   const int tokens = decay_segment_tokens(a->segment_tokens, a->cu_seqlens, a->N, a->H, a->T, a->d_k, a->d_v, a->dtype,
                                           3);
   const DecayLayout l = decay_layout(a->cu_seqlens, a->N, a->H, a->T, a->d_k, a->d_v, tokens, false);
-  *floats = (decay_on_tc(a->dtype, a->T, a->d_k, a->d_v) ? 2 : 3) * l.run_floats;
+  *floats = (decay_on_tc(a->dtype, a->T, a->d_k, a->d_v, true) ? 2 : 3) * l.run_floats;
   return l;
 }
 
@@ -327,7 +327,7 @@ ttt_la_status ttt_la_forward_decay(const ttt_la_decay_args* a, void* stream) {
   ttt::DecayRun r = decay_forward_run(a);
   r.ws = need ? static_cast<float*>(a->workspace) : nullptr;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (!decay_on_tc(a->dtype, a->T, a->d_k, a->d_v))
+  if (!decay_on_tc(a->dtype, a->T, a->d_k, a->d_v, false))
     return decay_simt_runs(l.g, &r, 1, a->dtype, a->log_decay, st);
   ttt::DecayTcArgs m = {};
   const int batch = packed ? 1 : a->N;
@@ -410,7 +410,7 @@ ttt_la_status ttt_la_backward_decay(const ttt_la_decay_grad_args* a, void* strea
     r[2].ws = r[0].ws + l.run_floats;
   }
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (!decay_on_tc(a->dtype, a->T, a->d_k, a->d_v)) {
+  if (!decay_on_tc(a->dtype, a->T, a->d_k, a->d_v, true)) {
     if (need) r[1].ws = r[2].ws + l.run_floats;
     return decay_simt_runs(l.g, r, 3, a->dtype, a->log_decay, st);
   }
