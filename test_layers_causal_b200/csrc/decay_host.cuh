@@ -121,8 +121,8 @@ ttt_la_status decay_simt_runs(const ttt::DecayGeom& g, const ttt::DecayRun* r, i
 // and 177 to 388 for 64 x 16 x 64.  Prompts of one token 22 and 19 for few, 96 and
 // 70 for 64 x 16 x 64, 86 and 111 for 32 x 16 x 128; of 63 tokens 23 and 19 to 35,
 // 97 and 138, 91 and 258.  Of many short packed ones, which come here, 64 x 16
-// heads x 128 of 1, 15, 46 tokens: prompts 114, 143, 151 and 184, 250, 417,
-// gradients 211, 280, 293 and 493, 682, 1181.
+// heads x 128 of 1, 15, 46 tokens: prompts 126, 154, 160 and 184, 250, 417,
+// gradients 241, 316, 320 and 493, 682, 1181.
 bool decay_on_tc(int dtype, int T, int dk, int dv, bool gradient) {
   return dtype == TTT_LA_BF16 && T >= (gradient ? 1 : 64) && dk <= 128 && dv <= 128;
 }
@@ -154,10 +154,10 @@ int decay_tc_plan_tokens(long long heads, int rows, int runs, bool packed, int s
   // Packed sequences end where they end, and what fills the SMs evenly as one long one leaves them waiting for the
   // longest: at least 1.3 blocks for each SM, but no segment below 512 tokens for that.  The host does not see the
   // lengths, and the rule pays where they differ: us with the even split, then with the rule, of 10 sequences of 1 to
-  // 3999 tokens, gradient of 4 heads x 128 93 and 86, of 12 x 64 151 and 133; 30 of 1 to 2000, prompt of 4 x 128 111
-  // and 99; no difference for 16 heads x 128 of either, 200 of 1 to 120, 64 of 256.  It costs where a few are equally
-  // long or one is nearly all: 2 of 6000, prompt of 16 x 128 93 and 116, gradient of 4 x 128 72 and 86; 12000 tokens
-  // and 20 of 20, gradient of 4 x 128 86 and 94.
+  // 3999 tokens, gradient of 4 heads x 128 106 and 97, of 12 x 64 152 and 136; 30 of 1 to 2000, prompt of 4 x 128 119
+  // and 107; no difference for 16 heads x 128 of either, 200 of 1 to 120, 64 of 256.  It costs where a few are equally
+  // long or one is nearly all: 2 of 6000, prompt of 16 x 128 98 and 123, gradient of 4 x 128 86 and 98; 12000 tokens
+  // and 20 of 20, gradient of 4 x 128 95 and 104.
   if (packed) {
     const long long even = static_cast<long long>(rows) * heads * runs * 10 / (13ll * slots) / ttt::kDecayTcC;
     best = static_cast<int>(std::min<long long>(best, std::max<long long>(even, 512 / ttt::kDecayTcC)));

@@ -24,8 +24,8 @@
 //       and K~ are two bf16 parts each, which carry them to 2^-14, so that an
 //       output is off by its own rounding, 1.66e-3 of its norm.  With one part
 //       of P and of the state it was 2.35e-3, at 196 us for 1 x 8 x 65536 x 128
-//       where two take 210, and 281 us for the gradient of 2 x 16 x 8192 x 128
-//       where two take 303.
+//       where two take 210 (227 and 254 at the power cap's clock), and 281 us
+//       for the gradient of 2 x 16 x 8192 x 128 where two take 303 (313, 356).
 //
 // Weights gamma^(r-c) <= 1 come as products of a row's and a column's power,
 // each with a distance >= 0 to the edge of a 32-column block, so no power
