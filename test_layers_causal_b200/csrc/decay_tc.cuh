@@ -569,7 +569,8 @@ __global__ void __launch_bounds__(576, 1) decay_tc_total_kernel(const __grid_con
 // Where tensor memory has room for one set of score columns, Sc of tile i + 1
 // follows O1 of tile i; where it has two, it comes before O1 and the warps
 // write P of tile i + 1 before they read the output of tile i.  Q and K are
-// free once O2 and D are done, V once the output, staged over it, is stored.
+// free once O2 and D are done (Q, where it then holds a part of the state, once
+// the next tile's O2 is), V once the output, staged over it, is stored.
 //
 // A barrier's next phase must not complete before each waiter has seen this
 // one (two phases look like none).  Each single barrier below has that from the
@@ -765,8 +766,6 @@ __global__ void __launch_bounds__(608, 1) decay_tc_out_kernel(const __grid_const
 #pragma unroll
           for (int kk = 0; kk < DK / 16; ++kk)
             mma_bf16_ss(t_o2, dq + k_step(C, kk), d_w + k_step(DV, kk), ID_Q, kk > 0);
-        }
-        if (!dead) {
           const uint64_t d_wl = sdesc_sw128(sbase + second_of(i), 16, 1024);
 #pragma unroll
           for (int kk = 0; kk < DK / 16; ++kk)
